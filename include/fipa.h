@@ -343,6 +343,133 @@ fipa_status fipa_ipa_layer(fipa_handle* h, const float* s, const float* W_in, co
                            float* out_s, float* out_rot, float* out_trans, float* out_local_points,
                            void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention along the chain with a sliding window and a few first tokens that
+ * stay visible (sinks): the sequence mixer between IPA blocks, O(N) like the
+ * core, for training on whole chains, for sampling, and for single tokens
+ * against a cache of keys and values.
+ *
+ * Query i of sample b stands at position p = q_start[b] + i (q_start NULL: the
+ * queries are the last Nq positions, p = Nk - Nq + i).  It sees key j iff
+ *   0 <= j < Nk,  j <= p + right,  (j >= p - left or j < sinks),  mask[b,j];
+ * a query whose p is outside [0, Nk) or has mask[b,p] = 0 sees nothing.
+ *   S_ij = scale q_i.k_j,  P = softmax over the visible j,  out_i = sum_j P_ij v_j
+ * A query that sees nothing gets a zero row, lse -inf, and passes no gradient.
+ * Query head h reads key head h / (H / Hkv).  Values at masked positions (in q,
+ * k, v, out, d_out) are never used, whatever they hold; elsewhere every value
+ * is finite.
+ *
+ * Tensors: out, d_out and the gradients have the handle's dtype (they feed the
+ * next product in that type; every sum and the softmax are float32, rounded
+ * once), lse is float32. */
+typedef struct {
+  int B, Nq, Nk;      /* batch, queries and keys of a sample                            */
+  int H, Hkv;         /* query and key heads; H a multiple of Hkv                       */
+  int D, Dv;          /* query / key and value channels, 1..128 each                    */
+  int left, right;    /* window before and after the query's own position; < 0: no bound */
+  int sinks;          /* first tokens that stay visible, 0..128                         */
+  double scale;       /* finite, > 0                                                    */
+} fipa_window;
+
+/* [B, N, heads, width] with strides in elements (>= 0), the width contiguous:
+ * a slice of a fused projection is passed as it is. */
+typedef struct {
+  const void* ptr;
+  int64_t stride_b, stride_n, stride_h;
+} fipa_heads;
+
+/*   q [B,Nq,H,D], k [B,Nk,Hkv,D], v [B,Nk,Hkv,Dv]
+ *   mask     [B,Nk] uint8 or NULL (all valid)
+ *   q_start  [B] int32 or NULL
+ *   out      [B,Nq,H,Dv] contiguous, every row written
+ *   lse      [B,H,Nq] or NULL: natural-log logsumexp of the visible scores
+ * FIPA_ERR_UNSUPPORTED for D or Dv > 128 or sinks > 128.  Allocates nothing;
+ * runs on `stream`. */
+fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
+                                  const fipa_heads* v, const uint8_t* mask, const int32_t* q_start,
+                                  const fipa_window* win, void* out, float* lse, void* stream);
+
+/* Gradients of <d_out, out>: d_q [B,Nq,H,D], d_k [B,Nk,Hkv,D] (summed over the
+ * heads of a group), d_v [B,Nk,Hkv,Dv], contiguous, every element written.
+ * out and lse are those of the forward call; workspace >=
+ * fipa_window_attention_backward_workspace_size() bytes, 256-byte aligned.
+ * Deterministic: every sum is taken in a fixed order. */
+fipa_status fipa_window_attention_backward_workspace_size(const fipa_handle* h, const fipa_window* win,
+                                                          size_t* bytes);
+fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
+                                           const fipa_heads* v, const uint8_t* mask,
+                                           const int32_t* q_start, const fipa_window* win,
+                                           const void* out, const float* lse, const void* d_out,
+                                           void* d_q, void* d_k, void* d_v,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* The junction between two blocks of a residual network: the norm after a
+ * block, its gate and residual scale, the residual sum, and the norm before the
+ * next block, in one pass over each tensor:
+ *   y = Norm(u) post_w + post_b        (post_w NULL: y = u)
+ *   r = s + res_scale sigmoid(gate) y  (gate NULL: no gate; res_scale NULL: 1)
+ *   x = Norm(r) pre_w + pre_b          (pre_w NULL: no x; pre_b, post_b NULL: 0)
+ * FIPA_NORM_LAYER: Norm(z) = (z - mean z) / sqrt(var z + eps), the variance over
+ * C; FIPA_NORM_RMS: z / sqrt(mean z^2 + eps).  u NULL (then no gate, res_scale,
+ * post_w): r = s is not written and x = Norm(s) pre_w + pre_b.
+ * A row whose mask is 0 is padding: r = s, x = 0, its u, gate and d_x are never
+ * used, and it passes d_r on to d_s and nothing else.
+ * The stream (s, r, d_r, d_s) and the branch (u, gate, x and their gradients)
+ * have a type each; parameters and their gradients are float32, as is all
+ * arithmetic, rounded once on the way out.  x and the gradients use r before it
+ * is rounded to the stream's type. */
+typedef enum { FIPA_NORM_LAYER = 0, FIPA_NORM_RMS = 1 } fipa_norm_kind;
+typedef struct {
+  int64_t rows;                 /* >= 0                                        */
+  int C;                        /* channels, 1..8192                           */
+  fipa_dtype stream_dtype, branch_dtype;
+  fipa_norm_kind norm;
+  double eps;                   /* > 0                                         */
+} fipa_norm_dims;
+typedef struct {
+  const void *s, *u, *gate;     /* [rows, C]; u, gate optional                 */
+  const uint8_t* mask;          /* [rows] or NULL (all valid)                  */
+  const float *res_scale, *post_w, *post_b, *pre_w, *pre_b;   /* [C], optional */
+} fipa_norm_inputs;
+typedef struct {
+  void *s, *u, *gate;           /* [rows, C]; NULL: not wanted                 */
+  float *res_scale, *post_w, *post_b, *pre_w, *pre_b;         /* [C], likewise */
+} fipa_norm_grads;
+
+/*   r      [rows,C] stream type (NULL iff u is NULL); may be s itself
+ *   x      [rows,C] branch type (NULL iff pre_w is NULL)
+ *   stats  [rows,4] float32, 16-byte aligned, or NULL: mean and 1/deviation of u
+ *          and of r, which the backward needs
+ * No handle: every pointer belongs to the current device.  Allocates nothing. */
+fipa_status fipa_norm_residual(const fipa_norm_dims* dims, const fipa_norm_inputs* in, void* r, void* x,
+                               float* stats, void* stream);
+
+/* Gradients of <d_r, r> + <d_x, x> (d_r or d_x NULL: zero); s, u, gate and the
+ * parameters as given to the forward, stats as it wrote them.  Gradients must
+ * not overlap the inputs.  Deterministic.  workspace >=
+ * fipa_norm_residual_backward_workspace_size() bytes, 256-byte aligned. */
+fipa_status fipa_norm_residual_backward_workspace_size(const fipa_norm_dims* dims, size_t* bytes);
+fipa_status fipa_norm_residual_backward(const fipa_norm_dims* dims, const fipa_norm_inputs* in,
+                                        const float* stats, const void* d_r, const void* d_x,
+                                        const fipa_norm_grads* grads, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Embedding of residue types, tokens or distogram bins with scaling:
+ *   out[t] = scale table[idx[t]]      idx [T] int32, table [V,C], out [T,C] in `dtype`
+ * An index outside [0, V) gives a zero row (the -1 bins of fipa_knn_distogram's
+ * empty slots pass as they are) and no gradient.
+ * Gradient: d_table[v] = scale sum over t with idx[t] = v of d_out[t], float32,
+ * every row written.  Tokens are sorted by index and the sums of a row taken in
+ * a fixed order: the result does not depend on timing, nor its cost on how the
+ * tokens fall.  FIPA_ERR_UNSUPPORTED for T or V > 2^30 or C > 65536.  No handle:
+ * every pointer belongs to the current device.  Allocates nothing; the workspace
+ * of the gradient is 256-byte aligned. */
+fipa_status fipa_embedding(fipa_dtype dtype, const int32_t* idx, const void* table, int64_t T, int V, int C,
+                           double scale, void* out, void* stream);
+fipa_status fipa_embedding_backward_workspace_size(int64_t T, int V, int C, size_t* bytes);
+fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* idx, const void* d_out, int64_t T, int V,
+                                    int C, double scale, float* d_table, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* k-nearest-neighbour distogram features ("Flash Invariant Point Attention",
  * rebuttal answer 6: keep the k nearest neighbours of each residue,
  * (B, L, k, n_bins), instead of the (B, L, L, n_bins) distogram; found

@@ -2,5 +2,6 @@
 
 The compute lives in libfipa.so (C ABI in include/fipa.h); this package is
 its thin Python binding and build step."""
-from .fipa import (Fipa, FipaError, FipaDims, invariant_point_attention, load_library,  # noqa: F401
-                   library_path, make_dims)
+from .fipa import (Fipa, FipaError, FipaDims, embedding, embedding_backward,  # noqa: F401
+                   embedding_backward_workspace_size, invariant_point_attention, load_library,
+                   library_path, make_dims, norm_residual, norm_residual_backward)

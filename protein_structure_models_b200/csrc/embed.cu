@@ -1,0 +1,437 @@
+// embed.cu -- embedding lookup with scaling, and its gradient by sorted tokens
+// (fipa_embedding, fipa_embedding_backward):
+//   out[t] = scale table[idx[t]]                     (idx outside [0, V): a zero row)
+//   dtable[v] = scale sum over t with idx[t] = v of dout[t], in the order of t.
+//
+// Bound by memory: idx, dout and out once, the table's used rows, dtable once.
+// The gradient sorts (index, token) by a stable radix sort on the bits that V
+// needs, cuts the sorted list into chunks of equal length, one group of threads
+// each, and adds rows of dout while the index stays the same.  A run inside one
+// chunk is final; the pieces of a run that crosses chunks are kept in float32
+// and added in chunk order, so no sum depends on the order of atomics and a row
+// with all the tokens costs what many rows cost.
+#include "fipa.h"
+#include "kernels.h"
+
+#define FIPA_API extern "C" __attribute__((visibility("default")))
+
+namespace fipa {
+namespace {
+
+constexpr int kSortThreads = 256;
+constexpr int kSortItems = 8;                              // per thread
+constexpr int kSortBlock = kSortThreads * kSortItems;
+constexpr int kDigits = 256;
+
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& w, float* v);
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4& w, float* v) {
+  v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
+}
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& w, float* v) {
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(ww[e] << 16);
+    v[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float* v);
+template <>
+__device__ __forceinline__ uint4 pack<float>(const float* v) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+template <>
+__device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float cvt(float x) { return x; }
+__device__ __forceinline__ float cvt(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// One piece (16 bytes, or one element) of an output row per thread.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) embed_fwd_kernel(const int* __restrict__ idx, const T* __restrict__ table, T* __restrict__ out,
+                                                        long long rows, int V, int C, int pieces, float scale) {
+  const long long n = rows * pieces, step = (long long)gridDim.x * blockDim.x;
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += step) {
+    const long long t = e / pieces;
+    const int p = (int)(e - t * pieces), v = __ldg(idx + t);
+    const bool on = v >= 0 && v < V;
+    if (VEC) {
+      constexpr int N = Vec<T>::n;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (on) {
+        float x[N];
+        unpack<T>(__ldg(reinterpret_cast<const uint4*>(table + (long long)v * C) + p), x);
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] *= scale;
+        w = pack<T>(x);
+      }
+      reinterpret_cast<uint4*>(out + t * C)[p] = w;
+    } else {
+      put(out + t * C + p, on ? cvt(table[(long long)v * C + p]) * scale : 0.f);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- stable sort
+// Digit counts of every block of 2048 elements: hist[digit][block].
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __restrict__ key, int n, int V, int first, int shift,
+                                                                  int mask, int* __restrict__ hist) {
+  __shared__ int cnt[kDigits];
+  cnt[threadIdx.x] = 0;
+  __syncthreads();
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = blockIdx.x * kSortBlock + k * kSortThreads + threadIdx.x;
+    if (i < n) {
+      int v = key[i];
+      if (first && (v < 0 || v >= V)) v = V;
+      atomicAdd(&cnt[(v >> shift) & mask], 1);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x <= mask) hist[(size_t)threadIdx.x * gridDim.x + blockIdx.x] = cnt[threadIdx.x];
+}
+// Exclusive prefix sums of one digit's block counts, and its total (one CTA per digit).
+__global__ void __launch_bounds__(256) sort_scan_kernel(int* __restrict__ hist, int* __restrict__ total, int nblk) {
+  __shared__ int ws[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int* h = hist + (size_t)blockIdx.x * nblk;
+  int carry = 0;
+  for (int b0 = 0; b0 < nblk; b0 += 256) {
+    const int b = b0 + threadIdx.x, x = b < nblk ? h[b] : 0;
+    int y = x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    if (lane == 31) ws[warp] = y;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += ws[w];
+      all += ws[w];
+    }
+    if (b < nblk) h[b] = carry + before + y - x;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) total[blockIdx.x] = carry;
+}
+// Moves every element to its place.  A warp owns 256 neighbours and takes them
+// 32 at a time: an element's rank among its warp's equal digits is the warp's
+// running count plus the equal lanes below it.
+__global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int* __restrict__ key, const int* __restrict__ tok, int n, int V,
+                                                                 int first, int shift, int mask, const int* __restrict__ hist,
+                                                                 const int* __restrict__ total, int nblk, int* __restrict__ okey,
+                                                                 int* __restrict__ otok) {
+  __shared__ int cnt[8][kDigits];
+  __shared__ int base[kDigits];
+  __shared__ int ws[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int w = 0; w < 8; ++w) cnt[w][threadIdx.x] = 0;
+  // digits below this one, in all
+  const int tot = threadIdx.x <= mask ? total[threadIdx.x] : 0;
+  int y = tot;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) ws[warp] = y;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += ws[w];
+  if (threadIdx.x <= mask) base[threadIdx.x] = before + y - tot + hist[(size_t)threadIdx.x * nblk + blockIdx.x];
+  int v[kSortItems], tk[kSortItems], rank[kSortItems];
+  const int i0 = blockIdx.x * kSortBlock + warp * 256 + lane;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = i0 + k * 32;
+    v[k] = -1;
+    tk[k] = i;
+    if (i < n) {
+      v[k] = key[i];
+      if (first) {
+        if (v[k] < 0 || v[k] >= V) v[k] = V;
+      } else {
+        tk[k] = tok[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const bool on = v[k] >= 0;
+    const int d = on ? (v[k] >> shift) & mask : kDigits;
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int below = __popc(same & ((1u << lane) - 1u));
+    int c = 0;
+    if (on) c = cnt[warp][d];
+    rank[k] = c + below;
+    __syncwarp();
+    if (on && below == 0) cnt[warp][d] = c + __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    if (v[k] < 0) continue;
+    const int d = (v[k] >> shift) & mask;
+    int p = base[d] + rank[k];
+    for (int w = 0; w < warp; ++w) p += cnt[w][d];
+    okey[p] = v[k];
+    otok[p] = tk[k];
+  }
+}
+
+// ---------------------------------------------------------------- run sums
+// A group of `tpc` threads adds one chunk of the sorted list for a slab of
+// columns.  part[chunk][0]: the run that came from the chunk before; [1]: the
+// run that starts here and goes on.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) embed_sum_kernel(const int* __restrict__ key, const int* __restrict__ tok, const T* __restrict__ dout,
+                                                        int n, int V, int C, int L, int tpc, int slabs, float scale,
+                                                        float* __restrict__ dtable, float* __restrict__ part, int nchunk) {
+  constexpr int N = VEC ? Vec<T>::n : 1;
+  const int gpb = blockDim.x / tpc;
+  const long long unit = (long long)blockIdx.x * gpb + threadIdx.x / tpc;
+  const int chunk = (int)(unit / slabs), slab = (int)(unit - (long long)chunk * slabs);
+  const int c = (slab * tpc + (int)threadIdx.x % tpc) * N;
+  if (chunk >= nchunk || c >= C) return;
+  const int b = chunk * L, e = min(n, b + L);
+  float acc[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) acc[k] = 0.f;
+  int cur = key[b];
+  bool open = b > 0 && key[b - 1] == cur;                     // the run began in an earlier chunk
+  auto flush = [&](float* dst, float f) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) dst[k] = acc[k] * f;
+  };
+  for (int i0 = b; i0 < e; i0 += 4) {
+    int kk[4], tt[4];
+    float x[4][N];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      kk[j] = i0 + j < e ? key[i0 + j] : V;
+      tt[j] = i0 + j < e ? tok[i0 + j] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[j][k] = 0.f;
+      if (kk[j] < V) {
+        const T* p = dout + (long long)tt[j] * C + c;
+        if (VEC) unpack<T>(__ldg(reinterpret_cast<const uint4*>(p)), x[j]);
+        else x[j][0] = cvt(*p);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (i0 + j >= e) break;
+      if (kk[j] != cur) {
+        if (cur < V) {
+          if (open) flush(part + ((size_t)chunk * 2) * C + c, 1.f);
+          else flush(dtable + (size_t)cur * C + c, scale);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] = 0.f;
+        cur = kk[j];
+        open = false;
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] += x[j][k];
+    }
+  }
+  if (cur >= V) return;
+  const bool goes_on = e < n && key[e] == cur;
+  if (open) flush(part + ((size_t)chunk * 2) * C + c, 1.f);
+  else if (goes_on) flush(part + ((size_t)chunk * 2 + 1) * C + c, 1.f);
+  else flush(dtable + (size_t)cur * C + c, scale);
+}
+
+__device__ __forceinline__ int lower_bound(const int* key, int n, int v) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (key[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+// Rows without a token are zero; rows whose run crosses chunks are the pieces' sum.
+__global__ void __launch_bounds__(256) embed_rows_kernel(const int* __restrict__ key, int n, int V, int C, int L, float scale,
+                                                         const float* __restrict__ part, float* __restrict__ dtable) {
+  const int lane = threadIdx.x & 31;
+  const long long v = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (v >= V) return;
+  const int b = lower_bound(key, n, (int)v);
+  float* o = dtable + v * C;
+  if (b >= n || key[b] != v) {
+    for (int c = lane; c < C; c += 32) o[c] = 0.f;
+    return;
+  }
+  const int first = b / L, e = lower_bound(key, n, (int)v + 1), last = (e - 1) / L;
+  if (first == last) return;
+  for (int c = lane; c < C; c += 32) {
+    float x = part[((size_t)first * 2 + 1) * C + c];
+    for (int q = first + 1; q <= last; ++q) x += part[((size_t)q * 2) * C + c];
+    o[c] = x * scale;
+  }
+}
+
+bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Workspace of the gradient: two copies of (key, token), digit counts, pieces.
+struct EmbedPlan {
+  int nblk, passes, bits, L, nchunk;
+  size_t off_key[2], off_tok[2], off_hist, off_total, off_part, total;
+};
+EmbedPlan embed_plan(long long T, int V, int C) {
+  EmbedPlan p;
+  int need = 1;
+  while (need < 31 && (V >> need) != 0) ++need;              // bits of the values 0 .. V
+  p.passes = (need + 7) / 8;
+  p.bits = (need + p.passes - 1) / p.passes;
+  p.nblk = (int)((T + kSortBlock - 1) / kSortBlock);
+  p.L = 32;
+  while (p.L < 512 && (T + p.L - 1) / p.L > 148 * 32) p.L *= 2;
+  p.nchunk = (int)((T + p.L - 1) / p.L);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  for (int k = 0; k < 2; ++k) {
+    p.off_key[k] = take((size_t)T * 4);
+    p.off_tok[k] = take((size_t)T * 4);
+  }
+  p.off_hist = take((size_t)p.nblk * kDigits * 4);
+  p.off_total = take(kDigits * 4);
+  p.off_part = take((size_t)p.nchunk * 2 * C * 4);
+  p.total = o;
+  return p;
+}
+
+template <typename T>
+cudaError_t embed_fwd(const int* idx, const void* table, void* out, long long rows, int V, int C, float scale, cudaStream_t s) {
+  const bool vec = C % Vec<T>::n == 0 && is_aligned(table, 16) && is_aligned(out, 16);
+  const int pieces = vec ? C / Vec<T>::n : C;
+  const long long need = (rows * pieces + 255) / 256, most = 148 * 64;
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  if (vec)
+    embed_fwd_kernel<T, true><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, scale);
+  else
+    embed_fwd_kernel<T, false><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, scale);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t embed_sum(const EmbedPlan& p, uint8_t* ws, int at, const void* dout, int n, int V, int C, float scale, float* dtable,
+                      cudaStream_t s) {
+  const bool vec = C % Vec<T>::n == 0 && is_aligned(dout, 16) && is_aligned(dtable, 16);
+  const int pieces = vec ? C / Vec<T>::n : C;
+  int tpc = 1;
+  while (tpc < pieces && tpc < 256) tpc *= 2;
+  const int slabs = (pieces + tpc - 1) / tpc, gpb = 256 / tpc;
+  const unsigned grid = (unsigned)(((long long)p.nchunk * slabs + gpb - 1) / gpb);
+  const int* key = reinterpret_cast<const int*>(ws + p.off_key[at]);
+  const int* tok = reinterpret_cast<const int*>(ws + p.off_tok[at]);
+  float* part = reinterpret_cast<float*>(ws + p.off_part);
+  if (vec)
+    embed_sum_kernel<T, true><<<grid, 256, 0, s>>>(key, tok, static_cast<const T*>(dout), n, V, C, p.L, tpc, slabs, scale, dtable, part, p.nchunk);
+  else
+    embed_sum_kernel<T, false><<<grid, 256, 0, s>>>(key, tok, static_cast<const T*>(dout), n, V, C, p.L, tpc, slabs, scale, dtable, part, p.nchunk);
+  return cudaGetLastError();
+}
+
+constexpr long long kEmbedMaxTokens = 1ll << 30;
+
+fipa_status embed_check(fipa_dtype dtype, long long T, int V, int C, double scale) {
+  if (dtype != FIPA_F32 && dtype != FIPA_BF16) return FIPA_ERR_INVALID_ARG;
+  if (T < 0 || V <= 0 || C <= 0 || !isfinite((float)scale)) return FIPA_ERR_INVALID_ARG;
+  if (T > kEmbedMaxTokens || C > 65536 || V > (1 << 30)) return FIPA_ERR_UNSUPPORTED;
+  return FIPA_OK;
+}
+
+}  // namespace
+}  // namespace fipa
+
+FIPA_API fipa_status fipa_embedding(fipa_dtype dtype, const int32_t* idx, const void* table, int64_t T, int V, int C,
+                                    double scale, void* out, void* stream) {
+  const fipa_status st = fipa::embed_check(dtype, T, V, C, scale);
+  if (st != FIPA_OK) return st;
+  if (T == 0) return FIPA_OK;
+  const size_t es = dtype == FIPA_F32 ? 4 : 2;
+  if (idx == nullptr || table == nullptr || out == nullptr || !fipa::is_aligned(idx, 4) || !fipa::is_aligned(table, es) ||
+      !fipa::is_aligned(out, es))
+    return FIPA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == FIPA_F32 ? fipa::embed_fwd<float>(idx, table, out, T, V, C, (float)scale, s)
+                                          : fipa::embed_fwd<__nv_bfloat16>(idx, table, out, T, V, C, (float)scale, s);
+  return e == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
+}
+
+FIPA_API fipa_status fipa_embedding_backward_workspace_size(int64_t T, int V, int C, size_t* bytes) {
+  if (bytes == nullptr) return FIPA_ERR_INVALID_ARG;
+  const fipa_status st = fipa::embed_check(FIPA_F32, T, V, C, 1.0);
+  if (st != FIPA_OK) return st;
+  *bytes = fipa::embed_plan(T, V, C).total;
+  return FIPA_OK;
+}
+
+FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* idx, const void* d_out, int64_t T, int V, int C,
+                                             double scale, float* d_table, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace fipa;
+  const fipa_status st = embed_check(dtype, T, V, C, scale);
+  if (st != FIPA_OK) return st;
+  const size_t es = dtype == FIPA_F32 ? 4 : 2;
+  if (d_table == nullptr || !is_aligned(d_table, 4)) return FIPA_ERR_INVALID_ARG;
+  if (T > 0 && (idx == nullptr || d_out == nullptr || !is_aligned(idx, 4) || !is_aligned(d_out, es))) return FIPA_ERR_INVALID_ARG;
+  const EmbedPlan p = embed_plan(T, V, C);
+  if (workspace == nullptr || workspace_bytes < p.total) return FIPA_ERR_WORKSPACE;
+  if (!is_aligned(workspace, 256)) return FIPA_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int n = (int)T;
+  int* hist = reinterpret_cast<int*>(ws + p.off_hist);
+  int* total = reinterpret_cast<int*>(ws + p.off_total);
+  const int* key = idx;
+  const int* tok = nullptr;
+  int at = 0;
+  if (n > 0) {
+    const int mask = (1 << p.bits) - 1;
+    for (int k = 0; k < p.passes; ++k) {
+      at = k & 1;
+      int* okey = reinterpret_cast<int*>(ws + p.off_key[at]);
+      int* otok = reinterpret_cast<int*>(ws + p.off_tok[at]);
+      sort_count_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, n, V, k == 0, k * p.bits, mask, hist);
+      sort_scan_kernel<<<mask + 1, 256, 0, s>>>(hist, total, p.nblk);
+      sort_move_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, tok, n, V, k == 0, k * p.bits, mask, hist, total, p.nblk, okey, otok);
+      key = okey;
+      tok = otok;
+    }
+    const cudaError_t e = dtype == FIPA_F32 ? embed_sum<float>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s)
+                                            : embed_sum<__nv_bfloat16>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s);
+    if (e != cudaSuccess) return FIPA_ERR_CUDA;
+  }
+  embed_rows_kernel<<<(unsigned)(((long long)V + 7) / 8), 256, 0, s>>>(key, n, V, C, p.L, (float)scale,
+                                                                      reinterpret_cast<float*>(ws + p.off_part), d_table);
+  return cudaGetLastError() == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
+}

@@ -10,6 +10,7 @@
 #include "fipa.h"
 #include "kernels.h"
 #include "sm100.cuh"
+#include "window.h"
 
 #define FIPA_API extern "C" __attribute__((visibility("default")))
 
@@ -784,4 +785,139 @@ FIPA_API fipa_status fipa_ipa_layer(fipa_handle* h, const float* s, const float*
                                     st)) != cudaSuccess)
     return cuda_fail(h, "layer frame-update launch", e);
   return FIPA_OK;
+}
+
+// ------------------------------------------------ window attention with sinks
+namespace {
+
+// Validates a window problem and fills the argument block (no tensors yet).
+fipa_status window_args(fipa_handle* h, const fipa_window* w, fipa::WinArgs* a) {
+  if (w == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, "win is NULL");
+  if (w->B <= 0 || w->Nq <= 0 || w->Nk <= 0 || w->H <= 0 || w->Hkv <= 0 || w->D <= 0 || w->Dv <= 0)
+    return fail(h, FIPA_ERR_INVALID_ARG, "every size must be > 0");
+  if (w->H % w->Hkv != 0) return fail(h, FIPA_ERR_INVALID_ARG, "H must be a multiple of Hkv");
+  if (w->sinks < 0) return fail(h, FIPA_ERR_INVALID_ARG, "sinks must be >= 0");
+  if (!(w->scale > 0.0) || !std::isfinite((float)w->scale) || !((float)w->scale > 0.f))
+    return fail(h, FIPA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (w->D > fipa::kWinMaxD || w->Dv > fipa::kWinMaxD) return fail(h, FIPA_ERR_UNSUPPORTED, "D and Dv must be <= 128");
+  if (w->sinks > fipa::kWinMaxSinks) return fail(h, FIPA_ERR_UNSUPPORTED, "sinks must be <= 128");
+  const int64_t lim = 0x3fffffff;
+  if (w->Nk > lim || (int64_t)w->Nq * (w->H / w->Hkv) > lim ||
+      (int64_t)w->B * w->Hkv * ((int64_t)w->Nk + (int64_t)w->Nq * (w->H / w->Hkv) + 65536) / 16 > lim)
+    return fail(h, FIPA_ERR_UNSUPPORTED, "problem too large for one launch");
+  *a = fipa::WinArgs{};
+  a->B = w->B; a->Nq = w->Nq; a->Nk = w->Nk; a->H = w->H; a->Hkv = w->Hkv; a->G = w->H / w->Hkv;
+  a->D = w->D; a->Dv = w->Dv;
+  a->left = w->left < 0 || w->left > w->Nk ? w->Nk : w->left;
+  a->right = w->right < 0 || w->right > w->Nk ? w->Nk : w->right;
+  a->sinks = w->sinks < w->Nk ? w->sinks : w->Nk;
+  a->scale = (float)w->scale;
+  a->status = h->d_status;
+  a->timeout_ns = h->timeout_ns;
+  return FIPA_OK;
+}
+
+fipa_status window_heads(fipa_handle* h, const fipa_heads* t, const char* name, const void** p, long long* sb,
+                         long long* sn, long long* sh) {
+  if (t == nullptr || t->ptr == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (!aligned(t->ptr, h->dtype == FIPA_F32 ? 4 : 2)) return fail(h, FIPA_ERR_INVALID_ARG, std::string(name) + " is misaligned");
+  if (t->stride_b < 0 || t->stride_n < 0 || t->stride_h < 0)
+    return fail(h, FIPA_ERR_INVALID_ARG, std::string(name) + " has a negative stride");
+  *p = t->ptr;
+  *sb = t->stride_b;
+  *sn = t->stride_n;
+  *sh = t->stride_h;
+  return FIPA_OK;
+}
+
+fipa_status window_inputs(fipa_handle* h, const fipa_heads* q, const fipa_heads* k, const fipa_heads* v,
+                          const uint8_t* mask, const int32_t* q_start, fipa::WinArgs* a) {
+  fipa_status st;
+  if ((st = window_heads(h, q, "q", &a->q, &a->qb, &a->qn, &a->qh)) != FIPA_OK) return st;
+  if ((st = window_heads(h, k, "k", &a->k, &a->kb, &a->kn, &a->kh)) != FIPA_OK) return st;
+  if ((st = window_heads(h, v, "v", &a->v, &a->vb, &a->vn, &a->vh)) != FIPA_OK) return st;
+  if (!aligned(q_start, 4)) return fail(h, FIPA_ERR_INVALID_ARG, "q_start is misaligned");
+  a->mask = mask;
+  a->q_start = q_start;
+  return FIPA_OK;
+}
+
+// Workspace of the backward: delta [B,H,Nq], then the sinks' partial sums.
+size_t window_bwd_bytes(const fipa::WinArgs& a, fipa::WinSinkPlan* sp) {
+  *sp = fipa::win_sink_plan(a.B, a.Nq, a.Nk, a.Hkv, a.G, a.D, a.Dv, a.left, a.sinks, fipa::kWinSimtTile,
+                            fipa::kWinSimtTile);
+  const size_t delta = ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256;
+  return delta + sp->part_floats * sizeof(float);
+}
+
+}  // namespace
+
+FIPA_API fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
+                                           const fipa_heads* v, const uint8_t* mask, const int32_t* q_start,
+                                           const fipa_window* win, void* out, float* lse, void* stream) {
+  if (h == nullptr) return FIPA_ERR_INVALID_ARG;
+  h->last_error.clear();
+  fipa::WinArgs a;
+  fipa_status st;
+  if ((st = window_args(h, win, &a)) != FIPA_OK) return st;
+  if ((st = window_inputs(h, q, k, v, mask, q_start, &a)) != FIPA_OK) return st;
+  if (out == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, "out is NULL");
+  if (!aligned(out, h->dtype == FIPA_F32 ? 4 : 2) || !aligned(lse, 4))
+    return fail(h, FIPA_ERR_INVALID_ARG, "output pointer misaligned");
+  a.out = out;
+  a.lse = lse;
+  DeviceGuard g(h->device);
+  const cudaError_t e = fipa::launch_win_fwd_simt(a, h->dtype == FIPA_F32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention launch", e);
+}
+
+FIPA_API fipa_status fipa_window_attention_backward_workspace_size(const fipa_handle* hc, const fipa_window* win,
+                                                                   size_t* bytes) {
+  fipa_handle* h = const_cast<fipa_handle*>(hc);
+  if (h == nullptr || bytes == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, "null argument");
+  fipa::WinArgs a;
+  const fipa_status st = window_args(h, win, &a);
+  if (st != FIPA_OK) return st;
+  fipa::WinSinkPlan sp;
+  *bytes = window_bwd_bytes(a, &sp);
+  return FIPA_OK;
+}
+
+FIPA_API fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
+                                                    const fipa_heads* v, const uint8_t* mask, const int32_t* q_start,
+                                                    const fipa_window* win, const void* out, const float* lse,
+                                                    const void* d_out, void* d_q, void* d_k, void* d_v,
+                                                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (h == nullptr) return FIPA_ERR_INVALID_ARG;
+  h->last_error.clear();
+  fipa::WinArgs a;
+  fipa_status st;
+  if ((st = window_args(h, win, &a)) != FIPA_OK) return st;
+  if ((st = window_inputs(h, q, k, v, mask, q_start, &a)) != FIPA_OK) return st;
+  const void* req[] = {out, lse, d_out, d_q, d_k, d_v};
+  const char* names[] = {"out", "lse", "d_out", "d_q", "d_k", "d_v"};
+  const size_t es = h->dtype == FIPA_F32 ? 4 : 2;
+  for (int i = 0; i < 6; ++i) {
+    if (req[i] == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, std::string(names[i]) + " is NULL");
+    if (!aligned(req[i], i == 1 ? 4 : es)) return fail(h, FIPA_ERR_INVALID_ARG, std::string(names[i]) + " is misaligned");
+  }
+  fipa::WinSinkPlan sp;
+  const size_t need = window_bwd_bytes(a, &sp);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(h, FIPA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  if (!aligned(workspace, 256)) return fail(h, FIPA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  a.out = const_cast<void*>(out);
+  a.lse = const_cast<float*>(lse);
+  a.d_out = d_out;
+  a.d_q = d_q;
+  a.d_k = d_k;
+  a.d_v = d_v;
+  a.delta = static_cast<float*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                    ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256);
+  a.nchunk = sp.nchunk;
+  a.chunk_tiles = sp.chunk_tiles;
+  DeviceGuard g(h->device);
+  const cudaError_t e = fipa::launch_win_bwd_simt(a, h->dtype == FIPA_F32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention backward launch", e);
 }

@@ -1,0 +1,480 @@
+// norm.cu -- the junction between two blocks of a residual network, and its
+// gradient (fipa_norm_residual, fipa_norm_residual_backward):
+//   y = Norm(u) post_w + post_b,  r = s + res_scale sigmoid(gate) y,
+//   x = Norm(r) pre_w + pre_b,    Norm(z) = (z - mean z) rstd (layer) or z rstd (rms).
+// With zhat = Norm(z) and h = w dy, dz = rstd (h - mean h - zhat mean(h zhat))
+// (rms: without mean h).
+//
+// Bound by memory: one pass, every tensor read or written once, a row held in
+// the registers of the 2^k threads (8 elements each) that own it.  The mean is
+// subtracted before squares are summed, so a large mean costs no digits.  The
+// backward recomputes r from s, u and gate (as many bytes as reading r, and not
+// rounded to the stream's type).  Parameter gradients: every thread keeps the
+// sums of its own columns over the rows its CTA walks; the CTAs' sums are added
+// in CTA order by a second kernel.  All arithmetic is float32; a tensor's type
+// is only how it is stored, rounded once.
+#include <math.h>
+
+#include "fipa.h"
+#include "kernels.h"
+
+#define FIPA_API extern "C" __attribute__((visibility("default")))
+
+namespace fipa {
+namespace {
+
+constexpr int E = 8;                       // elements of a row per thread
+constexpr int kNormMaxC = 8192;
+
+struct NormArgs {
+  const void *s, *u, *gate;
+  const uint8_t* mask;
+  const float *res_scale, *post_w, *post_b, *pre_w, *pre_b;
+  void *r, *x;
+  float* stats;                            // [rows][4]: mean u, rstd u, mean r, rstd r
+  const void *d_r, *d_x;
+  void *d_s, *d_u, *d_gate;
+  float* part;                             // [grid][5][C]
+  long long rows;
+  int C, tpr, rms;                         // threads per row: a power of two
+  float eps;
+};
+
+__device__ __forceinline__ float cvt(float x) { return x; }
+__device__ __forceinline__ float cvt(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// The thread's elements of a row: 8 neighbours by 16-byte accesses (VEC), or
+// every tpr-th element, so that a warp's accesses are contiguous at any width.
+template <bool VEC>
+__device__ __forceinline__ int col(int t, int tpr, int e) { return VEC ? t * E + e : t + e * tpr; }
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void get_row(const T* p, int t, int tpr, int C, bool on, float (&v)[E]) {
+  if (VEC) {
+    if (on && t * E < C) {
+      if (sizeof(T) == 2) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + t * E));
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = __uint_as_float(ww[e] << 16);
+          v[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
+        }
+      } else {
+        const float4 lo = __ldg(reinterpret_cast<const float4*>(p + t * E));
+        const float4 hi = __ldg(reinterpret_cast<const float4*>(p + t * E) + 1);
+        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = t + e * tpr;
+      v[e] = on && c < C ? cvt(p[c]) : 0.f;
+    }
+  }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void put_row(T* p, int t, int tpr, int C, const float (&v)[E]) {
+  if (VEC) {
+    if (t * E >= C) return;
+    if (sizeof(T) == 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(p + t * E) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float4* q = reinterpret_cast<float4*>(p + t * E);
+      q[0] = make_float4(v[0], v[1], v[2], v[3]);
+      q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = t + e * tpr;
+      if (c < C) put(p + c, v[e]);
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void get_param(const float* p, float none, int t, int tpr, int C, float (&v)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = col<VEC>(t, tpr, e);
+    v[e] = p == nullptr ? none : (c < C ? __ldg(p + c) : 0.f);
+  }
+}
+
+// Sums of two values over the tpr threads of a row, the same in all of them.
+// Every thread of the CTA calls it (rows of more than a warp meet in shared memory).
+__device__ __forceinline__ float2 row_sum(float2 v, int tpr, float2* red) {
+  const int w = tpr < 32 ? tpr : 32;
+  for (int o = w >> 1; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  if (tpr > 32) {
+    const int nw = tpr >> 5, warp = threadIdx.x >> 5, first = warp / nw * nw;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    v = make_float2(0.f, 0.f);
+    for (int k = 0; k < nw; ++k) {
+      v.x += red[first + k].x;
+      v.y += red[first + k].y;
+    }
+  }
+  return v;
+}
+
+// mean and rstd of the row (elements beyond C hold 0 and are left out)
+template <bool VEC>
+__device__ __forceinline__ float2 moments(const float (&z)[E], int t, const NormArgs& a, float2* red) {
+  const float inv = 1.f / (float)a.C;
+  float mean = 0.f;
+  if (!a.rms) {
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v.x += z[e];
+    mean = row_sum(v, a.tpr, red).x * inv;
+  }
+  float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float d = col<VEC>(t, a.tpr, e) < a.C ? z[e] - mean : 0.f;
+    v.x = fmaf(d, d, v.x);
+  }
+  return make_float2(mean, rsqrtf(row_sum(v, a.tpr, red).x * inv + a.eps));
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+template <typename TS, typename TB, bool VEC>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
+  __shared__ float2 red[32];
+  const int t = threadIdx.x & (a.tpr - 1), rpb = blockDim.x / a.tpr;
+  float ga[E], pw[E], pb[E], qw[E], qb[E];
+  get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
+  get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, pw);
+  get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, pb);
+  get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, qw);
+  get_param<VEC>(a.pre_b, 0.f, t, a.tpr, a.C, qb);
+  for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += (long long)gridDim.x * rpb) {
+    const long long row = r0 + threadIdx.x / a.tpr;
+    const bool in = row < a.rows, live = in && (a.mask == nullptr || a.mask[row] != 0);
+    const long long o = (in ? row : 0) * a.C;
+    float s[E], u[E], g[E];
+    get_row<VEC>(static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, in, s);
+    float2 mu = make_float2(0.f, 0.f), mr = mu;
+    if (a.u != nullptr) {
+      get_row<VEC>(static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
+      if (a.gate != nullptr) get_row<VEC>(static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
+      if (a.post_w != nullptr) mu = moments<VEC>(u, t, a, red);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float y = u[e];
+        if (a.post_w != nullptr) y = fmaf((u[e] - mu.x) * mu.y, pw[e], pb[e]);
+        if (a.gate != nullptr) y *= sigmoid(g[e]);
+        if (live && col<VEC>(t, a.tpr, e) < a.C) s[e] = fmaf(ga[e], y, s[e]);
+      }
+      if (in) put_row<VEC>(static_cast<TS*>(a.r) + o, t, a.tpr, a.C, s);
+    }
+    if (a.pre_w != nullptr) {
+      float z[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) z[e] = live ? s[e] : 0.f;
+      mr = moments<VEC>(z, t, a, red);
+#pragma unroll
+      for (int e = 0; e < E; ++e) z[e] = live ? fmaf((z[e] - mr.x) * mr.y, qw[e], qb[e]) : 0.f;
+      if (in) put_row<VEC>(static_cast<TB*>(a.x) + o, t, a.tpr, a.C, z);
+    }
+    if (a.stats != nullptr && in && t == 0)
+      *reinterpret_cast<float4*>(a.stats + 4 * row) = live ? make_float4(mu.x, mu.y, mr.x, mr.y) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
+template <typename TS, typename TB, bool VEC>
+__global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
+  extern __shared__ float acc_s[];           // [5][C] when several rows share a CTA
+  __shared__ float2 red[32];
+  const int t = threadIdx.x & (a.tpr - 1), rpb = blockDim.x / a.tpr;
+  const float inv = 1.f / (float)a.C;
+  float dga[E], dpw[E], dpb[E], dqw[E], dqb[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) dga[e] = dpw[e] = dpb[e] = dqw[e] = dqb[e] = 0.f;
+  for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += (long long)gridDim.x * rpb) {
+    const long long row = r0 + threadIdx.x / a.tpr;
+    const bool in = row < a.rows, live = in && (a.mask == nullptr || a.mask[row] != 0);
+    const long long o = (in ? row : 0) * a.C;
+    float s[E], u[E], g[E], dr[E], dx[E];
+    if (a.d_r != nullptr) {
+      get_row<VEC>(static_cast<const TS*>(a.d_r) + o, t, a.tpr, a.C, in, dr);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) dr[e] = 0.f;
+    }
+    get_row<VEC>(static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, live, s);
+    if (a.u != nullptr) get_row<VEC>(static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
+    if (a.gate != nullptr) get_row<VEC>(static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
+    const bool pre = a.d_x != nullptr;
+    if (pre) get_row<VEC>(static_cast<const TB*>(a.d_x) + o, t, a.tpr, a.C, live, dx);
+    const float4 st = live ? *reinterpret_cast<const float4*>(a.stats + 4 * row) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float w[E];
+    // u -> uhat; y in w; s -> r; gate -> sigmoid
+    if (a.u != nullptr) {
+      float pb[E], ga[E];
+      get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
+      get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, pb);
+      get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool cin = col<VEC>(t, a.tpr, e) < a.C;
+        if (a.post_w != nullptr) {
+          u[e] = cin ? (u[e] - st.x) * st.y : 0.f;
+          w[e] = fmaf(u[e], w[e], pb[e]);
+        } else {
+          w[e] = u[e];
+        }
+        g[e] = a.gate != nullptr ? sigmoid(g[e]) : 1.f;
+        s[e] = fmaf(ga[e], g[e] * w[e], s[e]);
+      }
+    }
+    if (pre) {
+      float qw[E];
+      get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, qw);
+      float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        s[e] = col<VEC>(t, a.tpr, e) < a.C ? (s[e] - st.z) * st.w : 0.f;      // rhat
+        dqw[e] = fmaf(dx[e], s[e], dqw[e]);
+        dqb[e] += dx[e];
+        dx[e] *= qw[e];
+        m.x += dx[e];
+        m.y = fmaf(dx[e], s[e], m.y);
+      }
+      m = row_sum(m, a.tpr, red);
+      const float c1 = a.rms ? 0.f : m.x * inv, c2 = m.y * inv;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (live) dr[e] = fmaf(st.w, dx[e] - c1 - s[e] * c2, dr[e]);
+    }
+    if (a.d_s != nullptr && in) put_row<VEC>(static_cast<TS*>(a.d_s) + o, t, a.tpr, a.C, dr);
+    if (a.u != nullptr) {
+      float ga[E], pw[E];
+      get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
+      get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, pw);
+      float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool cin = live && col<VEC>(t, a.tpr, e) < a.C;
+        const float d = cin ? dr[e] : 0.f;
+        dga[e] = fmaf(d, g[e] * w[e], dga[e]);
+        const float dgy = d * ga[e], dy = dgy * g[e];
+        g[e] = dgy * w[e] * g[e] * (1.f - g[e]);
+        dpw[e] = fmaf(dy, u[e], dpw[e]);
+        dpb[e] += dy;
+        w[e] = a.post_w != nullptr ? dy * pw[e] : dy;
+        m.x += w[e];
+        m.y = fmaf(w[e], u[e], m.y);
+      }
+      if (a.d_gate != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_gate) + o, t, a.tpr, a.C, g);
+      if (a.post_w != nullptr) {
+        m = row_sum(m, a.tpr, red);
+        const float e1 = a.rms ? 0.f : m.x * inv, e2 = m.y * inv;
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = st.y * (w[e] - e1 - u[e] * e2);
+      }
+      if (a.d_u != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_u) + o, t, a.tpr, a.C, w);
+    }
+  }
+  // the CTA's rows in order, then one line of sums per CTA
+  float* out = a.part + (size_t)blockIdx.x * 5 * a.C;
+  float* sum[5] = {dga, dpw, dpb, dqw, dqb};
+  if (rpb == 1) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = col<VEC>(t, a.tpr, e);
+        if (c < a.C) out[k * a.C + c] = sum[k][e];
+      }
+    return;
+  }
+  const int mine = threadIdx.x / a.tpr;
+  for (int q = 0; q < rpb; ++q) {
+    if (mine == q) {
+#pragma unroll
+      for (int k = 0; k < 5; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int c = col<VEC>(t, a.tpr, e);
+          if (c < a.C) acc_s[k * a.C + c] = sum[k][e] + (q == 0 ? 0.f : acc_s[k * a.C + c]);
+        }
+    }
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < 5 * a.C; c += blockDim.x) out[c] = acc_s[c];
+}
+
+// Sums over the CTAs' lines: 8 interleaved partial sums a column, added in order.
+__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* part, int lines, int C, float* const o0, float* const o1,
+                                                          float* const o2, float* const o3, float* const o4) {
+  __shared__ float red[8][32];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5, n = 5 * C;
+  float x = 0.f;
+  if (c < n)
+    for (int l = k; l < lines; l += 8) x += part[(size_t)l * n + c];
+  red[k][threadIdx.x & 31] = x;
+  __syncthreads();
+  if (k == 0 && c < n) {
+    for (int q = 1; q < 8; ++q) x += red[q][threadIdx.x];
+    float* const o[5] = {o0, o1, o2, o3, o4};
+    float* p = o[c / C];
+    if (p != nullptr) p[c % C] = x;
+  }
+}
+
+bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int norm_tpr(int C) {
+  int t = 1;
+  while (t * E < C) t *= 2;
+  return t;
+}
+int norm_block(int tpr) { return tpr < 256 ? 256 : tpr; }
+int norm_bwd_grid(long long rows, int C) {
+  const int rpb = norm_block(norm_tpr(C)) / norm_tpr(C);
+  const long long need = (rows + rpb - 1) / rpb, most = 148 * 2;
+  return (int)(need < most ? need : most);
+}
+
+template <typename TS, typename TB>
+cudaError_t norm_launch(const NormArgs& a, bool vec, bool bwd, int grid, cudaStream_t st) {
+  const int block = norm_block(a.tpr);
+  if (!bwd) {
+    if (vec) norm_fwd_kernel<TS, TB, true><<<grid, block, 0, st>>>(a);
+    else norm_fwd_kernel<TS, TB, false><<<grid, block, 0, st>>>(a);
+  } else {
+    const size_t smem = block > a.tpr ? (size_t)5 * a.C * sizeof(float) : 0;
+    if (vec) norm_bwd_kernel<TS, TB, true><<<grid, block, smem, st>>>(a);
+    else norm_bwd_kernel<TS, TB, false><<<grid, block, smem, st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+fipa_status norm_args(const fipa_norm_dims* d, const fipa_norm_inputs* in, NormArgs* a) {
+  if (d == nullptr || in == nullptr) return FIPA_ERR_INVALID_ARG;
+  if (d->rows < 0 || d->C <= 0) return FIPA_ERR_INVALID_ARG;
+  if ((d->stream_dtype != FIPA_F32 && d->stream_dtype != FIPA_BF16) ||
+      (d->branch_dtype != FIPA_F32 && d->branch_dtype != FIPA_BF16) ||
+      (d->norm != FIPA_NORM_LAYER && d->norm != FIPA_NORM_RMS) || !(d->eps > 0.0) || !isfinite((float)d->eps))
+    return FIPA_ERR_INVALID_ARG;
+  if (d->C > kNormMaxC) return FIPA_ERR_UNSUPPORTED;
+  const bool u = in->u != nullptr || d->rows == 0;           // an empty tensor may have no address
+  if (d->rows > 0 && in->s == nullptr) return FIPA_ERR_INVALID_ARG;
+  if (!u && (in->gate || in->res_scale || in->post_w)) return FIPA_ERR_INVALID_ARG;
+  if ((in->post_b && !in->post_w) || (in->pre_b && !in->pre_w)) return FIPA_ERR_INVALID_ARG;
+  if (!u && !in->pre_w) return FIPA_ERR_INVALID_ARG;
+  const size_t es = d->stream_dtype == FIPA_F32 ? 4 : 2, eb = d->branch_dtype == FIPA_F32 ? 4 : 2;
+  if (!is_aligned(in->s, es) || !is_aligned(in->u, eb) || !is_aligned(in->gate, eb) || !is_aligned(in->res_scale, 4) ||
+      !is_aligned(in->post_w, 4) || !is_aligned(in->post_b, 4) || !is_aligned(in->pre_w, 4) || !is_aligned(in->pre_b, 4))
+    return FIPA_ERR_INVALID_ARG;
+  *a = NormArgs{};
+  a->s = in->s; a->u = in->u; a->gate = in->gate; a->mask = in->mask;
+  a->res_scale = in->res_scale; a->post_w = in->post_w; a->post_b = in->post_b; a->pre_w = in->pre_w; a->pre_b = in->pre_b;
+  a->rows = d->rows;
+  a->C = d->C;
+  a->tpr = norm_tpr(d->C);
+  a->rms = d->norm == FIPA_NORM_RMS;
+  a->eps = (float)d->eps;
+  return FIPA_OK;
+}
+
+cudaError_t norm_dispatch(const fipa_norm_dims* d, const NormArgs& a, bool vec, bool bwd, int grid, cudaStream_t st) {
+  const bool s32 = d->stream_dtype == FIPA_F32, b32 = d->branch_dtype == FIPA_F32;
+  if (s32 && b32) return norm_launch<float, float>(a, vec, bwd, grid, st);
+  if (s32) return norm_launch<float, __nv_bfloat16>(a, vec, bwd, grid, st);
+  if (b32) return norm_launch<__nv_bfloat16, float>(a, vec, bwd, grid, st);
+  return norm_launch<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, grid, st);
+}
+
+}  // namespace
+}  // namespace fipa
+
+FIPA_API fipa_status fipa_norm_residual(const fipa_norm_dims* d, const fipa_norm_inputs* in, void* r, void* x, float* stats,
+                                        void* stream) {
+  using namespace fipa;
+  NormArgs a;
+  const fipa_status st = norm_args(d, in, &a);
+  if (st != FIPA_OK) return st;
+  if (d->rows == 0) return FIPA_OK;
+  if ((r == nullptr) != (in->u == nullptr) || (x == nullptr) != (in->pre_w == nullptr)) return FIPA_ERR_INVALID_ARG;
+  const size_t es = d->stream_dtype == FIPA_F32 ? 4 : 2, eb = d->branch_dtype == FIPA_F32 ? 4 : 2;
+  if (!is_aligned(r, es) || !is_aligned(x, eb) || !is_aligned(stats, 16)) return FIPA_ERR_INVALID_ARG;
+  a.r = r;
+  a.x = x;
+  a.stats = stats;
+  const bool vec = a.C % E == 0 && is_aligned(a.s, 16) && is_aligned(a.u, 16) && is_aligned(a.gate, 16) &&
+                   is_aligned(r, 16) && is_aligned(x, 16);
+  const int rpb = norm_block(a.tpr) / a.tpr;
+  const long long need = (a.rows + rpb - 1) / rpb, most = 148 * 4;
+  return norm_dispatch(d, a, vec, false, (int)(need < most ? need : most), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FIPA_OK
+             : FIPA_ERR_CUDA;
+}
+
+FIPA_API fipa_status fipa_norm_residual_backward_workspace_size(const fipa_norm_dims* d, size_t* bytes) {
+  if (d == nullptr || bytes == nullptr || d->rows < 0 || d->C <= 0) return FIPA_ERR_INVALID_ARG;
+  if (d->C > fipa::kNormMaxC) return FIPA_ERR_UNSUPPORTED;
+  *bytes = (size_t)fipa::norm_bwd_grid(d->rows, d->C) * 5 * d->C * sizeof(float);
+  return FIPA_OK;
+}
+
+FIPA_API fipa_status fipa_norm_residual_backward(const fipa_norm_dims* d, const fipa_norm_inputs* in, const float* stats,
+                                                 const void* d_r, const void* d_x, const fipa_norm_grads* g,
+                                                 void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace fipa;
+  NormArgs a;
+  const fipa_status st = norm_args(d, in, &a);
+  if (st != FIPA_OK) return st;
+  if (g == nullptr) return FIPA_ERR_INVALID_ARG;
+  if (d_x != nullptr && in->pre_w == nullptr) return FIPA_ERR_INVALID_ARG;
+  if (d->rows > 0 && stats == nullptr) return FIPA_ERR_INVALID_ARG;
+  if ((d->rows > 0 && ((g->u && !in->u) || (g->gate && !in->gate))) || (g->res_scale && !in->res_scale) || (g->post_w && !in->post_w) ||
+      (g->post_b && !in->post_b) || (g->pre_w && !in->pre_w) || (g->pre_b && !in->pre_b))
+    return FIPA_ERR_INVALID_ARG;
+  const size_t es = d->stream_dtype == FIPA_F32 ? 4 : 2, eb = d->branch_dtype == FIPA_F32 ? 4 : 2;
+  if (!is_aligned(stats, 16) || !is_aligned(d_r, es) || !is_aligned(d_x, eb) || !is_aligned(g->s, es) ||
+      !is_aligned(g->u, eb) || !is_aligned(g->gate, eb) || !is_aligned(g->res_scale, 4) || !is_aligned(g->post_w, 4) ||
+      !is_aligned(g->post_b, 4) || !is_aligned(g->pre_w, 4) || !is_aligned(g->pre_b, 4))
+    return FIPA_ERR_INVALID_ARG;
+  size_t need = 0;
+  fipa_norm_residual_backward_workspace_size(d, &need);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FIPA_ERR_WORKSPACE;
+  if (!is_aligned(workspace, 256)) return FIPA_ERR_INVALID_ARG;
+  a.stats = const_cast<float*>(stats);
+  a.d_r = d_r;
+  a.d_x = d_x;
+  a.d_s = g->s;
+  a.d_u = g->u;
+  a.d_gate = g->gate;
+  a.part = static_cast<float*>(workspace);
+  const bool vec = a.C % E == 0 && is_aligned(a.s, 16) && is_aligned(a.u, 16) && is_aligned(a.gate, 16) &&
+                   is_aligned(d_r, 16) && is_aligned(d_x, 16) && is_aligned(g->s, 16) && is_aligned(g->u, 16) &&
+                   is_aligned(g->gate, 16);
+  const int grid = norm_bwd_grid(d->rows, d->C);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (grid > 0 && norm_dispatch(d, a, vec, true, grid, s) != cudaSuccess) return FIPA_ERR_CUDA;
+  norm_reduce_kernel<<<(5 * d->C + 31) / 32, 256, 0, s>>>(a.part, grid, d->C, g->res_scale, g->post_w, g->post_b, g->pre_w,
+                                                         g->pre_b);
+  return cudaGetLastError() == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
+}

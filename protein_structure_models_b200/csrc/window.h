@@ -1,0 +1,111 @@
+// window.h -- argument block, geometry and launchers of the window attention
+// with sinks (fipa_window_attention and its backward).
+//
+// Query i of sample b stands at position p = q_start[b] + i.  It sees key j iff
+//   0 <= j < Nk,  j <= p + right,  j >= p - left or j < sinks,  mask[b, j],
+// and nothing at all if p is outside [0, Nk) or mask[b, p] is 0.
+//
+// The G = H / Hkv query heads that share a key head are rows of one problem:
+// row f = i G + g of (b, hkv) is query i of head hkv G + g, so that a row tile
+// covers few positions, its window is short, and K and V are read once a group.
+//
+// Columns of a row tile are virtual: u < s are the sinks that lie before the
+// tile's window, then come the window's keys lo .. hi.  Both ranges that a row
+// sees are ranges of u (a sink inside the window has u = j as well).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace fipa {
+
+struct WinArgs {
+  const void *q, *k, *v;             // [B,N,heads,width] with element strides, width contiguous
+  long long qb, qn, qh, kb, kn, kh, vb, vn, vh;
+  void* out;                         // [B,Nq,H,Dv]
+  float* lse;                        // [B,H,Nq] or null (forward), given (backward)
+  const uint8_t* mask;               // [B,Nk] or null
+  const int* q_start;                // [B] or null: Nk - Nq
+  int B, Nq, Nk, H, Hkv, G, D, Dv;
+  int left, right, sinks;            // left, right <= Nk; sinks <= min(Nk, kWinMaxSinks)
+  float scale;
+  // backward
+  const void* d_out;                 // [B,Nq,H,Dv]
+  void *d_q, *d_k, *d_v;             // contiguous
+  float* delta;                      // [B,H,Nq] workspace: sum_c d_out out
+  float* part;                       // sink partials, see win_sink_plan
+  int nchunk, chunk_tiles;           // sink jobs of a key tile, row tiles of each
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+constexpr int kWinMaxD = 128;
+constexpr int kWinMaxSinks = 128;
+
+// The gradient of a sink key sums over every later query, which one CTA would
+// walk alone: the queries beyond the window of the sinks' key tile are cut into
+// `nchunk` chunks of `chunk_tiles` row tiles, whose float32 partial sums (and
+// the window's own) are added in chunk order by win_sink_reduce.
+struct WinSinkPlan {
+  int nchunk, chunk_tiles, nsink_tiles;
+  size_t part_floats;
+};
+inline WinSinkPlan win_sink_plan(int B, int Nq, int Nk, int Hkv, int G, int D, int Dv, int left, int sinks, int key_tile,
+                                 int row_tile) {
+  WinSinkPlan s{0, 0, 0, 0};
+  if (sinks <= 0 || (long long)key_tile - 1 + left >= Nk - 1) return s;   // the window of tile 0 reaches every position
+  const long long tiles = ((long long)Nq * G + row_tile - 1) / row_tile;
+  s.nsink_tiles = (sinks + key_tile - 1) / key_tile;
+  s.chunk_tiles = 8;                                                     // about the window loop of the other key tiles
+  while ((tiles + s.chunk_tiles - 1) / s.chunk_tiles > 64) s.chunk_tiles *= 2;
+  s.nchunk = (int)((tiles + s.chunk_tiles - 1) / s.chunk_tiles);
+  s.part_floats = (size_t)B * Hkv * (s.nchunk + 1) * sinks * (D + Dv);
+  return s;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int win_q0(const WinArgs& a, int b) {
+  if (a.q_start == nullptr) return a.Nk - a.Nq;
+  return min(max(a.q_start[b], -a.Nq), a.Nk);       // beyond these no row is inside [0, Nk), and p cannot overflow
+}
+
+// Virtual columns of the row tile [f0, f1) of a sample with first position q0.
+struct WinCols {
+  int lo, hi, s, n;       // window keys lo..hi, sinks before it, columns in all (0: the tile sees nothing)
+  __device__ __forceinline__ int key(int u) const { return u < s ? u : lo + (u - s); }
+};
+__device__ __forceinline__ WinCols win_cols(const WinArgs& a, int q0, int f0, int f1) {
+  const int pl = max(q0 + f0 / a.G, 0), ph = min(q0 + (f1 - 1) / a.G, a.Nk - 1);
+  WinCols c{0, -1, 0, 0};
+  if (pl > ph) return c;
+  c.lo = max(0, pl - a.left);
+  c.hi = min(a.Nk - 1, ph + a.right);
+  c.s = min(a.sinks, c.lo);
+  c.n = c.s + c.hi - c.lo + 1;
+  return c;
+}
+// The two column ranges of the row at position p: [0, s1) and [w0, w1).
+struct WinRow {
+  int s1, w0, w1;
+  __device__ __forceinline__ bool sees(int u) const { return u < s1 || (u >= w0 && u < w1); }
+};
+__device__ __forceinline__ WinRow win_row(const WinArgs& a, const WinCols& c, int p, bool alive) {
+  WinRow r{0, 0, 0};
+  if (!alive) return r;
+  r.s1 = min(a.sinks, p + a.right + 1);
+  r.w0 = max(p - a.left, c.lo) - c.lo + c.s;
+  r.w1 = min(p + a.right, c.hi) - c.lo + c.s + 1;
+  return r;
+}
+__device__ __forceinline__ bool win_alive(const WinArgs& a, int b, int p) {
+  return p >= 0 && p < a.Nk && (a.mask == nullptr || a.mask[(long long)b * a.Nk + p] != 0);
+}
+#endif
+
+cudaError_t launch_win_fwd_simt(const WinArgs& a, int f32, cudaStream_t s);
+cudaError_t launch_win_bwd_simt(const WinArgs& a, int f32, cudaStream_t s);
+
+constexpr int kWinSimtTile = 64;       // rows and keys of a SIMT tile
+
+}  // namespace fipa

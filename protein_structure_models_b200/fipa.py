@@ -35,6 +35,32 @@ class FipaGrads(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in GRAD_FIELDS]
 
 
+class FipaWindow(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("B", "Nq", "Nk", "H", "Hkv", "D", "Dv", "left", "right", "sinks")] \
+        + [("scale", ctypes.c_double)]
+
+
+class FipaHeads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_n", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class FipaNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int), ("stream_dtype", ctypes.c_int),
+                ("branch_dtype", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_double)]
+
+
+NORM_PARAMS = ("res_scale", "post_w", "post_b", "pre_w", "pre_b")
+
+
+class FipaNormInputs(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("s", "u", "gate", "mask") + NORM_PARAMS]
+
+
+class FipaNormGrads(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("s", "u", "gate") + NORM_PARAMS]
+
+
 class FipaError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -109,6 +135,27 @@ def load_library():
     lib.fipa_ipa_layer.argtypes = [vp] + [vp] * 5 + [vp, vp] + [vp] * 6 + [ctypes.c_double, ctypes.POINTER(FipaDims)] \
         + [vp] * 4 + [vp, sz, vp]
     lib.fipa_ipa_layer.restype = c_int
+    heads, win = ctypes.POINTER(FipaHeads), ctypes.POINTER(FipaWindow)
+    lib.fipa_window_attention.argtypes = [vp, heads, heads, heads, vp, vp, win, vp, vp, vp]
+    lib.fipa_window_attention.restype = c_int
+    lib.fipa_window_attention_backward_workspace_size.argtypes = [vp, win, ctypes.POINTER(sz)]
+    lib.fipa_window_attention_backward_workspace_size.restype = c_int
+    lib.fipa_window_attention_backward.argtypes = [vp, heads, heads, heads, vp, vp, win] + [vp] * 7 + [sz, vp]
+    lib.fipa_window_attention_backward.restype = c_int
+    nd, ni = ctypes.POINTER(FipaNormDims), ctypes.POINTER(FipaNormInputs)
+    lib.fipa_norm_residual.argtypes = [nd, ni, vp, vp, vp, vp]
+    lib.fipa_norm_residual.restype = c_int
+    lib.fipa_norm_residual_backward_workspace_size.argtypes = [nd, ctypes.POINTER(sz)]
+    lib.fipa_norm_residual_backward_workspace_size.restype = c_int
+    lib.fipa_norm_residual_backward.argtypes = [nd, ni, vp, vp, vp, ctypes.POINTER(FipaNormGrads), vp, sz, vp]
+    lib.fipa_norm_residual_backward.restype = c_int
+    i64, dbl = ctypes.c_int64, ctypes.c_double
+    lib.fipa_embedding.argtypes = [c_int, vp, vp, i64, c_int, c_int, dbl, vp, vp]
+    lib.fipa_embedding.restype = c_int
+    lib.fipa_embedding_backward_workspace_size.argtypes = [i64, c_int, c_int, ctypes.POINTER(sz)]
+    lib.fipa_embedding_backward_workspace_size.restype = c_int
+    lib.fipa_embedding_backward.argtypes = [c_int, vp, vp, i64, c_int, c_int, dbl, vp, vp, sz, vp]
+    lib.fipa_embedding_backward.restype = c_int
     lib.fipa_destroy.argtypes = [vp]
     lib.fipa_destroy.restype = c_int
     _lib = lib
@@ -334,6 +381,106 @@ class Fipa:
             ctypes.c_size_t(workspace.numel()), ctypes.c_void_p(st.cuda_stream)))
         return out
 
+    def _window_problem(self, q, k, v, window, sinks, mask, q_start, scale):
+        """Checks the tensors of a window attention call; returns its sizes and head views."""
+        dev, td = q.device, self.torch_dtype
+        if dev.type != "cuda" or dev.index != self.device:
+            raise ValueError(f"q: need a tensor on cuda:{self.device}")
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            if t.dim() != 4 or t.dtype != td or t.device != dev or (t.shape[3] > 1 and t.stride(3) != 1):
+                raise ValueError(f"{name}: need a {td} tensor [B, N, heads, width] on {dev}, its width contiguous")
+        B, Nq, H, D = q.shape
+        _, Nk, Hkv, Dv = v.shape
+        if k.shape != (B, Nk, Hkv, D) or v.shape[0] != B:
+            raise ValueError("q [B,Nq,H,D], k [B,Nk,Hkv,D], v [B,Nk,Hkv,Dv] do not fit together")
+        if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.device != dev
+                                 or mask.shape != (B, Nk) or not mask.is_contiguous()):
+            raise ValueError(f"mask: need a contiguous bool/uint8 tensor [B, Nk] on {dev}")
+        if q_start is not None and (q_start.dtype != torch.int32 or q_start.device != dev
+                                    or q_start.shape != (B,) or not q_start.is_contiguous()):
+            raise ValueError(f"q_start: need a contiguous int32 tensor [B] on {dev}")
+        left, right = (-1 if w is None else int(w) for w in window)
+        big = 0x7fffffff
+        w = FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, min(left, big), min(right, big), int(sinks),
+                       D ** -0.5 if scale is None and D > 0 else float(scale or 0.0))
+        return w, [FipaHeads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)) for t in (q, k, v)]
+
+    def window_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: tuple, sinks: int = 0,
+                         mask: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+                         scale: Optional[float] = None, want_lse: bool = False, out: Optional[dict] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> dict:
+        """fipa_window_attention: q [B,Nq,H,D], k [B,Nk,Hkv,D], v [B,Nk,Hkv,Dv] of the
+        handle's dtype (any strides, width contiguous); window = (left, right), None or
+        a negative number for no bound; the first `sinks` tokens stay visible.  q_start
+        [B] int32: position of each sample's first query (default: the queries are the
+        last Nq positions); a single token of a cached sequence is Nq = 1 with
+        window = (left, 0) and its position in q_start.  Returns {"out": [B,Nq,H,Dv]}
+        (+ "lse" [B,H,Nq] float32, which the backward needs)."""
+        w, hd = self._window_problem(q, k, v, window, sinks, mask, q_start, scale)
+        if out is None:
+            out = {"out": torch.empty((w.B, w.Nq, w.H, w.Dv), dtype=q.dtype, device=q.device)}
+            if want_lse:
+                out["lse"] = torch.empty((w.B, w.H, w.Nq), dtype=torch.float32, device=q.device)
+        else:
+            self._check_buffers(out, {"out": ((w.B, w.Nq, w.H, w.Dv), q.dtype),
+                                      "lse": ((w.B, w.H, w.Nq), torch.float32)}, q.device, ("out",))
+        s = stream if stream is not None else torch.cuda.current_stream(q.device)
+        self._check(self.lib.fipa_window_attention(
+            self.handle, *[ctypes.byref(x) for x in hd], _ptr(mask), _ptr(q_start), ctypes.byref(w), _ptr(out["out"]),
+            _ptr(out.get("lse")), ctypes.c_void_p(s.cuda_stream)))
+        return out
+
+    @staticmethod
+    def _check_buffers(bufs, want, dev, needed):
+        for name, (shape, dt) in want.items():
+            t = bufs.get(name)
+            if t is None:
+                if name in needed:
+                    raise ValueError(f"{name}: buffer missing")
+            elif t.shape != shape or t.dtype != dt or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{name}: need a contiguous {dt} tensor {tuple(shape)} on {dev}")
+
+    def window_attention_backward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                                  lse: torch.Tensor, d_out: torch.Tensor, window: tuple, sinks: int = 0,
+                                  mask: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+                                  scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                                  grads: Optional[dict] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
+        """fipa_window_attention_backward: gradients "q", "k", "v" (handle's dtype) of
+        <d_out, out>, from the forward's out and lse."""
+        w, hd = self._window_problem(q, k, v, window, sinks, mask, q_start, scale)
+        dev, td = q.device, q.dtype
+        o = ((w.B, w.Nq, w.H, w.Dv), td)
+        self._check_buffers({"out": out, "lse": lse, "d_out": d_out},
+                            {"out": o, "lse": ((w.B, w.H, w.Nq), torch.float32), "d_out": o}, dev,
+                            ("out", "lse", "d_out"))
+        shapes = {"q": ((w.B, w.Nq, w.H, w.D), td), "k": ((w.B, w.Nk, w.Hkv, w.D), td),
+                  "v": ((w.B, w.Nk, w.Hkv, w.Dv), td)}
+        if grads is None:
+            grads = {key: torch.empty(s, dtype=dt, device=dev) for key, (s, dt) in shapes.items()}
+        else:
+            self._check_buffers(grads, shapes, dev, ("q", "k", "v"))
+        if workspace is None:
+            workspace = torch.empty(self._window_workspace(w), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        self._check(self.lib.fipa_window_attention_backward(
+            self.handle, *[ctypes.byref(x) for x in hd], _ptr(mask), _ptr(q_start), ctypes.byref(w), _ptr(out),
+            _ptr(lse), _ptr(d_out), _ptr(grads["q"]), _ptr(grads["k"]), _ptr(grads["v"]), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(s.cuda_stream)))
+        return grads
+
+    def _window_workspace(self, w) -> int:
+        n = ctypes.c_size_t()
+        self._check(self.lib.fipa_window_attention_backward_workspace_size(self.handle, ctypes.byref(w),
+                                                                           ctypes.byref(n)))
+        return int(n.value)
+
+    def window_attention_backward_workspace_size(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                                 window: tuple, sinks: int = 0) -> int:
+        """Bytes of workspace window_attention_backward needs for these tensors."""
+        return self._window_workspace(self._window_problem(q, k, v, window, sinks, None, None, None)[0])
+
     BWD_STAGES = ("recompute", "prep", "q_side", "k_side", "chain")
 
     def backward_stage_times(self) -> dict:
@@ -432,6 +579,191 @@ def knn_distogram(translation: torch.Tensor, mask: torch.Tensor, k: int, edges: 
     if st != FIPA_OK:
         raise FipaError(st, "fipa_knn_distogram failed")
     return out
+
+
+def _need(name, t, shape, dtypes, dev):
+    if t.shape != tuple(shape) or t.dtype not in dtypes or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous tensor {tuple(shape)} of {dtypes} on {dev}")
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _code(t: torch.Tensor) -> int:
+    return F32 if t.dtype == torch.float32 else BF16
+
+
+def _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype):
+    """Checks the inputs of the junction; returns its dims, inputs, branch type and parameters."""
+    dev = s.device
+    if dev.type != "cuda" or s.dim() < 1:
+        raise ValueError("s: need a CUDA tensor [..., C]")
+    C = s.shape[-1]
+    _need("s", s, s.shape, _FLOATS, dev)
+    tb = u.dtype if u is not None else (branch_dtype or s.dtype)
+    if u is not None:
+        _need("u", u, s.shape, _FLOATS, dev)
+    if gate is not None:
+        _need("gate", gate, s.shape, (tb,), dev)
+    if mask is not None:
+        _need("mask", mask, s.shape[:-1], (torch.bool, torch.uint8), dev)
+    par = dict(zip(NORM_PARAMS, (res_scale, *(post or (None, None)), *(pre or (None, None)))))
+    for name, t in par.items():
+        if t is not None:
+            _need(name, t, (C,), (torch.float32,), dev)
+    if norm not in ("layer", "rms"):
+        raise ValueError('norm: "layer" or "rms"')
+    if tb not in _FLOATS:
+        raise ValueError("branch_dtype: float32 or bfloat16")
+    rows = s.numel() // C if C else 0
+    d = FipaNormDims(rows, C, _code(s), F32 if tb == torch.float32 else BF16, 0 if norm == "layer" else 1, float(eps))
+    i = FipaNormInputs(*[None if t is None else t.data_ptr() for t in (s, u, gate, mask, *par.values())])
+    return d, i, tb, par
+
+
+def _ok(st, what):
+    if st != FIPA_OK:
+        raise FipaError(st, what + " failed")
+
+
+def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  res_scale: Optional[torch.Tensor] = None, post: Optional[tuple] = None, pre: Optional[tuple] = None,
+                  mask: Optional[torch.Tensor] = None, norm: str = "layer", eps: float = 1e-5,
+                  want_stats: bool = False, branch_dtype: Optional[torch.dtype] = None, out: Optional[dict] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """fipa_norm_residual: the norm after a block (`post` = (weight, bias or None)), its gate
+    and residual scale, the residual sum and the norm before the next block (`pre`), fused:
+        r = s + res_scale * sigmoid(gate) * Norm(u, post),   x = Norm(r, pre)
+    s [..., C] (the residual stream's type), u and gate [..., C] (the branch's type),
+    parameters [C] float32, mask [...] bool/uint8 (0: padding, r = s and x = 0).
+    Returns {"r" (with u), "x" (with pre)} and, with want_stats, "stats" [rows, 4] for the
+    backward.  Without u, x = Norm(s, pre) in branch_dtype (default: that of s)."""
+    lib = load_library()
+    d, i, tb, _ = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
+    dev = s.device
+    with torch.cuda.device(dev):
+        want = {}
+        if u is not None:
+            want["r"] = (s.shape, s.dtype)
+        if pre is not None:
+            want["x"] = (s.shape, tb)
+        if out is None:
+            if want_stats:
+                want["stats"] = ((d.rows, 4), torch.float32)
+            out = {k: torch.empty(sh, dtype=dt, device=dev) for k, (sh, dt) in want.items()}
+        else:
+            for k, (sh, dt) in (want | {"stats": ((d.rows, 4), torch.float32)}).items():
+                if k in out:
+                    _need(k, out[k], sh, (dt,), dev)
+                elif k in want:
+                    raise ValueError(f"{k}: buffer missing")
+        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        _ok(lib.fipa_norm_residual(ctypes.byref(d), ctypes.byref(i), _ptr(out.get("r")), _ptr(out.get("x")),
+                                   _ptr(out.get("stats")), ctypes.c_void_p(st.cuda_stream)), "fipa_norm_residual")
+    return out
+
+
+def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: torch.Tensor,
+                           d_r: Optional[torch.Tensor], d_x: Optional[torch.Tensor], gate: Optional[torch.Tensor] = None,
+                           res_scale: Optional[torch.Tensor] = None, post: Optional[tuple] = None,
+                           pre: Optional[tuple] = None, mask: Optional[torch.Tensor] = None, norm: str = "layer",
+                           eps: float = 1e-5, branch_dtype: Optional[torch.dtype] = None,
+                           workspace: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
+                           stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """fipa_norm_residual_backward: gradients of <d_r, r> + <d_x, x> (either None: zero) for
+    every input that was given, keyed "s", "u", "gate", "res_scale", "post_w", "post_b",
+    "pre_w", "pre_b" (None where there was no input).  `grads`, if given, holds the buffers
+    of the gradients that are wanted."""
+    lib = load_library()
+    d, i, tb, par = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
+    dev = s.device
+    _need("stats", stats, (d.rows, 4), (torch.float32,), dev)
+    if d_r is not None:
+        _need("d_r", d_r, s.shape, (s.dtype,), dev)
+    if d_x is not None:
+        _need("d_x", d_x, s.shape, (tb,), dev)
+    have = {"s": s, "u": u, "gate": gate, **par}
+    with torch.cuda.device(dev):
+        if grads is None:
+            grads = {k: None if t is None else torch.empty_like(t) for k, t in have.items()}
+        else:
+            for k, t in grads.items():
+                if t is not None:
+                    if have.get(k) is None:
+                        raise ValueError(f"{k}: a gradient of an input that was not given")
+                    _need(k, t, have[k].shape, (have[k].dtype,), dev)
+        if workspace is None:
+            n = ctypes.c_size_t()
+            _ok(lib.fipa_norm_residual_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)),
+                "fipa_norm_residual_backward_workspace_size")
+            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
+        g = FipaNormGrads(*[None if grads.get(f) is None else grads[f].data_ptr() for f, _ in FipaNormGrads._fields_])
+        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        _ok(lib.fipa_norm_residual_backward(
+            ctypes.byref(d), ctypes.byref(i), _ptr(stats), _ptr(d_r), _ptr(d_x), ctypes.byref(g), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(st.cuda_stream)),
+            "fipa_norm_residual_backward")
+    return grads
+
+
+def embedding(idx: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[dict] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """fipa_embedding: {"out": scale * table[idx]} for idx [...] int32 and table [V, C]
+    float32/bfloat16; an index outside [0, V) gives a zero row."""
+    lib = load_library()
+    dev = table.device
+    if dev.type != "cuda" or table.dim() != 2:
+        raise ValueError("table: need a CUDA tensor [V, C]")
+    _need("table", table, table.shape, _FLOATS, dev)
+    _need("idx", idx, idx.shape, (torch.int32,), dev)
+    V, C = table.shape
+    with torch.cuda.device(dev):
+        if out is None:
+            out = {"out": torch.empty((*idx.shape, C), dtype=table.dtype, device=dev)}
+        else:
+            _need("out", out["out"], (*idx.shape, C), (table.dtype,), dev)
+        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        _ok(lib.fipa_embedding(_code(table), _ptr(idx), _ptr(table), idx.numel(), V, C, float(scale), _ptr(out["out"]),
+                               ctypes.c_void_p(st.cuda_stream)), "fipa_embedding")
+    return out
+
+
+def embedding_backward_workspace_size(tokens: int, V: int, C: int) -> int:
+    """Bytes of workspace embedding_backward needs."""
+    n = ctypes.c_size_t()
+    _ok(load_library().fipa_embedding_backward_workspace_size(int(tokens), int(V), int(C), ctypes.byref(n)),
+        "fipa_embedding_backward_workspace_size")
+    return int(n.value)
+
+
+def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: float = 1.0,
+                       workspace: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """fipa_embedding_backward: {"table": [V, C] float32}, the gradient of <d_out, out>."""
+    lib = load_library()
+    dev = d_out.device
+    if dev.type != "cuda" or d_out.dim() < 1:
+        raise ValueError("d_out: need a CUDA tensor [..., C]")
+    C = d_out.shape[-1]
+    _need("d_out", d_out, d_out.shape, _FLOATS, dev)
+    _need("idx", idx, d_out.shape[:-1], (torch.int32,), dev)
+    with torch.cuda.device(dev):
+        if grads is None:
+            grads = {"table": torch.empty((V, C), dtype=torch.float32, device=dev)}
+        else:
+            _need("table", grads["table"], (V, C), (torch.float32,), dev)
+        if workspace is None:
+            workspace = torch.empty(embedding_backward_workspace_size(idx.numel(), V, C), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
+        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        _ok(lib.fipa_embedding_backward(
+            _code(d_out), _ptr(idx), _ptr(d_out), idx.numel(), V, C, float(scale), _ptr(grads["table"]), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(st.cuda_stream)),
+            "fipa_embedding_backward")
+    return grads
 
 
 _handles: dict = {}
