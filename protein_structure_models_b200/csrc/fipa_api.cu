@@ -867,7 +867,8 @@ FIPA_API fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, 
   a.out = out;
   a.lse = lse;
   DeviceGuard g(h->device);
-  const cudaError_t e = fipa::launch_win_fwd_simt(a, h->dtype == FIPA_F32, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_fwd_simt(a, s) : fipa::launch_win_fwd_mma(a, s);
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention launch", e);
 }
 
@@ -918,6 +919,7 @@ FIPA_API fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_h
   a.nchunk = sp.nchunk;
   a.chunk_tiles = sp.chunk_tiles;
   DeviceGuard g(h->device);
-  const cudaError_t e = fipa::launch_win_bwd_simt(a, h->dtype == FIPA_F32, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_bwd_simt(a, s) : fipa::launch_win_bwd_mma(a, s);
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention backward launch", e);
 }

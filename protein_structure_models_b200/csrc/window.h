@@ -103,9 +103,12 @@ __device__ __forceinline__ bool win_alive(const WinArgs& a, int b, int p) {
 }
 #endif
 
-cudaError_t launch_win_fwd_simt(const WinArgs& a, int f32, cudaStream_t s);
-cudaError_t launch_win_bwd_simt(const WinArgs& a, int f32, cudaStream_t s);
+cudaError_t launch_win_fwd_simt(const WinArgs& a, cudaStream_t s);       // float32 tensors
+cudaError_t launch_win_bwd_simt(const WinArgs& a, cudaStream_t s);
+cudaError_t launch_win_fwd_mma(const WinArgs& a, cudaStream_t s);        // bfloat16 tensors
+cudaError_t launch_win_bwd_mma(const WinArgs& a, cudaStream_t s);
+cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s);
 
-constexpr int kWinSimtTile = 64;       // rows and keys of a SIMT tile
+constexpr int kWinSimtTile = 64;       // rows and keys of a tile
 
 }  // namespace fipa

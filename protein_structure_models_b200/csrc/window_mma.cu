@@ -1,0 +1,722 @@
+// window_mma.cu -- window attention with sinks on bfloat16 tensors, forward and
+// backward, with warp-level matrix instructions (m16n8k16, float32 sums).
+//
+// The mathematics, the row and column numbering and the visibility rule are
+// those of window_simt.cu and window.h.  A warp owns 16 rows (forward, dq) or
+// 16 keys (dk, dv) and keeps its scores, probabilities and sums in registers:
+// the accumulator layout of one product is the operand layout of the next, so
+// nothing of the softmax touches shared memory.  Because a warp covers only 16
+// positions it walks just the columns that they see: columns are taken 16 at a
+// time, skipped when no row of the warp sees them, and tested element by element
+// only at the edges of the window, which is what makes short windows cheap.
+// Tiles of 64 columns arrive by 16-byte asynchronous copies, the next one while
+// the present one is in use; rows in shared memory are padded by 16 bytes, so
+// that eight neighbouring rows start in different banks.
+//
+// Probabilities and ds go into the second product as bfloat16 (half a step is
+// 2^-8 of each, the tensors' own rounding); l, m, delta and all sums are float32.
+#include <math.h>
+
+#include "kernels.h"
+#include "sm100.cuh"
+#include "window.h"
+
+namespace fipa {
+namespace {
+
+typedef __nv_bfloat16 bf16;
+constexpr int T = kWinSimtTile;            // rows and columns of a tile
+constexpr int kThreads = 128;              // 4 warps x 16 rows
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int DP>
+struct Tile {
+  static constexpr int ld = DP + 8;        // elements of a padded row
+  static constexpr int elems = T * ld;
+};
+
+__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct Src {                               // one of the inputs, for one (b, hkv)
+  const bf16* p;
+  long long sn, sh;
+  int width;
+  bool vec;
+};
+// One tile of 64 rows x width elements; at(r) gives row r's elements, or null for a row of zeros.
+template <int DP, typename At>
+__device__ __forceinline__ void load_tile(bf16* dst, const Src& s, At at) {
+  constexpr int CH = DP / 8;
+  for (int e = threadIdx.x; e < T * CH; e += kThreads) {
+    const int r = e / CH, c = e % CH;
+    const bf16* p = at(r);
+    bf16* d = dst + r * Tile<DP>::ld + c * 8;
+    const bool on = p != nullptr && c * 8 < s.width;
+    if (s.vec) {
+      cp16_zfill(smem_u32(d), on ? p + c * 8 : s.p, on);
+    } else {
+      uint16_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = on && c * 8 + k < s.width ? reinterpret_cast<const uint16_t*>(p)[c * 8 + k] : (uint16_t)0;
+      *reinterpret_cast<uint4*>(d) = make_uint4(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16,
+                                                w[4] | (uint32_t)w[5] << 16, w[6] | (uint32_t)w[7] << 16);
+    }
+  }
+}
+__device__ __forceinline__ Src source(const void* base, long long sb, long long sn, long long sh, int width, int b, int h0) {
+  Src s;
+  s.p = static_cast<const bf16*>(base) + b * sb + h0 * sh;
+  s.sn = sn;
+  s.sh = sh;
+  s.width = width;
+  s.vec = ((reinterpret_cast<uintptr_t>(base) & 15) | ((sb | sn | sh | width) & 7)) == 0;
+  return s;
+}
+// The 16 x 16 A operand at row r0, depth k0 of a tile; the 16 x 16 B operand of
+// columns n0 .. n0+15 at depth k0 (rows = columns of the product), and the one
+// whose rows are the product's depth.
+template <int DP>
+__device__ __forceinline__ uint32_t a_addr(uint32_t base, int r0, int k0, int lane) {
+  return base + 2 * ((r0 + (lane & 15)) * Tile<DP>::ld + k0 + ((lane >> 4) << 3));
+}
+template <int DP>
+__device__ __forceinline__ uint32_t b_addr(uint32_t base, int n0, int k0, int lane) {
+  return base + 2 * ((n0 + (lane & 7) + ((lane >> 4) << 3)) * Tile<DP>::ld + k0 + (((lane >> 3) & 1) << 3));
+}
+template <int DP>
+__device__ __forceinline__ uint32_t bt_addr(uint32_t base, int k0, int n0, int lane) {
+  return base + 2 * ((k0 + (lane & 7) + (((lane >> 3) & 1) << 3)) * Tile<DP>::ld + n0 + ((lane >> 4) << 3));
+}
+
+// Columns that the 16 rows of a warp see: any of them, and all of them.
+struct Reach {
+  int s_any, s_all, a_any, a_all, e_any, e_all;       // sinks [0, s), window [a, e)
+  __device__ __forceinline__ bool any(int u) const { return u < s_any || (u + 15 >= a_any && u < e_any); }
+  __device__ __forceinline__ bool all(int u) const { return u + 15 < s_all || (u >= a_all && u + 15 < e_all); }
+};
+__device__ __forceinline__ Reach reach(const WinArgs& a, const WinCols& c, int q0, int f, int f1) {
+  const int lo = min(max(q0 + f / a.G, 0), a.Nk - 1), hi = min(max(q0 + (min(f + 16, f1) - 1) / a.G, 0), a.Nk - 1);
+  const WinRow x = win_row(a, c, lo, true), y = win_row(a, c, hi, true);
+  if (f >= f1) return Reach{0, 0, 0, 0, 0, 0};
+  return Reach{y.s1, x.s1, x.w0, y.w0, y.w1, x.w1};
+}
+
+// Whether columns u0 .. u0+63 exist and are not masked: two words.
+__device__ __forceinline__ void column_bits(uint32_t* bits, const WinArgs& a, int b, const WinCols& c, int u0) {
+  if (threadIdx.x < T) {
+    const int u = u0 + threadIdx.x;
+    const bool on = u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0);
+    const uint32_t w = __ballot_sync(0xffffffffu, on);
+    if ((threadIdx.x & 31) == 0) bits[threadIdx.x >> 5] = w;
+  }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16* Qs = reinterpret_cast<bf16*>(smem);
+  bf16* Ks = Qs + Tile<DP>::elems;                     // two stages each
+  bf16* Vs = Ks + 2 * Tile<DP>::elems;
+  __shared__ uint32_t bits[2][2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
+  const int F = a.Nq * a.G, tiles = (F + T - 1) / T;
+  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
+  const int f0 = tile * T, f1 = min(F, f0 + T), q0 = win_q0(a, b);
+  const WinCols c = win_cols(a, q0, f0, f1);
+  const Src q = source(a.q, a.qb, a.qn, a.qh, a.D, b, hkv * a.G);
+  const Src k = source(a.k, a.kb, a.kn, a.kh, a.D, b, hkv), v = source(a.v, a.vb, a.vn, a.vh, a.Dv, b, hkv);
+  bool alive[2];
+  WinRow row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int f = f0 + 16 * warp + (lane >> 2) + 8 * i, p = q0 + f / a.G;
+    alive[i] = f < f1 && win_alive(a, b, p);
+    row[i] = win_row(a, c, p, alive[i]);
+  }
+  const int ntile = __syncthreads_or(alive[0] || alive[1]) ? (c.n + T - 1) / T : 0;
+  const Reach rc = reach(a, c, q0, f0 + 16 * warp, f1);
+  auto load = [&](int t) {
+    const int st = t & 1, u0 = t * T;
+    auto keyed = [&](const Src& s) {
+      return [&, u0](int r) -> const bf16* {
+        const int u = u0 + r;
+        return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
+      };
+    };
+    load_tile<DP>(Ks + st * Tile<DP>::elems, k, keyed(k));
+    load_tile<DP>(Vs + st * Tile<DP>::elems, v, keyed(v));
+    column_bits(bits[st], a, b, c, u0);
+    cp_async_commit();
+  };
+  const int kd = (a.D + 15) / 16, kv = (a.Dv + 15) / 16;
+  float acc[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  uint32_t qf[DP / 16][4];
+  const float sc = a.scale * kLog2e;
+  if (ntile > 0) {
+    load_tile<DP>(Qs, q, [&](int r) -> const bf16* {
+      const int f = f0 + r, i = f / a.G;
+      return f < f1 && win_alive(a, b, q0 + i) ? q.p + i * q.sn + (f - i * a.G) * q.sh : nullptr;
+    });
+    load(0);
+  }
+  for (int t = 0; t < ntile; ++t) {
+    const int st = t & 1, u0 = t * T;
+    if (t + 1 < ntile) {
+      load(t + 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncthreads();
+    if (t == 0) {
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) ldsm4(qf[kk], a_addr<DP>(smem_u32(Qs), 16 * warp, 16 * kk, lane));
+    }
+    const uint32_t ks = smem_u32(Ks + st * Tile<DP>::elems), vs = smem_u32(Vs + st * Tile<DP>::elems);
+    const uint32_t w[2] = {bits[st][0], bits[st][1]};
+    float s[8][4];
+    bool on[4];
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t wg = (w[g >> 1] >> ((g & 1) * 16)) & 0xffffu;
+      on[g] = wg != 0u && rc.any(u0 + 16 * g);
+      if (!on[g]) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[2 * g + h][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        if (kk >= kd) break;
+        uint32_t bf[4];
+        ldsm4(bf, b_addr<DP>(ks, 16 * g, 16 * kk, lane));
+        mma(s[2 * g], qf[kk], bf[0], bf[1]);
+        mma(s[2 * g + 1], qf[kk], bf[2], bf[3]);
+      }
+      if (wg != 0xffffu || !rc.all(u0 + 16 * g)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int u = 16 * g + 8 * h + col2 + (e & 1);
+            if (!((wg >> (u & 15)) & 1u) || !row[e >> 1].sees(u0 + u)) s[2 * g + h][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[2 * g + h][e]);
+    }
+    if (on[0] || on[1] || on[2] || on[3]) {
+      float mb[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        const float mn = fmaxf(m[i], mx[i]);
+        mb[i] = mn == -INFINITY ? 0.f : mn * sc;
+        const float f = ex2_approx(m[i] * sc - mb[i]);
+        m[i] = mn;
+        l[i] *= f;
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n) {
+          acc[n][2 * i] *= f;
+          acc[n][2 * i + 1] *= f;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (!on[g]) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[2 * g + h][e] = ex2_approx(fmaf(s[2 * g + h][e], sc, -mb[e >> 1]));
+            sum[e >> 1] += s[2 * g + h][e];
+          }
+        const uint32_t pf[4] = {pack(s[2 * g][0], s[2 * g][1]), pack(s[2 * g][2], s[2 * g][3]),
+                                pack(s[2 * g + 1][0], s[2 * g + 1][1]), pack(s[2 * g + 1][2], s[2 * g + 1][3])};
+#pragma unroll
+        for (int n = 0; n < DP / 16; ++n) {
+          if (n >= kv) break;
+          uint32_t bf[4];
+          ldsm4t(bf, bt_addr<DP>(vs, 16 * g, 16 * n, lane));
+          mma(acc[2 * n], pf, bf[0], bf[1]);
+          mma(acc[2 * n + 1], pf, bf[2], bf[3]);
+        }
+      }
+      l[0] += sum[0];
+      l[1] += sum[1];
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    const int f = f0 + 16 * warp + (lane >> 2) + 8 * i;
+    if (f >= f1) continue;
+    const int qi = f / a.G, h = hkv * a.G + (f - qi * a.G);
+    const bool some = alive[i] && l[i] != 0.f;
+    const float inv = some ? 1.f / l[i] : 0.f;
+    bf16* o = static_cast<bf16*>(a.out) + (((long long)b * a.Nq + qi) * a.H + h) * a.Dv;
+    const bool pair = (a.Dv & 1) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) {
+      const int d = 8 * n + col2;
+      const float x = some ? acc[n][2 * i] * inv : 0.f, y = some ? acc[n][2 * i + 1] * inv : 0.f;
+      if (pair && d < a.Dv) {
+        *reinterpret_cast<uint32_t*>(o + d) = pack(x, y);
+      } else {
+        if (d < a.Dv) o[d] = __float2bfloat16_rn(x);
+        if (d + 1 < a.Dv) o[d + 1] = __float2bfloat16_rn(y);
+      }
+    }
+    if (a.lse != nullptr && (lane & 3) == 0)
+      a.lse[((long long)b * a.H + h) * a.Nq + qi] = some ? fmaf(m[i], a.scale, logf(l[i])) : -INFINITY;
+  }
+}
+
+// Writes a warp's 16 x DP sums as bfloat16 rows; at(i) is the row of this thread's half i, null: not written.
+template <int DP, typename At>
+__device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], int width, const void* base, float f, int lane, At at) {
+  const bool pair = (width & 1) == 0 && (reinterpret_cast<uintptr_t>(base) & 3) == 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    bool keep;
+    bf16* o = at(i, keep);
+    if (o == nullptr) continue;
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) {
+      const int d = 8 * n + (lane & 3) * 2;
+      const float x = keep ? acc[n][2 * i] * f : 0.f, y = keep ? acc[n][2 * i + 1] * f : 0.f;
+      if (pair && d < width) {
+        *reinterpret_cast<uint32_t*>(o + d) = pack(x, y);
+      } else {
+        if (d < width) o[d] = __float2bfloat16_rn(x);
+        if (d + 1 < width) o[d + 1] = __float2bfloat16_rn(y);
+      }
+    }
+  }
+}
+
+// delta = dO.out of a row tile, four neighbouring lanes a row (two passes of 32 rows); dead rows 0.
+template <int DP>
+__device__ __forceinline__ void row_delta(float* sdelta, const bf16* dOs, const WinArgs& a, const bf16* out, int b, int hkv, int q0,
+                                          int f0, int f1) {
+  for (int r = threadIdx.x >> 2; r < T; r += kThreads / 4) {
+    const int f = f0 + r, i = f / a.G, h = hkv * a.G + (f - i * a.G);
+    float x = 0.f;
+    if (f < f1 && win_alive(a, b, q0 + i)) {
+      const bf16* o = out + (((long long)b * a.Nq + i) * a.H + h) * a.Dv;
+      if ((a.Dv & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+        for (int d = (threadIdx.x & 3) * 8; d < a.Dv; d += 32) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(o + d));
+          const uint4 g = *reinterpret_cast<const uint4*>(dOs + r * Tile<DP>::ld + d);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x = fmaf(__uint_as_float(ww[e] << 16), __uint_as_float(gg[e] << 16), x);
+            x = fmaf(__uint_as_float(ww[e] & 0xffff0000u), __uint_as_float(gg[e] & 0xffff0000u), x);
+          }
+        }
+      } else {
+        for (int d = threadIdx.x & 3; d < a.Dv; d += 4)
+          x = fmaf(__bfloat162float(o[d]), __bfloat162float(dOs[r * Tile<DP>::ld + d]), x);
+      }
+    }
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    if ((threadIdx.x & 3) == 0) {
+      sdelta[r] = x;
+      if (f < f1) a.delta[((long long)b * a.H + h) * a.Nq + i] = x;
+    }
+  }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16* Qs = reinterpret_cast<bf16*>(smem);
+  bf16* Os = Qs + Tile<DP>::elems;
+  bf16* Ks = Os + Tile<DP>::elems;
+  bf16* Vs = Ks + 2 * Tile<DP>::elems;
+  __shared__ uint32_t bits[2][2];
+  __shared__ float sdelta[T];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
+  const int F = a.Nq * a.G, tiles = (F + T - 1) / T;
+  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
+  const int f0 = tile * T, f1 = min(F, f0 + T), q0 = win_q0(a, b);
+  const WinCols c = win_cols(a, q0, f0, f1);
+  const Src q = source(a.q, a.qb, a.qn, a.qh, a.D, b, hkv * a.G);
+  const Src g_ = source(a.d_out, (long long)a.Nq * a.H * a.Dv, (long long)a.H * a.Dv, a.Dv, a.Dv, b, hkv * a.G);
+  const Src k = source(a.k, a.kb, a.kn, a.kh, a.D, b, hkv), v = source(a.v, a.vb, a.vn, a.vh, a.Dv, b, hkv);
+  bool alive[2];
+  WinRow row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int f = f0 + 16 * warp + (lane >> 2) + 8 * i, p = q0 + f / a.G;
+    alive[i] = f < f1 && win_alive(a, b, p);
+    row[i] = win_row(a, c, p, alive[i]);
+  }
+  const int ntile = __syncthreads_or(alive[0] || alive[1]) ? (c.n + T - 1) / T : 0;
+  const Reach rc = reach(a, c, q0, f0 + 16 * warp, f1);
+  auto load = [&](int t) {
+    const int st = t & 1, u0 = t * T;
+    auto keyed = [&](const Src& s) {
+      return [&, u0](int r) -> const bf16* {
+        const int u = u0 + r;
+        return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
+      };
+    };
+    load_tile<DP>(Ks + st * Tile<DP>::elems, k, keyed(k));
+    load_tile<DP>(Vs + st * Tile<DP>::elems, v, keyed(v));
+    column_bits(bits[st], a, b, c, u0);
+    cp_async_commit();
+  };
+  const int kd = (a.D + 15) / 16, kv = (a.Dv + 15) / 16;
+  float acc[DP / 8][4], lse2[2] = {INFINITY, INFINITY}, del[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  const float sc = a.scale * kLog2e;
+  if (ntile > 0) {
+    auto rows = [&](const Src& s) {
+      return [&](int r) -> const bf16* {
+        const int f = f0 + r, i = f / a.G;
+        return f < f1 && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
+      };
+    };
+    load_tile<DP>(Qs, q, rows(q));
+    load_tile<DP>(Os, g_, rows(g_));
+    load(0);
+    cp_wait<0>();
+    __syncthreads();
+    row_delta<DP>(sdelta, Os, a, static_cast<const bf16*>(a.out), b, hkv, q0, f0, f1);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 16 * warp + (lane >> 2) + 8 * i, f = f0 + r, qi = f / a.G;
+      del[i] = sdelta[r];
+      if (alive[i]) {
+        const float x = a.lse[((long long)b * a.H + hkv * a.G + (f - qi * a.G)) * a.Nq + qi];
+        lse2[i] = x == -INFINITY ? INFINITY : x * kLog2e;     // a row that sees nothing: every p is 0
+      }
+    }
+  } else if (threadIdx.x < T && f0 + (int)threadIdx.x < f1) {
+    const int f = f0 + threadIdx.x, i = f / a.G;
+    a.delta[((long long)b * a.H + hkv * a.G + (f - i * a.G)) * a.Nq + i] = 0.f;
+  }
+  for (int t = 0; t < ntile; ++t) {
+    const int st = t & 1, u0 = t * T;
+    if (t + 1 < ntile) {
+      load(t + 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncthreads();
+    const uint32_t ks = smem_u32(Ks + st * Tile<DP>::elems), vs = smem_u32(Vs + st * Tile<DP>::elems);
+    const uint32_t w[2] = {bits[st][0], bits[st][1]};
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t wg = (w[g >> 1] >> ((g & 1) * 16)) & 0xffffu;
+      if (wg == 0u || !rc.any(u0 + 16 * g)) continue;
+      float s[2][4], dp[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[h][e] = dp[h][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        uint32_t af[4], bf[4];
+        if (kk < kd) {
+          ldsm4(af, a_addr<DP>(smem_u32(Qs), 16 * warp, 16 * kk, lane));
+          ldsm4(bf, b_addr<DP>(ks, 16 * g, 16 * kk, lane));
+          mma(s[0], af, bf[0], bf[1]);
+          mma(s[1], af, bf[2], bf[3]);
+        }
+        if (kk < kv) {
+          ldsm4(af, a_addr<DP>(smem_u32(Os), 16 * warp, 16 * kk, lane));
+          ldsm4(bf, b_addr<DP>(vs, 16 * g, 16 * kk, lane));
+          mma(dp[0], af, bf[0], bf[1]);
+          mma(dp[1], af, bf[2], bf[3]);
+        }
+      }
+      const bool edge = wg != 0xffffu || !rc.all(u0 + 16 * g);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = e >> 1;
+          s[h][e] = ex2_approx(fmaf(s[h][e], sc, -lse2[i])) * (dp[h][e] - del[i]);
+          if (edge) {
+            const int u = 8 * h + col2 + (e & 1);
+            if (!((wg >> u) & 1u) || !row[i].sees(u0 + 16 * g + u)) s[h][e] = 0.f;
+          }
+        }
+      const uint32_t pf[4] = {pack(s[0][0], s[0][1]), pack(s[0][2], s[0][3]), pack(s[1][0], s[1][1]), pack(s[1][2], s[1][3])};
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n) {
+        if (n >= kd) break;
+        uint32_t bf[4];
+        ldsm4t(bf, bt_addr<DP>(ks, 16 * g, 16 * n, lane));
+        mma(acc[2 * n], pf, bf[0], bf[1]);
+        mma(acc[2 * n + 1], pf, bf[2], bf[3]);
+      }
+    }
+    __syncthreads();
+  }
+  store_rows<DP>(acc, a.D, a.d_q, a.scale, lane, [&](int i, bool& keep) -> bf16* {
+    const int f = f0 + 16 * warp + (lane >> 2) + 8 * i, qi = f / a.G;
+    keep = alive[i] && lse2[i] != INFINITY;
+    return f < f1 ? static_cast<bf16*>(a.d_q) + (((long long)b * a.Nq + qi) * a.H + hkv * a.G + (f - qi * a.G)) * a.D : nullptr;
+  });
+}
+
+// dk and dv of one key tile over the rows of its window, or (sink jobs) over one chunk of the rows beyond it.
+template <int DP>
+__global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16* Ks = reinterpret_cast<bf16*>(smem);
+  bf16* Vs = Ks + Tile<DP>::elems;
+  bf16* Qs = Vs + Tile<DP>::elems;
+  bf16* Os = Qs + 2 * Tile<DP>::elems;
+  __shared__ float slse[2][T], sdel[2][T];
+  __shared__ int spos[2][T];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
+  const int ktiles = (a.Nk + T - 1) / T;
+  const int nsink = a.nchunk > 0 ? (a.sinks + T - 1) / T : 0;
+  const int jobs = ktiles + nsink * a.nchunk;
+  const int job = blockIdx.x % jobs, bh = blockIdx.x / jobs, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
+  const bool sink_job = job >= ktiles;
+  const int kt = sink_job ? (job - ktiles) / a.nchunk : job;
+  const int chunk = sink_job ? (job - ktiles) % a.nchunk : -1;
+  const int q0 = win_q0(a, b);
+  const int j0 = kt * T, j1 = min(a.Nk, j0 + T) - 1;
+  const bool split = kt < nsink;
+  const int pl = sink_job ? j1 + a.left + 1 : max(0, j0 - a.right);
+  const int ph = sink_job || (j0 < a.sinks && !split) ? a.Nk - 1 : min(a.Nk - 1, j1 + a.left);
+  const int il = max(pl - q0, 0), ih = min(ph - q0, a.Nq - 1);
+  int fl = il * a.G, fh = (ih + 1) * a.G;
+  if (ih < il) fl = fh = 0;
+  if (sink_job) {
+    fl = max(fl, chunk * a.chunk_tiles * T);
+    fh = min(fh, (chunk + 1) * a.chunk_tiles * T);
+  }
+  const Src q = source(a.q, a.qb, a.qn, a.qh, a.D, b, hkv * a.G);
+  const Src g_ = source(a.d_out, (long long)a.Nq * a.H * a.Dv, (long long)a.H * a.Dv, a.Dv, a.Dv, b, hkv * a.G);
+  const Src k = source(a.k, a.kb, a.kn, a.kh, a.D, b, hkv), v = source(a.v, a.vb, a.vn, a.vh, a.Dv, b, hkv);
+  bool alive[2];
+  int plo[2], phi[2];                                   // positions that see this thread's keys
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = j0 + 16 * warp + (lane >> 2) + 8 * i;
+    alive[i] = j <= j1 && win_alive(a, b, j);
+    plo[i] = j - a.right;
+    phi[i] = j < a.sinks ? 0x7fffffff : j + a.left;
+  }
+  const int ka = j0 + 16 * warp, kb = min(ka + 15, j1);   // keys of the warp
+  const int ntile = __syncthreads_or(alive[0] || alive[1]) && fh > fl ? (fh - fl + T - 1) / T : 0;
+  auto load = [&](int t) {
+    const int st = t & 1, f0 = fl + t * T;
+    auto rows = [&](const Src& s) {
+      return [&, f0](int r) -> const bf16* {
+        const int f = f0 + r, i = f / a.G;
+        return f < fh && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
+      };
+    };
+    load_tile<DP>(Qs + st * Tile<DP>::elems, q, rows(q));
+    load_tile<DP>(Os + st * Tile<DP>::elems, g_, rows(g_));
+    cp_async_commit();
+    if (threadIdx.x < T) {
+      const int f = f0 + threadIdx.x, i = f / a.G;
+      float x = -INFINITY, d = 0.f;
+      if (f < fh && win_alive(a, b, q0 + i)) {
+        const long long o = ((long long)b * a.H + hkv * a.G + (f - i * a.G)) * a.Nq + i;
+        x = a.lse[o];
+        d = a.delta[o];
+      }
+      slse[st][threadIdx.x] = x == -INFINITY ? INFINITY : x * kLog2e;
+      sdel[st][threadIdx.x] = d;
+      spos[st][threadIdx.x] = q0 + i;
+    }
+  };
+  const int kd = (a.D + 15) / 16, kv = (a.Dv + 15) / 16;
+  float dk[DP / 8][4], dv[DP / 8][4];
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dk[n][e] = dv[n][e] = 0.f;
+  const float sc = a.scale * kLog2e;
+  if (ntile > 0) {
+    auto keyed = [&](const Src& s) {
+      return [&](int r) -> const bf16* { return j0 + r <= j1 && win_alive(a, b, j0 + r) ? s.p + (j0 + r) * s.sn : nullptr; };
+    };
+    load_tile<DP>(Ks, k, keyed(k));
+    load_tile<DP>(Vs, v, keyed(v));
+    load(0);
+  }
+  for (int t = 0; t < ntile; ++t) {
+    const int st = t & 1;
+    if (t + 1 < ntile) {
+      load(t + 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncthreads();
+    const uint32_t qs = smem_u32(Qs + st * Tile<DP>::elems), os = smem_u32(Os + st * Tile<DP>::elems);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (fl + t * T + 16 * g >= fh) break;
+      const int pa = spos[st][16 * g], pb = spos[st][16 * g + 15];
+      if (kb < ka || pb < ka - a.right || (pa > kb + a.left && ka >= a.sinks)) continue;
+      const bool edge = pa < kb - a.right || pb > ka + a.left;
+      float s[2][4], dp[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[h][e] = dp[h][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        uint32_t af[4], bf[4];
+        if (kk < kd) {
+          ldsm4(af, a_addr<DP>(smem_u32(Ks), 16 * warp, 16 * kk, lane));
+          ldsm4(bf, b_addr<DP>(qs, 16 * g, 16 * kk, lane));
+          mma(s[0], af, bf[0], bf[1]);
+          mma(s[1], af, bf[2], bf[3]);
+        }
+        if (kk < kv) {
+          ldsm4(af, a_addr<DP>(smem_u32(Vs), 16 * warp, 16 * kk, lane));
+          ldsm4(bf, b_addr<DP>(os, 16 * g, 16 * kk, lane));
+          mma(dp[0], af, bf[0], bf[1]);
+          mma(dp[1], af, bf[2], bf[3]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * g + 8 * h + col2 + (e & 1), i = e >> 1;
+          float p = ex2_approx(fmaf(s[h][e], sc, -slse[st][r]));
+          if (edge) {
+            const int pos = spos[st][r];
+            if (pos < plo[i] || pos > phi[i]) p = 0.f;
+          }
+          s[h][e] = p;
+          dp[h][e] = p * (dp[h][e] - sdel[st][r]);
+        }
+      const uint32_t pf[4] = {pack(s[0][0], s[0][1]), pack(s[0][2], s[0][3]), pack(s[1][0], s[1][1]), pack(s[1][2], s[1][3])};
+      const uint32_t df[4] = {pack(dp[0][0], dp[0][1]), pack(dp[0][2], dp[0][3]), pack(dp[1][0], dp[1][1]), pack(dp[1][2], dp[1][3])};
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n) {
+        uint32_t bf[4];
+        if (n < kv) {
+          ldsm4t(bf, bt_addr<DP>(os, 16 * g, 16 * n, lane));
+          mma(dv[2 * n], pf, bf[0], bf[1]);
+          mma(dv[2 * n + 1], pf, bf[2], bf[3]);
+        }
+        if (n < kd) {
+          ldsm4t(bf, bt_addr<DP>(qs, 16 * g, 16 * n, lane));
+          mma(dk[2 * n], df, bf[0], bf[1]);
+          mma(dk[2 * n + 1], df, bf[2], bf[3]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (split) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = j0 + 16 * warp + (lane >> 2) + 8 * i;
+      if (j > j1 || j >= a.sinks) continue;
+      float* o = a.part + (((long long)bh * (a.nchunk + 1) + chunk + 1) * a.sinks + j) * (a.D + a.Dv);
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int d = 8 * n + col2 + e;
+          if (d < a.D) o[d] = alive[i] ? dk[n][2 * i + e] : 0.f;
+          if (d < a.Dv) o[a.D + d] = alive[i] ? dv[n][2 * i + e] : 0.f;
+        }
+    }
+    if (sink_job) return;
+  }
+  auto at = [&](void* base, int width, int i, bool& keep) -> bf16* {
+    const int j = j0 + 16 * warp + (lane >> 2) + 8 * i;
+    keep = alive[i];
+    return j <= j1 && !(split && j < a.sinks) ? static_cast<bf16*>(base) + (((long long)b * a.Nk + j) * a.Hkv + hkv) * width : nullptr;
+  };
+  store_rows<DP>(dk, a.D, a.d_k, a.scale, lane, [&](int i, bool& keep) { return at(a.d_k, a.D, i, keep); });
+  store_rows<DP>(dv, a.Dv, a.d_v, 1.f, lane, [&](int i, bool& keep) { return at(a.d_v, a.Dv, i, keep); });
+}
+
+template <int DP>
+cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
+  const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_fwd_mma_kernel<DP>));
+  if (e != cudaSuccess) return e;
+  win_fwd_mma_kernel<DP><<<(unsigned)grid, kThreads, 5 * Tile<DP>::elems * sizeof(bf16), s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int DP>
+cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
+  const size_t smem = 6 * Tile<DP>::elems * sizeof(bf16);
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP>));
+  if (e != cudaSuccess) return e;
+  e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP>));
+  if (e != cudaSuccess) return e;
+  const long long gq = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
+  win_bwd_q_mma_kernel<DP><<<(unsigned)gq, kThreads, smem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int nsink = a.nchunk > 0 ? (a.sinks + T - 1) / T : 0;
+  const long long gk = (long long)a.B * a.Hkv * ((a.Nk + T - 1) / T + (long long)nsink * a.nchunk);
+  win_bwd_k_mma_kernel<DP><<<(unsigned)gk, kThreads, smem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return a.nchunk > 0 ? launch_win_sink_reduce(a, 0, s) : cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_win_fwd_mma(const WinArgs& a, cudaStream_t s) {
+  const int w = a.D > a.Dv ? a.D : a.Dv;
+  return w <= 16 ? fwd<16>(a, s) : (w <= 32 ? fwd<32>(a, s) : (w <= 64 ? fwd<64>(a, s) : fwd<128>(a, s)));
+}
+cudaError_t launch_win_bwd_mma(const WinArgs& a, cudaStream_t s) {
+  const int w = a.D > a.Dv ? a.D : a.Dv;
+  return w <= 16 ? bwd<16>(a, s) : (w <= 32 ? bwd<32>(a, s) : (w <= 64 ? bwd<64>(a, s) : bwd<128>(a, s)));
+}
+
+}  // namespace fipa

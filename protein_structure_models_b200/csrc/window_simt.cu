@@ -1,4 +1,5 @@
-// window_simt.cu -- window attention with sinks on the CUDA cores (window.h has
+// window_simt.cu -- window attention with sinks on float32 tensors, on the CUDA
+// cores, whose products keep every bit of the operands (window.h has
 // the visibility rule and the row / column numbering).
 //
 // Forward, one pass over a row tile's columns: m the running row maximum, l the
@@ -412,24 +413,24 @@ cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
   const long long gk = (long long)a.B * a.Hkv * ((a.Nk + T - 1) / T + (long long)nsink * a.nchunk);
   win_bwd_k_simt_kernel<E, NC><<<(unsigned)gk, kThreads, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.nchunk > 0) {
-    win_sink_reduce_kernel<E><<<(unsigned)(a.B * a.Hkv * a.sinks), 128, 0, s>>>(a);
-    e = cudaGetLastError();
-  }
-  return e;
+  return a.nchunk > 0 ? launch_win_sink_reduce(a, sizeof(E) == 4, s) : cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_win_fwd_simt(const WinArgs& a, int f32, cudaStream_t s) {
-  const int nc = (a.Dv + 15) / 16;
-  if (f32) return nc <= 2 ? fwd<float, 2>(a, s) : (nc <= 4 ? fwd<float, 4>(a, s) : fwd<float, 8>(a, s));
-  return nc <= 2 ? fwd<__nv_bfloat16, 2>(a, s) : (nc <= 4 ? fwd<__nv_bfloat16, 4>(a, s) : fwd<__nv_bfloat16, 8>(a, s));
+cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s) {
+  const unsigned grid = (unsigned)(a.B * a.Hkv * a.sinks);
+  if (f32) win_sink_reduce_kernel<float><<<grid, 128, 0, s>>>(a);
+  else win_sink_reduce_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError();
 }
-cudaError_t launch_win_bwd_simt(const WinArgs& a, int f32, cudaStream_t s) {
+cudaError_t launch_win_fwd_simt(const WinArgs& a, cudaStream_t s) {
+  const int nc = (a.Dv + 15) / 16;
+  return nc <= 2 ? fwd<float, 2>(a, s) : (nc <= 4 ? fwd<float, 4>(a, s) : fwd<float, 8>(a, s));
+}
+cudaError_t launch_win_bwd_simt(const WinArgs& a, cudaStream_t s) {
   const int nc = ((a.D > a.Dv ? a.D : a.Dv) + 15) / 16;
-  if (f32) return nc <= 2 ? bwd<float, 2>(a, s) : (nc <= 4 ? bwd<float, 4>(a, s) : bwd<float, 8>(a, s));
-  return nc <= 2 ? bwd<__nv_bfloat16, 2>(a, s) : (nc <= 4 ? bwd<__nv_bfloat16, 4>(a, s) : bwd<__nv_bfloat16, 8>(a, s));
+  return nc <= 2 ? bwd<float, 2>(a, s) : (nc <= 4 ? bwd<float, 4>(a, s) : bwd<float, 8>(a, s));
 }
 
 }  // namespace fipa
