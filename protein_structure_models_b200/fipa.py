@@ -162,12 +162,41 @@ def load_library():
     return lib
 
 
+_FLOATS = (torch.float32, torch.bfloat16)
+_BYTES = (torch.bool, torch.uint8)
+
+
 def make_dims(**kw) -> FipaDims:
     return FipaDims(*[int(kw[f]) for f in DIM_FIELDS])
 
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    """Address of `stream`, or of the device's current stream, without building a Stream object."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
+class _OnDevice:
+    """torch.cuda.device(dev), at no cost when dev is current already."""
+    __slots__ = ("guard",)
+
+    def __init__(self, dev):
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 INPUT_KEYS = ("q", "k", "v", "q_points", "k_points", "v_points", "rotation", "translation",
@@ -386,24 +415,26 @@ class Fipa:
         dev, td = q.device, self.torch_dtype
         if dev.type != "cuda" or dev.index != self.device:
             raise ValueError(f"q: need a tensor on cuda:{self.device}")
+        heads, shapes = [], []
         for name, t in (("q", q), ("k", k), ("v", v)):
-            if t.dim() != 4 or t.dtype != td or t.device != dev or (t.shape[3] > 1 and t.stride(3) != 1):
+            sh, st = t.shape, t.stride()
+            if len(sh) != 4 or t.dtype != td or t.device != dev or (st[3] != 1 and sh[3] > 1):
                 raise ValueError(f"{name}: need a {td} tensor [B, N, heads, width] on {dev}, its width contiguous")
-        B, Nq, H, D = q.shape
-        _, Nk, Hkv, Dv = v.shape
-        if k.shape != (B, Nk, Hkv, D) or v.shape[0] != B:
+            heads.append(FipaHeads(t.data_ptr(), st[0], st[1], st[2]))
+            shapes.append(sh)
+        B, Nq, H, D = shapes[0]
+        Bv, Nk, Hkv, Dv = shapes[2]
+        if shapes[1] != (B, Nk, Hkv, D) or Bv != B:
             raise ValueError("q [B,Nq,H,D], k [B,Nk,Hkv,D], v [B,Nk,Hkv,Dv] do not fit together")
-        if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.device != dev
+        if mask is not None and (mask.dtype not in _BYTES or mask.device != dev
                                  or mask.shape != (B, Nk) or not mask.is_contiguous()):
             raise ValueError(f"mask: need a contiguous bool/uint8 tensor [B, Nk] on {dev}")
         if q_start is not None and (q_start.dtype != torch.int32 or q_start.device != dev
                                     or q_start.shape != (B,) or not q_start.is_contiguous()):
             raise ValueError(f"q_start: need a contiguous int32 tensor [B] on {dev}")
-        left, right = (-1 if w is None else int(w) for w in window)
-        big = 0x7fffffff
-        w = FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, min(left, big), min(right, big), int(sinks),
-                       D ** -0.5 if scale is None and D > 0 else float(scale or 0.0))
-        return w, [FipaHeads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)) for t in (q, k, v)]
+        left, right = (-1 if w is None else min(int(w), 0x7fffffff) for w in window)
+        return FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, left, right, int(sinks),
+                          D ** -0.5 if scale is None and D > 0 else float(scale or 0.0)), heads
 
     def window_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: tuple, sinks: int = 0,
                          mask: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
@@ -424,10 +455,9 @@ class Fipa:
         else:
             self._check_buffers(out, {"out": ((w.B, w.Nq, w.H, w.Dv), q.dtype),
                                       "lse": ((w.B, w.H, w.Nq), torch.float32)}, q.device, ("out",))
-        s = stream if stream is not None else torch.cuda.current_stream(q.device)
-        self._check(self.lib.fipa_window_attention(
-            self.handle, *[ctypes.byref(x) for x in hd], _ptr(mask), _ptr(q_start), ctypes.byref(w), _ptr(out["out"]),
-            _ptr(out.get("lse")), ctypes.c_void_p(s.cuda_stream)))
+        self._check(self.lib.fipa_window_attention(self.handle, hd[0], hd[1], hd[2], _addr(mask), _addr(q_start), w,
+                                                   out["out"].data_ptr(), _addr(out.get("lse")),
+                                                   _raw_stream(stream, self.device)))
         return out
 
     @staticmethod
@@ -463,11 +493,10 @@ class Fipa:
             workspace = torch.empty(self._window_workspace(w), dtype=torch.uint8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
         self._check(self.lib.fipa_window_attention_backward(
-            self.handle, *[ctypes.byref(x) for x in hd], _ptr(mask), _ptr(q_start), ctypes.byref(w), _ptr(out),
-            _ptr(lse), _ptr(d_out), _ptr(grads["q"]), _ptr(grads["k"]), _ptr(grads["v"]), _ptr(workspace),
-            ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(s.cuda_stream)))
+            self.handle, hd[0], hd[1], hd[2], _addr(mask), _addr(q_start), w, out.data_ptr(), lse.data_ptr(),
+            d_out.data_ptr(), grads["q"].data_ptr(), grads["k"].data_ptr(), grads["v"].data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _raw_stream(stream, self.device)))
         return grads
 
     def _window_workspace(self, w) -> int:
@@ -582,11 +611,10 @@ def knn_distogram(translation: torch.Tensor, mask: torch.Tensor, k: int, edges: 
 
 
 def _need(name, t, shape, dtypes, dev):
-    if t.shape != tuple(shape) or t.dtype not in dtypes or t.device != dev or not t.is_contiguous():
+    if t.shape != shape or t.dtype not in dtypes or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous tensor {tuple(shape)} of {dtypes} on {dev}")
 
 
-_FLOATS = (torch.float32, torch.bfloat16)
 
 
 def _code(t: torch.Tensor) -> int:
@@ -606,7 +634,7 @@ def _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtyp
     if gate is not None:
         _need("gate", gate, s.shape, (tb,), dev)
     if mask is not None:
-        _need("mask", mask, s.shape[:-1], (torch.bool, torch.uint8), dev)
+        _need("mask", mask, s.shape[:-1], _BYTES, dev)
     par = dict(zip(NORM_PARAMS, (res_scale, *(post or (None, None)), *(pre or (None, None)))))
     for name, t in par.items():
         if t is not None:
@@ -641,7 +669,7 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
     lib = load_library()
     d, i, tb, _ = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
     dev = s.device
-    with torch.cuda.device(dev):
+    with _OnDevice(dev):
         want = {}
         if u is not None:
             want["r"] = (s.shape, s.dtype)
@@ -657,9 +685,9 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
                     _need(k, out[k], sh, (dt,), dev)
                 elif k in want:
                     raise ValueError(f"{k}: buffer missing")
-        st = stream if stream is not None else torch.cuda.current_stream(dev)
-        _ok(lib.fipa_norm_residual(ctypes.byref(d), ctypes.byref(i), _ptr(out.get("r")), _ptr(out.get("x")),
-                                   _ptr(out.get("stats")), ctypes.c_void_p(st.cuda_stream)), "fipa_norm_residual")
+        st = _raw_stream(stream, dev.index)
+        _ok(lib.fipa_norm_residual(d, i, _addr(out.get("r")), _addr(out.get("x")),
+                                   _addr(out.get("stats")), st), "fipa_norm_residual")
     return out
 
 
@@ -683,7 +711,7 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
     if d_x is not None:
         _need("d_x", d_x, s.shape, (tb,), dev)
     have = {"s": s, "u": u, "gate": gate, **par}
-    with torch.cuda.device(dev):
+    with _OnDevice(dev):
         if grads is None:
             grads = {k: None if t is None else torch.empty_like(t) for k, t in have.items()}
         else:
@@ -700,10 +728,10 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
         g = FipaNormGrads(*[None if grads.get(f) is None else grads[f].data_ptr() for f, _ in FipaNormGrads._fields_])
-        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        st = _raw_stream(stream, dev.index)
         _ok(lib.fipa_norm_residual_backward(
-            ctypes.byref(d), ctypes.byref(i), _ptr(stats), _ptr(d_r), _ptr(d_x), ctypes.byref(g), _ptr(workspace),
-            ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(st.cuda_stream)),
+            d, i, _addr(stats), _addr(d_r), _addr(d_x), g, _addr(workspace),
+            workspace.numel() * workspace.element_size(), st),
             "fipa_norm_residual_backward")
     return grads
 
@@ -719,14 +747,14 @@ def embedding(idx: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: O
     _need("table", table, table.shape, _FLOATS, dev)
     _need("idx", idx, idx.shape, (torch.int32,), dev)
     V, C = table.shape
-    with torch.cuda.device(dev):
+    with _OnDevice(dev):
         if out is None:
             out = {"out": torch.empty((*idx.shape, C), dtype=table.dtype, device=dev)}
         else:
             _need("out", out["out"], (*idx.shape, C), (table.dtype,), dev)
-        st = stream if stream is not None else torch.cuda.current_stream(dev)
-        _ok(lib.fipa_embedding(_code(table), _ptr(idx), _ptr(table), idx.numel(), V, C, float(scale), _ptr(out["out"]),
-                               ctypes.c_void_p(st.cuda_stream)), "fipa_embedding")
+        st = _raw_stream(stream, dev.index)
+        _ok(lib.fipa_embedding(_code(table), _addr(idx), _addr(table), idx.numel(), V, C, float(scale), _addr(out["out"]),
+                               st), "fipa_embedding")
     return out
 
 
@@ -749,7 +777,7 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
     C = d_out.shape[-1]
     _need("d_out", d_out, d_out.shape, _FLOATS, dev)
     _need("idx", idx, d_out.shape[:-1], (torch.int32,), dev)
-    with torch.cuda.device(dev):
+    with _OnDevice(dev):
         if grads is None:
             grads = {"table": torch.empty((V, C), dtype=torch.float32, device=dev)}
         else:
@@ -758,10 +786,10 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
             workspace = torch.empty(embedding_backward_workspace_size(idx.numel(), V, C), dtype=torch.uint8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        st = _raw_stream(stream, dev.index)
         _ok(lib.fipa_embedding_backward(
-            _code(d_out), _ptr(idx), _ptr(d_out), idx.numel(), V, C, float(scale), _ptr(grads["table"]), _ptr(workspace),
-            ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.c_void_p(st.cuda_stream)),
+            _code(d_out), _addr(idx), _addr(d_out), idx.numel(), V, C, float(scale), _addr(grads["table"]), _addr(workspace),
+            workspace.numel() * workspace.element_size(), st),
             "fipa_embedding_backward")
     return grads
 
