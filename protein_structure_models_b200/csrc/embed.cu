@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const int* __restrict__ 
                                                         long long rows, int V, int C, int pieces, float scale) {
   const long long n = rows * pieces, step = (long long)gridDim.x * blockDim.x;
   for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += step) {
-    const long long t = e / pieces;
+    const long long t = n < (1ll << 31) ? (long long)((unsigned)e / (unsigned)pieces) : e / pieces;
     const int p = (int)(e - t * pieces), v = __ldg(idx + t);
     const bool on = v >= 0 && v < V;
     if (VEC) {
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const int* __restrict__ 
 // ---------------------------------------------------------------- stable sort
 // Digit counts of every block of 2048 elements: hist[digit][block].
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __restrict__ key, int n, int V, int first, int shift,
-                                                                  int mask, int* __restrict__ hist) {
+                                                                  int mask, int* __restrict__ hist, uint8_t* __restrict__ mark) {
   __shared__ int cnt[kDigits];
   cnt[threadIdx.x] = 0;
   __syncthreads();
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __r
     if (i < n) {
       int v = key[i];
       if (first && (v < 0 || v >= V)) v = V;
+      if (first && v < V) mark[v] = 1;                        // every writer writes the same
       atomicAdd(&cnt[(v >> shift) & mask], 1);
     }
   }
@@ -199,15 +200,82 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const int* __re
   }
 }
 
+// The whole sort of at most 2048 tokens in one CTA: the same passes, all of
+// whose counts fit in shared memory (8 or more launches would cost more than
+// the work).
+__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int* __restrict__ idx, int n, int V, int passes, int bits,
+                                                                  int* __restrict__ okey, int* __restrict__ otok) {
+  __shared__ int key[2][kSortBlock], tok[2][kSortBlock], cnt[8][kDigits], ws[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mask = (1 << bits) - 1;
+  for (int i = threadIdx.x; i < n; i += kSortThreads) {
+    const int v = idx[i];
+    key[0][i] = v < 0 || v >= V ? V : v;
+    tok[0][i] = i;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int from = pass & 1, shift = pass * bits;
+    for (int w = 0; w < 8; ++w) cnt[w][threadIdx.x] = 0;
+    __syncthreads();
+    int v[kSortItems], tk[kSortItems], rank[kSortItems];
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      const int i = warp * 256 + k * 32 + lane;
+      v[k] = i < n ? key[from][i] : -1;
+      tk[k] = i < n ? tok[from][i] : 0;
+      const int d = v[k] >= 0 ? (v[k] >> shift) & mask : kDigits;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      const int below = __popc(same & ((1u << lane) - 1u));
+      int c = 0;
+      if (v[k] >= 0) c = cnt[warp][d];
+      rank[k] = c + below;
+      __syncwarp();
+      if (v[k] >= 0 && below == 0) cnt[warp][d] = c + __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // digit d of warp w starts behind all smaller digits and the warps before
+    int tot = 0;
+    for (int w = 0; w < 8; ++w) tot += cnt[w][threadIdx.x];
+    int y = tot;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    if (lane == 31) ws[warp] = y;
+    __syncthreads();
+    int at = y - tot;
+    for (int w = 0; w < warp; ++w) at += ws[w];
+    for (int w = 0; w < 8; ++w) {
+      const int c = cnt[w][threadIdx.x];
+      cnt[w][threadIdx.x] = at;
+      at += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortItems; ++k) {
+      if (v[k] < 0) continue;
+      const int p = cnt[warp][(v[k] >> shift) & mask] + rank[k];
+      key[from ^ 1][p] = v[k];
+      tok[from ^ 1][p] = tk[k];
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += kSortThreads) {
+    okey[i] = key[passes & 1][i];
+    otok[i] = tok[passes & 1][i];
+  }
+}
+
 // ---------------------------------------------------------------- run sums
-// A group of `tpc` threads adds one chunk of the sorted list for a slab of
-// columns.  part[chunk][0]: the run that came from the chunk before; [1]: the
-// run that starts here and goes on.
+// A group of `tpc` threads adds one chunk of L (a multiple of 8) tokens of the
+// sorted list for a slab of columns, eight rows of dout in flight a thread.
+// part[chunk][0]: the run that came from the chunk before; [1]: the run that
+// starts here and goes on.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const int* __restrict__ key, const int* __restrict__ tok, const T* __restrict__ dout,
                                                         int n, int V, int C, int L, int tpc, int slabs, float scale,
                                                         float* __restrict__ dtable, float* __restrict__ part, int nchunk) {
-  constexpr int N = VEC ? Vec<T>::n : 1;
+  constexpr int N = VEC ? Vec<T>::n : 1, U = 8;
   const int gpb = blockDim.x / tpc;
   const long long unit = (long long)blockIdx.x * gpb + threadIdx.x / tpc;
   const int chunk = (int)(unit / slabs), slab = (int)(unit - (long long)chunk * slabs);
@@ -220,29 +288,40 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const int* __restrict__ 
   int cur = key[b];
   bool open = b > 0 && key[b - 1] == cur;                     // the run began in an earlier chunk
   auto flush = [&](float* dst, float f) {
+    if (VEC) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) dst[k] = acc[k] * f;
-  };
-  for (int i0 = b; i0 < e; i0 += 4) {
-    int kk[4], tt[4];
-    float x[4][N];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      kk[j] = i0 + j < e ? key[i0 + j] : V;
-      tt[j] = i0 + j < e ? tok[i0 + j] : 0;
+      for (int k = 0; k < N; k += 4)
+        *reinterpret_cast<float4*>(dst + k) = make_float4(acc[k] * f, acc[k + 1] * f, acc[k + 2] * f, acc[k + 3] * f);
+    } else {
+      dst[0] = acc[0] * f;
     }
+  };
+  for (int i0 = b; i0 < e; i0 += U) {
+    int kk[U], tt[U];
+    if (i0 + U <= e) {                                        // the lists' parts are 32-byte aligned
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < U; j += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(key + i0 + j), y = *reinterpret_cast<const int4*>(tok + i0 + j);
+        kk[j] = x.x; kk[j + 1] = x.y; kk[j + 2] = x.z; kk[j + 3] = x.w;
+        tt[j] = y.x; tt[j + 1] = y.y; tt[j + 2] = y.z; tt[j + 3] = y.w;
+      }
+    } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) x[j][k] = 0.f;
-      if (kk[j] < V) {
-        const T* p = dout + (long long)tt[j] * C + c;
-        if (VEC) unpack<T>(__ldg(reinterpret_cast<const uint4*>(p)), x[j]);
-        else x[j][0] = cvt(*p);
+      for (int j = 0; j < U; ++j) {
+        kk[j] = i0 + j < e ? key[i0 + j] : V;
+        tt[j] = i0 + j < e ? tok[i0 + j] : 0;
       }
     }
+    uint4 raw[U];
+    T one[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < U; ++j) {
+      const T* p = dout + (long long)tt[j] * C + c;
+      if (VEC) raw[j] = kk[j] < V ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+      else one[j] = kk[j] < V ? *p : T(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
       if (i0 + j >= e) break;
       if (kk[j] != cur) {
         if (cur < V) {
@@ -254,8 +333,11 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const int* __restrict__ 
         cur = kk[j];
         open = false;
       }
+      float x[N];
+      if (VEC) unpack<T>(raw[j], x);
+      else x[0] = cvt(one[j]);
 #pragma unroll
-      for (int k = 0; k < N; ++k) acc[k] += x[j][k];
+      for (int k = 0; k < N; ++k) acc[k] += x[k];
     }
   }
   if (cur >= V) return;
@@ -274,24 +356,54 @@ __device__ __forceinline__ int lower_bound(const int* key, int n, int v) {
   }
   return lo;
 }
-// Rows without a token are zero; rows whose run crosses chunks are the pieces' sum.
-__global__ void __launch_bounds__(256) embed_rows_kernel(const int* __restrict__ key, int n, int V, int C, int L, float scale,
-                                                         const float* __restrict__ part, float* __restrict__ dtable) {
-  const int lane = threadIdx.x & 31;
-  const long long v = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (v >= V) return;
-  const int b = lower_bound(key, n, (int)v);
-  float* o = dtable + v * C;
-  if (b >= n || key[b] != v) {
-    for (int c = lane; c < C; c += 32) o[c] = 0.f;
+// CTAs [0, ncross): the run that starts in chunk q and crosses into the next is
+// the sum of its pieces, taken by 16 warps in 16 neighbouring stretches that are
+// added in order.  CTAs beyond: rows without a token are zero (marked by the
+// sort's first pass, or searched for in a short list).
+__global__ void __launch_bounds__(512) embed_join_kernel(const int* __restrict__ key, int n, int V, int C, int L, int nchunk, int slabs,
+                                                         int ncross, float scale, const float* __restrict__ part,
+                                                         const uint8_t* __restrict__ mark, float* __restrict__ dtable) {
+  __shared__ float red[16][32];
+  __shared__ int shared_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int)blockIdx.x >= ncross) {
+    const long long step = (long long)(gridDim.x - ncross) * 16;
+    for (long long v = (long long)(blockIdx.x - ncross) * 16 + warp; v < V; v += step) {
+      bool used;
+      if (mark != nullptr) {
+        used = mark[v] != 0;
+      } else {
+        const int b = lower_bound(key, n, (int)v);
+        used = b < n && key[b] == (int)v;
+      }
+      if (used) continue;
+      float* o = dtable + v * C;
+      if ((C & 3) == 0 && (reinterpret_cast<uintptr_t>(dtable) & 15) == 0) {
+        for (int c = lane; c < C / 4; c += 32) reinterpret_cast<float4*>(o)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+        for (int c = lane; c < C; c += 32) o[c] = 0.f;
+      }
+    }
     return;
   }
-  const int first = b / L, e = lower_bound(key, n, (int)v + 1), last = (e - 1) / L;
-  if (first == last) return;
-  for (int c = lane; c < C; c += 32) {
-    float x = part[((size_t)first * 2 + 1) * C + c];
-    for (int q = first + 1; q <= last; ++q) x += part[((size_t)q * 2) * C + c];
-    o[c] = x * scale;
+  const int q = blockIdx.x / slabs, c = (blockIdx.x % slabs) * 32 + lane, e = (q + 1) * L;
+  if (e >= n) return;
+  const int cur = key[e];
+  if (cur >= V || key[e - 1] != cur || (q > 0 && key[q * L - 1] == cur)) return;     // no run starts here and goes on
+  if (threadIdx.x == 0) shared_last = (lower_bound(key + e, n - e, cur + 1) + e - 1) / L;
+  __syncthreads();
+  const int last = shared_last, m = last - q + 1, per = (m + 15) / 16;
+  float x = 0.f;
+  if (c < C) {
+    const int lo = q + warp * per, hi = min(lo + per, last + 1);
+#pragma unroll 8
+    for (int k = lo; k < hi; ++k) x += part[((size_t)k * 2 + (k == q ? 1 : 0)) * C + c];
+  }
+  red[warp][lane] = x;
+  __syncthreads();
+  if (warp == 0 && c < C) {
+    for (int w = 1; w < 16; ++w) x += red[w][lane];
+    dtable[(size_t)cur * C + c] = x * scale;
   }
 }
 
@@ -300,7 +412,7 @@ bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 // Workspace of the gradient: two copies of (key, token), digit counts, pieces.
 struct EmbedPlan {
   int nblk, passes, bits, L, nchunk;
-  size_t off_key[2], off_tok[2], off_hist, off_total, off_part, total;
+  size_t off_key[2], off_tok[2], off_hist, off_total, off_mark, off_part, total;
 };
 EmbedPlan embed_plan(long long T, int V, int C) {
   EmbedPlan p;
@@ -309,8 +421,10 @@ EmbedPlan embed_plan(long long T, int V, int C) {
   p.passes = (need + 7) / 8;
   p.bits = (need + p.passes - 1) / p.passes;
   p.nblk = (int)((T + kSortBlock - 1) / kSortBlock);
-  p.L = 32;
-  while (p.L < 512 && (T + p.L - 1) / p.L > 148 * 32) p.L *= 2;
+  // Chunks short enough for a full GPU of threads (16-byte pieces, 2048 an SM),
+  // long enough that the pieces of runs stay a small part of the traffic.
+  p.L = 16;
+  while (p.L < 256 && (T / p.L) * ((C + 7) / 8) > 148 * 2048) p.L *= 2;
   p.nchunk = (int)((T + p.L - 1) / p.L);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -324,6 +438,7 @@ EmbedPlan embed_plan(long long T, int V, int C) {
   }
   p.off_hist = take((size_t)p.nblk * kDigits * 4);
   p.off_total = take(kDigits * 4);
+  p.off_mark = take((size_t)V);
   p.off_part = take((size_t)p.nchunk * 2 * C * 4);
   p.total = o;
   return p;
@@ -415,23 +530,37 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
   const int* key = idx;
   const int* tok = nullptr;
   int at = 0;
-  if (n > 0) {
+  const uint8_t* mark = nullptr;
+  if (n > 0 && n <= kSortBlock) {
+    int* okey = reinterpret_cast<int*>(ws + p.off_key[0]);
+    int* otok = reinterpret_cast<int*>(ws + p.off_tok[0]);
+    sort_small_kernel<<<1, kSortThreads, 0, s>>>(idx, n, V, p.passes, p.bits, okey, otok);
+    key = okey;
+  } else if (n > 0) {
     const int mask = (1 << p.bits) - 1;
+    uint8_t* mk = ws + p.off_mark;
+    if (cudaMemsetAsync(mk, 0, (size_t)V, s) != cudaSuccess) return FIPA_ERR_CUDA;
+    mark = mk;
     for (int k = 0; k < p.passes; ++k) {
       at = k & 1;
       int* okey = reinterpret_cast<int*>(ws + p.off_key[at]);
       int* otok = reinterpret_cast<int*>(ws + p.off_tok[at]);
-      sort_count_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, n, V, k == 0, k * p.bits, mask, hist);
+      sort_count_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, n, V, k == 0, k * p.bits, mask, hist, mk);
       sort_scan_kernel<<<mask + 1, 256, 0, s>>>(hist, total, p.nblk);
       sort_move_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, tok, n, V, k == 0, k * p.bits, mask, hist, total, p.nblk, okey, otok);
       key = okey;
       tok = otok;
     }
+  }
+  if (n > 0) {
     const cudaError_t e = dtype == FIPA_F32 ? embed_sum<float>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s)
                                             : embed_sum<__nv_bfloat16>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s);
     if (e != cudaSuccess) return FIPA_ERR_CUDA;
   }
-  embed_rows_kernel<<<(unsigned)(((long long)V + 7) / 8), 256, 0, s>>>(key, n, V, C, p.L, (float)scale,
-                                                                      reinterpret_cast<float*>(ws + p.off_part), d_table);
+  const int slabs = (C + 31) / 32;
+  const long long cross = p.nchunk > 1 ? (long long)(p.nchunk - 1) * slabs : 0, fill = ((long long)V + 15) / 16;
+  if (cross > 0x3fffffff) return FIPA_ERR_UNSUPPORTED;
+  embed_join_kernel<<<(unsigned)(cross + (fill < 148 * 8 ? fill : 148 * 8)), 512, 0, s>>>(
+      key, n, V, C, p.L, p.nchunk, slabs, (int)cross, (float)scale, reinterpret_cast<float*>(ws + p.off_part), mark, d_table);
   return cudaGetLastError() == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
 }

@@ -50,36 +50,61 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bf
 template <bool VEC>
 __device__ __forceinline__ int col(int t, int tpr, int e) { return VEC ? t * E + e : t + e * tpr; }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void get_row(const T* p, int t, int tpr, int C, bool on, float (&v)[E]) {
-  if (VEC) {
-    if (on && t * E < C) {
-      if (sizeof(T) == 2) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + t * E));
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void cp_zfill16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_zfill4(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+
+// A thread's part of one tensor's row on its way through shared memory: the
+// thread that copies it is the one that reads it, so the copies of the next two
+// rows need no barrier and no registers.  Elements off 16-byte lines arrive 4
+// bytes at a time; 2-byte ones cannot and are loaded when they are used.
+template <typename T, bool VEC, int BLOCK>
+struct Slot {
+  static constexpr bool kAsync = VEC || sizeof(T) == 4;
+  static constexpr int kBytes = kAsync ? E * (int)sizeof(T) * BLOCK : 0;
+  static __device__ __forceinline__ void fetch(uint8_t* slot, const T* p, int t, int tpr, int C, bool on) {
+    if (VEC) {
+      on = on && t * E < C;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] = __uint_as_float(ww[e] << 16);
-          v[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
-        }
-      } else {
-        const float4 lo = __ldg(reinterpret_cast<const float4*>(p + t * E));
-        const float4 hi = __ldg(reinterpret_cast<const float4*>(p + t * E) + 1);
-        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+      for (int h = 0; h < E * (int)sizeof(T) / 16; ++h)
+        cp_zfill16(slot + (h * BLOCK + threadIdx.x) * 16, on ? p + t * E + h * (16 / (int)sizeof(T)) : p, on);
+    } else if (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = t + e * tpr;
+        cp_zfill4(slot + (e * BLOCK + threadIdx.x) * 4, on && c < C ? p + c : p, on && c < C);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = t + e * tpr;
-      v[e] = on && c < C ? cvt(p[c]) : 0.f;
     }
   }
-}
+  static __device__ __forceinline__ void get(const uint8_t* slot, const T* p, int t, int tpr, int C, bool on, float (&x)[E]) {
+    if (VEC && sizeof(T) == 2) {
+      const uint4 w = *reinterpret_cast<const uint4*>(slot + threadIdx.x * 16);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(ww[e] << 16);
+        x[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
+      }
+    } else if (VEC) {
+      const float4 lo = *reinterpret_cast<const float4*>(slot + threadIdx.x * 16);
+      const float4 hi = *reinterpret_cast<const float4*>(slot + (BLOCK + threadIdx.x) * 16);
+      x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+      x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+    } else if (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = *reinterpret_cast<const float*>(slot + (e * BLOCK + threadIdx.x) * 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = t + e * tpr;
+        x[e] = on && c < C ? cvt(p[c]) : 0.f;
+      }
+    }
+  }
+};
 template <bool VEC, typename T>
 __device__ __forceinline__ void put_row(T* p, int t, int tpr, int C, const float (&v)[E]) {
   if (VEC) {
@@ -105,47 +130,63 @@ __device__ __forceinline__ void put_row(T* p, int t, int tpr, int C, const float
     }
   }
 }
+// Parameters are read anew for every row: they stay in L1, and the registers go to rows in flight.
 template <bool VEC>
 __device__ __forceinline__ void get_param(const float* p, float none, int t, int tpr, int C, float (&v)[E]) {
+  if (p == nullptr) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = col<VEC>(t, tpr, e);
-    v[e] = p == nullptr ? none : (c < C ? __ldg(p + c) : 0.f);
+    for (int e = 0; e < E; ++e) v[e] = none;
+  } else if (VEC) {
+    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+    if (t * E < C) {
+      lo = __ldg(reinterpret_cast<const float4*>(p + t * E));
+      hi = __ldg(reinterpret_cast<const float4*>(p + t * E) + 1);
+    }
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = t + e * tpr < C ? __ldg(p + t + e * tpr) : 0.f;
   }
 }
 
 // Sums of two values over the tpr threads of a row, the same in all of them.
-// Every thread of the CTA calls it (rows of more than a warp meet in shared memory).
-__device__ __forceinline__ float2 row_sum(float2 v, int tpr, float2* red) {
-  const int w = tpr < 32 ? tpr : 32;
-  for (int o = w >> 1; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  if (tpr > 32) {
-    const int nw = tpr >> 5, warp = threadIdx.x >> 5, first = warp / nw * nw;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    v = make_float2(0.f, 0.f);
-    for (int k = 0; k < nw; ++k) {
-      v.x += red[first + k].x;
-      v.y += red[first + k].y;
+// Every thread of the CTA calls it (rows of more than a warp meet in shared
+// memory, in two places in turn, so that one barrier a sum is enough).
+struct RowSum {
+  float2 (*red)[32];
+  int turn;
+  __device__ __forceinline__ float2 operator()(float2 v, int tpr) {
+    const int w = tpr < 32 ? tpr : 32;
+    for (int o = w >> 1; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
+    if (tpr > 32) {
+      const int nw = tpr >> 5, warp = threadIdx.x >> 5, first = warp / nw * nw;
+      if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
+      __syncthreads();
+      v = make_float2(0.f, 0.f);
+      for (int k = 0; k < nw; ++k) {
+        v.x += red[turn][first + k].x;
+        v.y += red[turn][first + k].y;
+      }
+      turn ^= 1;
+    }
+    return v;
   }
-  return v;
-}
+};
 
 // mean and rstd of the row (elements beyond C hold 0 and are left out)
 template <bool VEC>
-__device__ __forceinline__ float2 moments(const float (&z)[E], int t, const NormArgs& a, float2* red) {
+__device__ __forceinline__ float2 moments(const float (&z)[E], int t, const NormArgs& a, RowSum& sum) {
   const float inv = 1.f / (float)a.C;
   float mean = 0.f;
   if (!a.rms) {
     float2 v = make_float2(0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < E; ++e) v.x += z[e];
-    mean = row_sum(v, a.tpr, red).x * inv;
+    mean = sum(v, a.tpr).x * inv;
   }
   float2 v = make_float2(0.f, 0.f);
 #pragma unroll
@@ -153,84 +194,148 @@ __device__ __forceinline__ float2 moments(const float (&z)[E], int t, const Norm
     const float d = col<VEC>(t, a.tpr, e) < a.C ? z[e] - mean : 0.f;
     v.x = fmaf(d, d, v.x);
   }
-  return make_float2(mean, rsqrtf(row_sum(v, a.tpr, red).x * inv + a.eps));
+  return make_float2(mean, rsqrtf(sum(v, a.tpr).x * inv + a.eps));
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
 
-template <typename TS, typename TB, bool VEC>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
-  __shared__ float2 red[32];
-  const int t = threadIdx.x & (a.tpr - 1), rpb = blockDim.x / a.tpr;
-  float ga[E], pw[E], pb[E], qw[E], qb[E];
-  get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
-  get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, pw);
-  get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, pb);
-  get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, qw);
-  get_param<VEC>(a.pre_b, 0.f, t, a.tpr, a.C, qb);
-  for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += (long long)gridDim.x * rpb) {
-    const long long row = r0 + threadIdx.x / a.tpr;
-    const bool in = row < a.rows, live = in && (a.mask == nullptr || a.mask[row] != 0);
+template <typename TS, typename TB, bool VEC, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const NormArgs a) {
+  typedef Slot<TS, VEC, BLOCK> SS;
+  typedef Slot<TB, VEC, BLOCK> SB;
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kStage = SS::kBytes + 2 * SB::kBytes;
+  __shared__ float2 red[2][32];
+  RowSum sum{red, 0};
+  const int t = threadIdx.x & (a.tpr - 1), rpb = BLOCK / a.tpr;
+  const bool branch = a.u != nullptr, gated = a.gate != nullptr;
+  const long long step = (long long)gridDim.x * rpb;
+  const long long first = (long long)blockIdx.x * rpb + threadIdx.x / a.tpr;     // this thread's rows: first, first + step, ...
+  bool soon;                                                                     // whether the row to be fetched next is valid
+  auto look = [&](long long row) { return row < a.rows && (a.mask == nullptr || a.mask[row] != 0); };
+  auto fetch = [&](int k, long long row, bool live) {
+    uint8_t* slot = ring + (k & 1) * kStage;
+    const long long o = (row < a.rows ? row : 0) * a.C;
+    SS::fetch(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, row < a.rows);
+    if (branch) SB::fetch(slot + SS::kBytes, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live);
+    if (gated) SB::fetch(slot + SS::kBytes + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  bool live0 = look(first), live1 = look(first + step);
+  fetch(0, first, live0);
+  fetch(1, first + step, live1);
+  soon = look(first + 2 * step);
+  long long row = first;
+  for (int k = 0; (long long)blockIdx.x * rpb + k * step < a.rows; ++k, row += step) {
+    const bool in = row < a.rows, live = live0;
     const long long o = (in ? row : 0) * a.C;
+    const uint8_t* slot = ring + (k & 1) * kStage;
     float s[E], u[E], g[E];
-    get_row<VEC>(static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, in, s);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    SS::get(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, in, s);
+    if (branch) SB::get(slot + SS::kBytes, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
+    if (gated) SB::get(slot + SS::kBytes + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
     float2 mu = make_float2(0.f, 0.f), mr = mu;
-    if (a.u != nullptr) {
-      get_row<VEC>(static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
-      if (a.gate != nullptr) get_row<VEC>(static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
-      if (a.post_w != nullptr) mu = moments<VEC>(u, t, a, red);
+    if (branch) {
+      if (a.post_w != nullptr) {
+        float w[E], b[E];
+        mu = moments<VEC>(u, t, a, sum);
+        get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
+        get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, b);
+#pragma unroll
+        for (int e = 0; e < E; ++e) u[e] = fmaf((u[e] - mu.x) * mu.y, w[e], b[e]);
+      }
+      float ga[E];
+      get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        float y = u[e];
-        if (a.post_w != nullptr) y = fmaf((u[e] - mu.x) * mu.y, pw[e], pb[e]);
-        if (a.gate != nullptr) y *= sigmoid(g[e]);
-        if (live && col<VEC>(t, a.tpr, e) < a.C) s[e] = fmaf(ga[e], y, s[e]);
+        if (gated) u[e] *= sigmoid(g[e]);
+        if (live && col<VEC>(t, a.tpr, e) < a.C) s[e] = fmaf(ga[e], u[e], s[e]);
       }
       if (in) put_row<VEC>(static_cast<TS*>(a.r) + o, t, a.tpr, a.C, s);
     }
     if (a.pre_w != nullptr) {
-      float z[E];
+      float w[E], b[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) z[e] = live ? s[e] : 0.f;
-      mr = moments<VEC>(z, t, a, red);
+      for (int e = 0; e < E; ++e) s[e] = live ? s[e] : 0.f;
+      mr = moments<VEC>(s, t, a, sum);
+      get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, w);
+      get_param<VEC>(a.pre_b, 0.f, t, a.tpr, a.C, b);
 #pragma unroll
-      for (int e = 0; e < E; ++e) z[e] = live ? fmaf((z[e] - mr.x) * mr.y, qw[e], qb[e]) : 0.f;
-      if (in) put_row<VEC>(static_cast<TB*>(a.x) + o, t, a.tpr, a.C, z);
+      for (int e = 0; e < E; ++e) s[e] = live ? fmaf((s[e] - mr.x) * mr.y, w[e], b[e]) : 0.f;
+      if (in) put_row<VEC>(static_cast<TB*>(a.x) + o, t, a.tpr, a.C, s);
     }
     if (a.stats != nullptr && in && t == 0)
       *reinterpret_cast<float4*>(a.stats + 4 * row) = live ? make_float4(mu.x, mu.y, mr.x, mr.y) : make_float4(0.f, 0.f, 0.f, 0.f);
+    live0 = live1;                            // what was read of this slot has been used: the row after next may take it
+    live1 = soon;
+    fetch(k, row + 2 * step, live1);
+    soon = look(row + 3 * step);
   }
 }
 
-template <typename TS, typename TB, bool VEC>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
-  extern __shared__ float acc_s[];           // [5][C] when several rows share a CTA
-  __shared__ float2 red[32];
-  const int t = threadIdx.x & (a.tpr - 1), rpb = blockDim.x / a.tpr;
+// Rows ahead in the backward: two, or one where 1024 threads' five tensors fill the shared memory.
+constexpr int bwd_slots(int block) { return block > 512 ? 1 : 2; }
+
+template <typename TS, typename TB, bool VEC, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd_kernel(const NormArgs a) {
+  typedef Slot<TS, VEC, BLOCK> SS;
+  typedef Slot<TB, VEC, BLOCK> SB;
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kStage = 2 * SS::kBytes + 3 * SB::kBytes, NS = bwd_slots(BLOCK);
+  float* acc_s = reinterpret_cast<float*>(ring);          // [5][C] when several rows share a CTA
+  __shared__ float2 red[2][32];
+  RowSum sums{red, 0};
+  const int t = threadIdx.x & (a.tpr - 1), rpb = BLOCK / a.tpr;
   const float inv = 1.f / (float)a.C;
+  const bool branch = a.u != nullptr, gated = a.gate != nullptr, pre = a.d_x != nullptr, thru = a.d_r != nullptr;
   float dga[E], dpw[E], dpb[E], dqw[E], dqb[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) dga[e] = dpw[e] = dpb[e] = dqw[e] = dqb[e] = 0.f;
-  for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += (long long)gridDim.x * rpb) {
-    const long long row = r0 + threadIdx.x / a.tpr;
-    const bool in = row < a.rows, live = in && (a.mask == nullptr || a.mask[row] != 0);
+  const long long step = (long long)gridDim.x * rpb;
+  const long long first = (long long)blockIdx.x * rpb + threadIdx.x / a.tpr;     // this thread's rows: first, first + step, ...
+  bool soon;                                                                     // whether the row to be fetched next is valid
+  auto look = [&](long long row) { return row < a.rows && (a.mask == nullptr || a.mask[row] != 0); };
+  auto fetch = [&](int k, long long row, bool live) {
+    uint8_t* slot = ring + (k % NS) * kStage;
+    const long long o = (row < a.rows ? row : 0) * a.C;
+    SS::fetch(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, live);
+    if (thru) SS::fetch(slot + SS::kBytes, static_cast<const TS*>(a.d_r) + o, t, a.tpr, a.C, row < a.rows);
+    slot += 2 * SS::kBytes;
+    if (branch) SB::fetch(slot, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live);
+    if (gated) SB::fetch(slot + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live);
+    if (pre) SB::fetch(slot + 2 * SB::kBytes, static_cast<const TB*>(a.d_x) + o, t, a.tpr, a.C, live);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  bool live0 = look(first), live1 = look(first + step);
+  fetch(0, first, live0);
+  if (NS == 2) fetch(1, first + step, live1);
+  soon = look(first + 2 * step);
+  float4 nst = live0 ? *reinterpret_cast<const float4*>(a.stats + 4 * first) : make_float4(0.f, 0.f, 0.f, 0.f);
+  long long row = first;
+  for (int k = 0; (long long)blockIdx.x * rpb + k * step < a.rows; ++k, row += step) {
+    const bool in = row < a.rows, live = live0;
     const long long o = (in ? row : 0) * a.C;
+    const uint8_t* slot = ring + (k % NS) * kStage;
     float s[E], u[E], g[E], dr[E], dx[E];
-    if (a.d_r != nullptr) {
-      get_row<VEC>(static_cast<const TS*>(a.d_r) + o, t, a.tpr, a.C, in, dr);
+    asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+    SS::get(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, live, s);
+    if (thru) {
+      SS::get(slot + SS::kBytes, static_cast<const TS*>(a.d_r) + o, t, a.tpr, a.C, in, dr);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) dr[e] = 0.f;
     }
-    get_row<VEC>(static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, live, s);
-    if (a.u != nullptr) get_row<VEC>(static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
-    if (a.gate != nullptr) get_row<VEC>(static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
-    const bool pre = a.d_x != nullptr;
-    if (pre) get_row<VEC>(static_cast<const TB*>(a.d_x) + o, t, a.tpr, a.C, live, dx);
-    const float4 st = live ? *reinterpret_cast<const float4*>(a.stats + 4 * row) : make_float4(0.f, 0.f, 0.f, 0.f);
+    slot += 2 * SS::kBytes;
+    if (branch) SB::get(slot, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
+    if (gated) SB::get(slot + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
+    if (pre) SB::get(slot + 2 * SB::kBytes, static_cast<const TB*>(a.d_x) + o, t, a.tpr, a.C, live, dx);
+    const float4 st = nst;
+    if (live1) nst = *reinterpret_cast<const float4*>(a.stats + 4 * (row + step));
+    else nst = make_float4(0.f, 0.f, 0.f, 0.f);
     float w[E];
     // u -> uhat; y in w; s -> r; gate -> sigmoid
-    if (a.u != nullptr) {
+    if (branch) {
       float pb[E], ga[E];
       get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
       get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, pb);
@@ -244,7 +349,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
         } else {
           w[e] = u[e];
         }
-        g[e] = a.gate != nullptr ? sigmoid(g[e]) : 1.f;
+        g[e] = gated ? sigmoid(g[e]) : 1.f;
         s[e] = fmaf(ga[e], g[e] * w[e], s[e]);
       }
     }
@@ -261,14 +366,14 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
         m.x += dx[e];
         m.y = fmaf(dx[e], s[e], m.y);
       }
-      m = row_sum(m, a.tpr, red);
+      m = sums(m, a.tpr);
       const float c1 = a.rms ? 0.f : m.x * inv, c2 = m.y * inv;
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (live) dr[e] = fmaf(st.w, dx[e] - c1 - s[e] * c2, dr[e]);
     }
     if (a.d_s != nullptr && in) put_row<VEC>(static_cast<TS*>(a.d_s) + o, t, a.tpr, a.C, dr);
-    if (a.u != nullptr) {
+    if (branch) {
       float ga[E], pw[E];
       get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
       get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, pw);
@@ -288,14 +393,21 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormArgs a) {
       }
       if (a.d_gate != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_gate) + o, t, a.tpr, a.C, g);
       if (a.post_w != nullptr) {
-        m = row_sum(m, a.tpr, red);
+        m = sums(m, a.tpr);
         const float e1 = a.rms ? 0.f : m.x * inv, e2 = m.y * inv;
 #pragma unroll
         for (int e = 0; e < E; ++e) w[e] = st.y * (w[e] - e1 - u[e] * e2);
       }
       if (a.d_u != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_u) + o, t, a.tpr, a.C, w);
     }
+    live0 = live1;
+    live1 = soon;
+    if (NS == 2) fetch(k, row + 2 * step, live1);
+    else fetch(k, row + step, live0);
+    soon = look(row + 3 * step);
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();                           // the ring's memory now takes the sums
   // the CTA's rows in order, then one line of sums per CTA
   float* out = a.part + (size_t)blockIdx.x * 5 * a.C;
   float* sum[5] = {dga, dpw, dpb, dqw, dqb};
@@ -345,30 +457,47 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* part, int
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+bool params_aligned(const NormArgs& a) {
+  return is_aligned(a.res_scale, 16) && is_aligned(a.post_w, 16) && is_aligned(a.post_b, 16) && is_aligned(a.pre_w, 16) &&
+         is_aligned(a.pre_b, 16);
+}
+
 int norm_tpr(int C) {
   int t = 1;
   while (t * E < C) t *= 2;
   return t;
 }
 int norm_block(int tpr) { return tpr < 256 ? 256 : tpr; }
+// CTAs of the backward: all that are resident at once (512 threads an SM, for
+// 128 registers a thread: 40 sums, a row and the next row), as each leaves a
+// line of parameter gradients.
 int norm_bwd_grid(long long rows, int C) {
-  const int rpb = norm_block(norm_tpr(C)) / norm_tpr(C);
-  const long long need = (rows + rpb - 1) / rpb, most = 148 * 2;
+  const int block = norm_block(norm_tpr(C)), rpb = block / norm_tpr(C);
+  const long long need = (rows + rpb - 1) / rpb, most = 148 * (block > 512 ? 1 : 512 / block);
   return (int)(need < most ? need : most);
 }
 
+template <typename TS, typename TB, bool VEC, int BLOCK>
+cudaError_t norm_launch(const NormArgs& a, bool bwd, int grid, cudaStream_t st) {
+  const int ks = Slot<TS, VEC, BLOCK>::kBytes, kb = Slot<TB, VEC, BLOCK>::kBytes;
+  size_t smem = bwd ? (size_t)bwd_slots(BLOCK) * (2 * ks + 3 * kb) : 2 * (size_t)(ks + 2 * kb);
+  if (bwd && BLOCK > a.tpr && smem < (size_t)5 * a.C * sizeof(float)) smem = (size_t)5 * a.C * sizeof(float);
+  const cudaError_t e = allow_max_smem(bwd ? reinterpret_cast<const void*>(&norm_bwd_kernel<TS, TB, VEC, BLOCK>)
+                                           : reinterpret_cast<const void*>(&norm_fwd_kernel<TS, TB, VEC, BLOCK>));
+  if (e != cudaSuccess) return e;
+  if (bwd) norm_bwd_kernel<TS, TB, VEC, BLOCK><<<grid, BLOCK, smem, st>>>(a);
+  else norm_fwd_kernel<TS, TB, VEC, BLOCK><<<grid, BLOCK, smem, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename TS, typename TB, int BLOCK>
+cudaError_t norm_launch(const NormArgs& a, bool vec, bool bwd, int grid, cudaStream_t st) {
+  return vec ? norm_launch<TS, TB, true, BLOCK>(a, bwd, grid, st) : norm_launch<TS, TB, false, BLOCK>(a, bwd, grid, st);
+}
 template <typename TS, typename TB>
 cudaError_t norm_launch(const NormArgs& a, bool vec, bool bwd, int grid, cudaStream_t st) {
   const int block = norm_block(a.tpr);
-  if (!bwd) {
-    if (vec) norm_fwd_kernel<TS, TB, true><<<grid, block, 0, st>>>(a);
-    else norm_fwd_kernel<TS, TB, false><<<grid, block, 0, st>>>(a);
-  } else {
-    const size_t smem = block > a.tpr ? (size_t)5 * a.C * sizeof(float) : 0;
-    if (vec) norm_bwd_kernel<TS, TB, true><<<grid, block, smem, st>>>(a);
-    else norm_bwd_kernel<TS, TB, false><<<grid, block, smem, st>>>(a);
-  }
-  return cudaGetLastError();
+  return block == 256 ? norm_launch<TS, TB, 256>(a, vec, bwd, grid, st)
+                      : (block == 512 ? norm_launch<TS, TB, 512>(a, vec, bwd, grid, st) : norm_launch<TS, TB, 1024>(a, vec, bwd, grid, st));
 }
 
 fipa_status norm_args(const fipa_norm_dims* d, const fipa_norm_inputs* in, NormArgs* a) {
@@ -423,10 +552,10 @@ FIPA_API fipa_status fipa_norm_residual(const fipa_norm_dims* d, const fipa_norm
   a.r = r;
   a.x = x;
   a.stats = stats;
-  const bool vec = a.C % E == 0 && is_aligned(a.s, 16) && is_aligned(a.u, 16) && is_aligned(a.gate, 16) &&
+  const bool vec = a.C % E == 0 && params_aligned(a) && is_aligned(a.s, 16) && is_aligned(a.u, 16) && is_aligned(a.gate, 16) &&
                    is_aligned(r, 16) && is_aligned(x, 16);
   const int rpb = norm_block(a.tpr) / a.tpr;
-  const long long need = (a.rows + rpb - 1) / rpb, most = 148 * 4;
+  const long long need = (a.rows + rpb - 1) / rpb, most = 148 * (1024 / norm_block(a.tpr));
   return norm_dispatch(d, a, vec, false, (int)(need < most ? need : most), static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FIPA_OK
              : FIPA_ERR_CUDA;
@@ -468,7 +597,7 @@ FIPA_API fipa_status fipa_norm_residual_backward(const fipa_norm_dims* d, const 
   a.d_u = g->u;
   a.d_gate = g->gate;
   a.part = static_cast<float*>(workspace);
-  const bool vec = a.C % E == 0 && is_aligned(a.s, 16) && is_aligned(a.u, 16) && is_aligned(a.gate, 16) &&
+  const bool vec = a.C % E == 0 && params_aligned(a) && is_aligned(a.s, 16) && is_aligned(a.u, 16) && is_aligned(a.gate, 16) &&
                    is_aligned(d_r, 16) && is_aligned(d_x, 16) && is_aligned(g->s, 16) && is_aligned(g->u, 16) &&
                    is_aligned(g->gate, 16);
   const int grid = norm_bwd_grid(d->rows, d->C);
