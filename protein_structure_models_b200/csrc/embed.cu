@@ -97,14 +97,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __r
   __shared__ int cnt[kDigits];
   cnt[threadIdx.x] = 0;
   __syncthreads();
+  int v[kSortItems];
+#pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     const int i = blockIdx.x * kSortBlock + k * kSortThreads + threadIdx.x;
-    if (i < n) {
-      int v = key[i];
-      if (first && (v < 0 || v >= V)) v = V;
-      if (first && v < V) mark[v] = 1;                        // every writer writes the same
-      atomicAdd(&cnt[(v >> shift) & mask], 1);
-    }
+    v[k] = i < n ? key[i] : -1;
+    if (first && i < n && (v[k] < 0 || v[k] >= V)) v[k] = V;
+  }
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    if (v[k] < 0) continue;
+    if (first && v[k] < V) mark[v[k]] = 1;                    // every writer writes the same
+    atomicAdd(&cnt[(v[k] >> shift) & mask], 1);
   }
   __syncthreads();
   if (threadIdx.x <= mask) hist[(size_t)threadIdx.x * gridDim.x + blockIdx.x] = cnt[threadIdx.x];
@@ -356,16 +360,32 @@ __device__ __forceinline__ int lower_bound(const int* key, int n, int v) {
   }
   return lo;
 }
-// CTAs [0, ncross): the run that starts in chunk q and crosses into the next is
-// the sum of its pieces, taken by 16 warps in 16 neighbouring stretches that are
-// added in order.  CTAs beyond: rows without a token are zero (marked by the
-// sort's first pass, or searched for in a short list).
-__global__ void __launch_bounds__(512) embed_join_kernel(const int* __restrict__ key, int n, int V, int C, int L, int nchunk, int slabs,
+// Sum of the pieces [lo, hi) of a run that starts in chunk q, for N columns.
+template <int N>
+__device__ __forceinline__ void add_pieces(float (&x)[N], const float* part, int C, int c, int q, int lo, int hi) {
+#pragma unroll 8
+  for (int k = lo; k < hi; ++k) {
+    const float* p = part + ((size_t)k * 2 + (k == q ? 1 : 0)) * C + c;
+    if (N == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p);
+      x[0] += y.x; x[1 % N] += y.y; x[2 % N] += y.z; x[3 % N] += y.w;
+    } else {
+      x[0] += *p;
+    }
+  }
+}
+// CTAs [0, ncross): a warp looks at one chunk.  If a run starts in it and goes
+// on, its pieces are added: up to 16 by the warp, more by all 16 warps of the
+// CTA, in 16 neighbouring stretches whose sums are added in order.  CTAs beyond:
+// rows without a token are zero (marked by the sort's first pass, or searched
+// for in a short list).  blockIdx.y: slab of 32 N columns.
+template <int N>
+__global__ void __launch_bounds__(512) embed_join_kernel(const int* __restrict__ key, int n, int V, int C, int L, int nchunk,
                                                          int ncross, float scale, const float* __restrict__ part,
                                                          const uint8_t* __restrict__ mark, float* __restrict__ dtable) {
-  __shared__ float red[16][32];
-  __shared__ int shared_last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float red[16][32 * N];
+  __shared__ int long_last[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.y * 32 * N, c = c0 + lane * N;
   if ((int)blockIdx.x >= ncross) {
     const long long step = (long long)(gridDim.x - ncross) * 16;
     for (long long v = (long long)(blockIdx.x - ncross) * 16 + warp; v < V; v += step) {
@@ -377,33 +397,60 @@ __global__ void __launch_bounds__(512) embed_join_kernel(const int* __restrict__
         used = b < n && key[b] == (int)v;
       }
       if (used) continue;
-      float* o = dtable + v * C;
-      if ((C & 3) == 0 && (reinterpret_cast<uintptr_t>(dtable) & 15) == 0) {
-        for (int c = lane; c < C / 4; c += 32) reinterpret_cast<float4*>(o)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      } else {
-        for (int c = lane; c < C; c += 32) o[c] = 0.f;
+      if (c < C) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) dtable[v * C + c + k] = 0.f;
       }
     }
     return;
   }
-  const int q = blockIdx.x / slabs, c = (blockIdx.x % slabs) * 32 + lane, e = (q + 1) * L;
-  if (e >= n) return;
-  const int cur = key[e];
-  if (cur >= V || key[e - 1] != cur || (q > 0 && key[q * L - 1] == cur)) return;     // no run starts here and goes on
-  if (threadIdx.x == 0) shared_last = (lower_bound(key + e, n - e, cur + 1) + e - 1) / L;
-  __syncthreads();
-  const int last = shared_last, m = last - q + 1, per = (m + 15) / 16;
-  float x = 0.f;
-  if (c < C) {
-    const int lo = q + warp * per, hi = min(lo + per, last + 1);
-#pragma unroll 8
-    for (int k = lo; k < hi; ++k) x += part[((size_t)k * 2 + (k == q ? 1 : 0)) * C + c];
+  const int q = blockIdx.x * 16 + warp, e = (q + 1) * L;
+  if (lane == 0) long_last[warp] = -1;
+  if (q + 1 < nchunk) {
+    const int cur = key[e];
+    if (cur < V && key[e - 1] == cur && !(q > 0 && key[q * L - 1] == cur)) {
+      // last chunk that begins inside the run
+      const bool in = q + 1 + lane < nchunk && key[(q + 1 + lane) * L] == cur;
+      const unsigned all = __ballot_sync(0xffffffffu, in);
+      int last = q + __ffs(~all) - 1;
+      if (all == 0xffffffffu) {
+        int lo = q + 32, hi = nchunk;                       // key at lo L is cur, at hi L it is not (or the list ends)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (key[(size_t)mid * L] == cur) lo = mid;
+          else hi = mid;
+        }
+        last = lo;
+      }
+      if (last - q < 16) {
+        if (c < C) {
+          float x[N] = {0.f};
+          add_pieces<N>(x, part, C, c, q, q, last + 1);
+#pragma unroll
+          for (int k = 0; k < N; ++k) dtable[(size_t)cur * C + c + k] = x[k] * scale;
+        }
+      } else if (lane == 0) {
+        long_last[warp] = last;
+      }
+    }
   }
-  red[warp][lane] = x;
   __syncthreads();
-  if (warp == 0 && c < C) {
-    for (int w = 1; w < 16; ++w) x += red[w][lane];
-    dtable[(size_t)cur * C + c] = x * scale;
+  for (int w = 0; w < 16; ++w) {
+    const int last = long_last[w], first = blockIdx.x * 16 + w;
+    if (last < 0) continue;
+    const int cur = key[(first + 1) * L], per = (last - first + 16) / 16;
+    const int lo = first + warp * per, hi = min(lo + per, last + 1);
+    float x[N] = {0.f};
+    if (c < C) add_pieces<N>(x, part, C, c, first, lo, hi);
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[warp][lane * N + k] = x[k];
+    __syncthreads();
+    if ((int)threadIdx.x < 32 * N && c0 + (int)threadIdx.x < C) {
+      float y = 0.f;
+      for (int v = 0; v < 16; ++v) y += red[v][threadIdx.x];
+      dtable[(size_t)cur * C + c0 + threadIdx.x] = y * scale;
+    }
+    __syncthreads();
   }
 }
 
@@ -557,10 +604,13 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
                                             : embed_sum<__nv_bfloat16>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s);
     if (e != cudaSuccess) return FIPA_ERR_CUDA;
   }
-  const int slabs = (C + 31) / 32;
-  const long long cross = p.nchunk > 1 ? (long long)(p.nchunk - 1) * slabs : 0, fill = ((long long)V + 15) / 16;
-  if (cross > 0x3fffffff) return FIPA_ERR_UNSUPPORTED;
-  embed_join_kernel<<<(unsigned)(cross + (fill < 148 * 8 ? fill : 148 * 8)), 512, 0, s>>>(
-      key, n, V, C, p.L, p.nchunk, slabs, (int)cross, (float)scale, reinterpret_cast<float*>(ws + p.off_part), mark, d_table);
+  const int ncross = p.nchunk > 1 ? (p.nchunk - 1 + 15) / 16 : 0;
+  const long long fill = ((long long)V + 15) / 16;
+  const unsigned gx = (unsigned)(ncross + (fill < 148 * 8 ? fill : 148 * 8));
+  const float* part = reinterpret_cast<const float*>(ws + p.off_part);
+  if (C % 4 == 0 && is_aligned(d_table, 16))
+    embed_join_kernel<4><<<dim3(gx, (unsigned)((C + 127) / 128)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, mark, d_table);
+  else
+    embed_join_kernel<1><<<dim3(gx, (unsigned)((C + 31) / 32)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, mark, d_table);
   return cudaGetLastError() == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
 }

@@ -42,6 +42,7 @@ struct WinArgs {
 
 constexpr int kWinMaxD = 128;
 constexpr int kWinMaxSinks = 128;
+constexpr int kWinStepRows = 32;       // up to here columns are split instead of rows (window_step.cu)
 
 // The gradient of a sink key sums over every later query, which one CTA would
 // walk alone: the queries beyond the window of the sinks' key tile are cut into
@@ -106,6 +107,7 @@ __device__ __forceinline__ bool win_alive(const WinArgs& a, int b, int p) {
 cudaError_t launch_win_fwd_simt(const WinArgs& a, cudaStream_t s);       // float32 tensors
 cudaError_t launch_win_bwd_simt(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_fwd_mma(const WinArgs& a, cudaStream_t s);        // bfloat16 tensors
+cudaError_t launch_win_step(const WinArgs& a, cudaStream_t s);           // few rows
 cudaError_t launch_win_bwd_mma(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s);
 

@@ -18,112 +18,15 @@
 #include <math.h>
 
 #include "kernels.h"
-#include "sm100.cuh"
-#include "window.h"
+#include "window_mma.cuh"
 
 namespace fipa {
 namespace {
 
-typedef __nv_bfloat16 bf16;
 constexpr int T = kWinSimtTile;            // rows and columns of a tile
 constexpr int kThreads = 128;              // 4 warps x 16 rows
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 template <int DP>
-struct Tile {
-  static constexpr int ld = DP + 8;        // elements of a padded row
-  static constexpr int elems = T * ld;
-};
-
-__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-struct Src {                               // one of the inputs, for one (b, hkv)
-  const bf16* p;
-  long long sn, sh;
-  int width;
-  bool vec;
-};
-// One tile of 64 rows x width elements; at(r) gives row r's elements, or null for a row of zeros.
-template <int DP, typename At>
-__device__ __forceinline__ void load_tile(bf16* dst, const Src& s, At at) {
-  constexpr int CH = DP / 8;
-  for (int e = threadIdx.x; e < T * CH; e += kThreads) {
-    const int r = e / CH, c = e % CH;
-    const bf16* p = at(r);
-    bf16* d = dst + r * Tile<DP>::ld + c * 8;
-    const bool on = p != nullptr && c * 8 < s.width;
-    if (s.vec) {
-      cp16_zfill(smem_u32(d), on ? p + c * 8 : s.p, on);
-    } else {
-      uint16_t w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = on && c * 8 + k < s.width ? reinterpret_cast<const uint16_t*>(p)[c * 8 + k] : (uint16_t)0;
-      *reinterpret_cast<uint4*>(d) = make_uint4(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16,
-                                                w[4] | (uint32_t)w[5] << 16, w[6] | (uint32_t)w[7] << 16);
-    }
-  }
-}
-__device__ __forceinline__ Src source(const void* base, long long sb, long long sn, long long sh, int width, int b, int h0) {
-  Src s;
-  s.p = static_cast<const bf16*>(base) + b * sb + h0 * sh;
-  s.sn = sn;
-  s.sh = sh;
-  s.width = width;
-  s.vec = ((reinterpret_cast<uintptr_t>(base) & 15) | ((sb | sn | sh | width) & 7)) == 0;
-  return s;
-}
-// The 16 x 16 A operand at row r0, depth k0 of a tile; the 16 x 16 B operand of
-// columns n0 .. n0+15 at depth k0 (rows = columns of the product), and the one
-// whose rows are the product's depth.
-template <int DP>
-__device__ __forceinline__ uint32_t a_addr(uint32_t base, int r0, int k0, int lane) {
-  return base + 2 * ((r0 + (lane & 15)) * Tile<DP>::ld + k0 + ((lane >> 4) << 3));
-}
-template <int DP>
-__device__ __forceinline__ uint32_t b_addr(uint32_t base, int n0, int k0, int lane) {
-  return base + 2 * ((n0 + (lane & 7) + ((lane >> 4) << 3)) * Tile<DP>::ld + k0 + (((lane >> 3) & 1) << 3));
-}
-template <int DP>
-__device__ __forceinline__ uint32_t bt_addr(uint32_t base, int k0, int n0, int lane) {
-  return base + 2 * ((k0 + (lane & 7) + (((lane >> 3) & 1) << 3)) * Tile<DP>::ld + n0 + ((lane >> 4) << 3));
-}
-
-// Columns that the 16 rows of a warp see: any of them, and all of them.
-struct Reach {
-  int s_any, s_all, a_any, a_all, e_any, e_all;       // sinks [0, s), window [a, e)
-  __device__ __forceinline__ bool any(int u) const { return u < s_any || (u + 15 >= a_any && u < e_any); }
-  __device__ __forceinline__ bool all(int u) const { return u + 15 < s_all || (u >= a_all && u + 15 < e_all); }
-};
-__device__ __forceinline__ Reach reach(const WinArgs& a, const WinCols& c, int q0, int f, int f1) {
-  const int lo = min(max(q0 + f / a.G, 0), a.Nk - 1), hi = min(max(q0 + (min(f + 16, f1) - 1) / a.G, 0), a.Nk - 1);
-  const WinRow x = win_row(a, c, lo, true), y = win_row(a, c, hi, true);
-  if (f >= f1) return Reach{0, 0, 0, 0, 0, 0};
-  return Reach{y.s1, x.s1, x.w0, y.w0, y.w1, x.w1};
-}
+constexpr int kElems = T * Tile<DP>::ld;
 
 // Whether columns u0 .. u0+63 exist and are not masked: two words.
 __device__ __forceinline__ void column_bits(uint32_t* bits, const WinArgs& a, int b, const WinCols& c, int u0) {
@@ -139,8 +42,8 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Qs = reinterpret_cast<bf16*>(smem);
-  bf16* Ks = Qs + Tile<DP>::elems;                     // two stages each
-  bf16* Vs = Ks + 2 * Tile<DP>::elems;
+  bf16* Ks = Qs + kElems<DP>;                     // two stages each
+  bf16* Vs = Ks + 2 * kElems<DP>;
   __shared__ uint32_t bits[2][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
   const int F = a.Nq * a.G, tiles = (F + T - 1) / T;
@@ -167,8 +70,8 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
         return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
       };
     };
-    load_tile<DP>(Ks + st * Tile<DP>::elems, k, keyed(k));
-    load_tile<DP>(Vs + st * Tile<DP>::elems, v, keyed(v));
+    load_tile<DP>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -181,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
   uint32_t qf[DP / 16][4];
   const float sc = a.scale * kLog2e;
   if (ntile > 0) {
-    load_tile<DP>(Qs, q, [&](int r) -> const bf16* {
+    load_tile<DP>(Qs, q, T, threadIdx.x, kThreads, [&](int r) -> const bf16* {
       const int f = f0 + r, i = f / a.G;
       return f < f1 && win_alive(a, b, q0 + i) ? q.p + i * q.sn + (f - i * a.G) * q.sh : nullptr;
     });
@@ -200,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) ldsm4(qf[kk], a_addr<DP>(smem_u32(Qs), 16 * warp, 16 * kk, lane));
     }
-    const uint32_t ks = smem_u32(Ks + st * Tile<DP>::elems), vs = smem_u32(Vs + st * Tile<DP>::elems);
+    const uint32_t ks = smem_u32(Ks + st * kElems<DP>), vs = smem_u32(Vs + st * kElems<DP>);
     const uint32_t w[2] = {bits[st][0], bits[st][1]};
     float s[8][4];
     bool on[4];
@@ -306,29 +209,6 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
   }
 }
 
-// Writes a warp's 16 x DP sums as bfloat16 rows; at(i) is the row of this thread's half i, null: not written.
-template <int DP, typename At>
-__device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], int width, const void* base, float f, int lane, At at) {
-  const bool pair = (width & 1) == 0 && (reinterpret_cast<uintptr_t>(base) & 3) == 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    bool keep;
-    bf16* o = at(i, keep);
-    if (o == nullptr) continue;
-#pragma unroll
-    for (int n = 0; n < DP / 8; ++n) {
-      const int d = 8 * n + (lane & 3) * 2;
-      const float x = keep ? acc[n][2 * i] * f : 0.f, y = keep ? acc[n][2 * i + 1] * f : 0.f;
-      if (pair && d < width) {
-        *reinterpret_cast<uint32_t*>(o + d) = pack(x, y);
-      } else {
-        if (d < width) o[d] = __float2bfloat16_rn(x);
-        if (d + 1 < width) o[d + 1] = __float2bfloat16_rn(y);
-      }
-    }
-  }
-}
-
 // delta = dO.out of a row tile, four neighbouring lanes a row (two passes of 32 rows); dead rows 0.
 template <int DP>
 __device__ __forceinline__ void row_delta(float* sdelta, const bf16* dOs, const WinArgs& a, const bf16* out, int b, int hkv, int q0,
@@ -367,9 +247,9 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Qs = reinterpret_cast<bf16*>(smem);
-  bf16* Os = Qs + Tile<DP>::elems;
-  bf16* Ks = Os + Tile<DP>::elems;
-  bf16* Vs = Ks + 2 * Tile<DP>::elems;
+  bf16* Os = Qs + kElems<DP>;
+  bf16* Ks = Os + kElems<DP>;
+  bf16* Vs = Ks + 2 * kElems<DP>;
   __shared__ uint32_t bits[2][2];
   __shared__ float sdelta[T];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
@@ -398,8 +278,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
         return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
       };
     };
-    load_tile<DP>(Ks + st * Tile<DP>::elems, k, keyed(k));
-    load_tile<DP>(Vs + st * Tile<DP>::elems, v, keyed(v));
+    load_tile<DP>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -417,8 +297,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
         return f < f1 && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
       };
     };
-    load_tile<DP>(Qs, q, rows(q));
-    load_tile<DP>(Os, g_, rows(g_));
+    load_tile<DP>(Qs, q, T, threadIdx.x, kThreads, rows(q));
+    load_tile<DP>(Os, g_, T, threadIdx.x, kThreads, rows(g_));
     load(0);
     cp_wait<0>();
     __syncthreads();
@@ -446,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
       cp_wait<0>();
     }
     __syncthreads();
-    const uint32_t ks = smem_u32(Ks + st * Tile<DP>::elems), vs = smem_u32(Vs + st * Tile<DP>::elems);
+    const uint32_t ks = smem_u32(Ks + st * kElems<DP>), vs = smem_u32(Vs + st * kElems<DP>);
     const uint32_t w[2] = {bits[st][0], bits[st][1]};
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -509,9 +389,9 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Ks = reinterpret_cast<bf16*>(smem);
-  bf16* Vs = Ks + Tile<DP>::elems;
-  bf16* Qs = Vs + Tile<DP>::elems;
-  bf16* Os = Qs + 2 * Tile<DP>::elems;
+  bf16* Vs = Ks + kElems<DP>;
+  bf16* Qs = Vs + kElems<DP>;
+  bf16* Os = Qs + 2 * kElems<DP>;
   __shared__ float slse[2][T], sdel[2][T];
   __shared__ int spos[2][T];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
@@ -556,8 +436,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
         return f < fh && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
       };
     };
-    load_tile<DP>(Qs + st * Tile<DP>::elems, q, rows(q));
-    load_tile<DP>(Os + st * Tile<DP>::elems, g_, rows(g_));
+    load_tile<DP>(Qs + st * kElems<DP>, q, T, threadIdx.x, kThreads, rows(q));
+    load_tile<DP>(Os + st * kElems<DP>, g_, T, threadIdx.x, kThreads, rows(g_));
     cp_async_commit();
     if (threadIdx.x < T) {
       const int f = f0 + threadIdx.x, i = f / a.G;
@@ -583,8 +463,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
     auto keyed = [&](const Src& s) {
       return [&](int r) -> const bf16* { return j0 + r <= j1 && win_alive(a, b, j0 + r) ? s.p + (j0 + r) * s.sn : nullptr; };
     };
-    load_tile<DP>(Ks, k, keyed(k));
-    load_tile<DP>(Vs, v, keyed(v));
+    load_tile<DP>(Ks, k, T, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP>(Vs, v, T, threadIdx.x, kThreads, keyed(v));
     load(0);
   }
   for (int t = 0; t < ntile; ++t) {
@@ -596,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
       cp_wait<0>();
     }
     __syncthreads();
-    const uint32_t qs = smem_u32(Qs + st * Tile<DP>::elems), os = smem_u32(Os + st * Tile<DP>::elems);
+    const uint32_t qs = smem_u32(Qs + st * kElems<DP>), os = smem_u32(Os + st * kElems<DP>);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       if (fl + t * T + 16 * g >= fh) break;
@@ -687,13 +567,13 @@ cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
   const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_fwd_mma_kernel<DP>));
   if (e != cudaSuccess) return e;
-  win_fwd_mma_kernel<DP><<<(unsigned)grid, kThreads, 5 * Tile<DP>::elems * sizeof(bf16), s>>>(a);
+  win_fwd_mma_kernel<DP><<<(unsigned)grid, kThreads, 5 * kElems<DP> * sizeof(bf16), s>>>(a);
   return cudaGetLastError();
 }
 
 template <int DP>
 cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
-  const size_t smem = 6 * Tile<DP>::elems * sizeof(bf16);
+  const size_t smem = 6 * kElems<DP> * sizeof(bf16);
   cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP>));
   if (e != cudaSuccess) return e;
   e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP>));
@@ -711,6 +591,7 @@ cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_win_fwd_mma(const WinArgs& a, cudaStream_t s) {
+  if ((long long)a.Nq * a.G <= kWinStepRows) return launch_win_step(a, s);
   const int w = a.D > a.Dv ? a.D : a.Dv;
   return w <= 16 ? fwd<16>(a, s) : (w <= 32 ? fwd<32>(a, s) : (w <= 64 ? fwd<64>(a, s) : fwd<128>(a, s)));
 }

@@ -1,0 +1,133 @@
+// window_mma.cuh -- shared by the bfloat16 window attention kernels: tiles in
+// padded shared memory, asynchronous copies into them, m16n8k16 products on them.
+#pragma once
+
+#include "sm100.cuh"
+#include "window.h"
+
+namespace fipa {
+namespace {
+
+typedef __nv_bfloat16 bf16;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Rows are padded by 16 bytes, so that eight neighbouring rows start in different banks.
+template <int DP>
+struct Tile {
+  static constexpr int ld = DP + 8;        // elements of a padded row
+};
+
+__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct Src {                               // one of the inputs, for one (b, hkv)
+  const bf16* p;
+  long long sn, sh;
+  int width;
+  bool vec;
+};
+// A tile of rows x width elements, by `threads` threads of which this is `me`; at(r) gives row r's elements, or null for a row of zeros.
+template <int DP, typename At>
+__device__ __forceinline__ void load_tile(bf16* dst, const Src& s, int rows, int me, int threads, At at) {
+  constexpr int CH = DP / 8;
+  for (int e = me; e < rows * CH; e += threads) {
+    const int r = e / CH, c = e % CH;
+    const bf16* p = at(r);
+    bf16* d = dst + r * Tile<DP>::ld + c * 8;
+    const bool on = p != nullptr && c * 8 < s.width;
+    if (s.vec) {
+      cp16_zfill(smem_u32(d), on ? p + c * 8 : s.p, on);
+    } else {
+      uint16_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = on && c * 8 + k < s.width ? reinterpret_cast<const uint16_t*>(p)[c * 8 + k] : (uint16_t)0;
+      *reinterpret_cast<uint4*>(d) = make_uint4(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16,
+                                                w[4] | (uint32_t)w[5] << 16, w[6] | (uint32_t)w[7] << 16);
+    }
+  }
+}
+__device__ __forceinline__ Src source(const void* base, long long sb, long long sn, long long sh, int width, int b, int h0) {
+  Src s;
+  s.p = static_cast<const bf16*>(base) + b * sb + h0 * sh;
+  s.sn = sn;
+  s.sh = sh;
+  s.width = width;
+  s.vec = ((reinterpret_cast<uintptr_t>(base) & 15) | ((sb | sn | sh | width) & 7)) == 0;
+  return s;
+}
+// The 16 x 16 A operand at row r0, depth k0 of a tile; the 16 x 16 B operand of
+// columns n0 .. n0+15 at depth k0 (rows = columns of the product), and the one
+// whose rows are the product's depth.
+template <int DP>
+__device__ __forceinline__ uint32_t a_addr(uint32_t base, int r0, int k0, int lane) {
+  return base + 2 * ((r0 + (lane & 15)) * Tile<DP>::ld + k0 + ((lane >> 4) << 3));
+}
+template <int DP>
+__device__ __forceinline__ uint32_t b_addr(uint32_t base, int n0, int k0, int lane) {
+  return base + 2 * ((n0 + (lane & 7) + ((lane >> 4) << 3)) * Tile<DP>::ld + k0 + (((lane >> 3) & 1) << 3));
+}
+template <int DP>
+__device__ __forceinline__ uint32_t bt_addr(uint32_t base, int k0, int n0, int lane) {
+  return base + 2 * ((k0 + (lane & 7) + (((lane >> 3) & 1) << 3)) * Tile<DP>::ld + n0 + ((lane >> 4) << 3));
+}
+
+// Columns that the 16 rows of a warp see: any of them, and all of them.
+struct Reach {
+  int s_any, s_all, a_any, a_all, e_any, e_all;       // sinks [0, s), window [a, e)
+  __device__ __forceinline__ bool any(int u) const { return u < s_any || (u + 15 >= a_any && u < e_any); }
+  __device__ __forceinline__ bool all(int u) const { return u + 15 < s_all || (u >= a_all && u + 15 < e_all); }
+};
+__device__ __forceinline__ Reach reach(const WinArgs& a, const WinCols& c, int q0, int f, int f1) {
+  const int lo = min(max(q0 + f / a.G, 0), a.Nk - 1), hi = min(max(q0 + (min(f + 16, f1) - 1) / a.G, 0), a.Nk - 1);
+  const WinRow x = win_row(a, c, lo, true), y = win_row(a, c, hi, true);
+  if (f >= f1) return Reach{0, 0, 0, 0, 0, 0};
+  return Reach{y.s1, x.s1, x.w0, y.w0, y.w1, x.w1};
+}
+
+// Writes a warp's 16 x DP sums as bfloat16 rows; at(i) is the row of this thread's half i, null: not written.
+template <int DP, typename At>
+__device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], int width, const void* base, float f, int lane, At at) {
+  const bool pair = (width & 1) == 0 && (reinterpret_cast<uintptr_t>(base) & 3) == 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    bool keep;
+    bf16* o = at(i, keep);
+    if (o == nullptr) continue;
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) {
+      const int d = 8 * n + (lane & 3) * 2;
+      const float x = keep ? acc[n][2 * i] * f : 0.f, y = keep ? acc[n][2 * i + 1] * f : 0.f;
+      if (pair && d < width) {
+        *reinterpret_cast<uint32_t*>(o + d) = pack(x, y);
+      } else {
+        if (d < width) o[d] = __float2bfloat16_rn(x);
+        if (d + 1 < width) o[d + 1] = __float2bfloat16_rn(y);
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace fipa
