@@ -65,6 +65,12 @@ inline WinSinkPlan win_sink_plan(int B, int Nq, int Nk, int Hkv, int G, int D, i
   return s;
 }
 
+// Whether q, k and v can be read 16 bytes at a time.
+inline bool win_vec(const WinArgs& a) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+  return ((p & 15) | ((a.qb | a.qn | a.qh | a.kb | a.kn | a.kh | a.vb | a.vn | a.vh | a.D | a.Dv) & 7)) == 0;
+}
+
 #ifdef __CUDACC__
 __device__ __forceinline__ int win_q0(const WinArgs& a, int b) {
   if (a.q_start == nullptr) return a.Nk - a.Nq;
