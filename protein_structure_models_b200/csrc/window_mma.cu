@@ -38,7 +38,7 @@ __device__ __forceinline__ void column_bits(uint32_t* bits, const WinArgs& a, in
   }
 }
 
-template <int DP>
+template <int DP, bool VEC>
 __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Qs = reinterpret_cast<bf16*>(smem);
@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
         return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
       };
     };
-    load_tile<DP>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
+    load_tile<DP, VEC>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP, VEC>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
   uint32_t qf[DP / 16][4];
   const float sc = a.scale * kLog2e;
   if (ntile > 0) {
-    load_tile<DP>(Qs, q, T, threadIdx.x, kThreads, [&](int r) -> const bf16* {
+    load_tile<DP, VEC>(Qs, q, T, threadIdx.x, kThreads, [&](int r) -> const bf16* {
       const int f = f0 + r, i = f / a.G;
       return f < f1 && win_alive(a, b, q0 + i) ? q.p + i * q.sn + (f - i * a.G) * q.sh : nullptr;
     });
@@ -145,17 +145,24 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
       for (int i = 0; i < 2; ++i) {
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        const float mn = fmaxf(m[i], mx[i]);
-        mb[i] = mn == -INFINITY ? 0.f : mn * sc;
-        const float f = ex2_approx(m[i] * sc - mb[i]);
-        m[i] = mn;
-        l[i] *= f;
+      }
+      // m follows the true maximum only when it would be left behind by 2^8: the
+      // sums keep their relative precision, and most tiles rescale nothing
+      if (__any_sync(0xffffffffu, (mx[0] - m[0]) * sc > kWinLag || (mx[1] - m[1]) * sc > kWinLag)) {
 #pragma unroll
-        for (int n = 0; n < DP / 8; ++n) {
-          acc[n][2 * i] *= f;
-          acc[n][2 * i + 1] *= f;
+        for (int i = 0; i < 2; ++i) {
+          const float mn = fmaxf(m[i], mx[i]), f = ex2_approx(mn == -INFINITY ? -INFINITY : (m[i] - mn) * sc);
+          m[i] = mn;
+          l[i] *= f;
+#pragma unroll
+          for (int n = 0; n < DP / 8; ++n) {
+            acc[n][2 * i] *= f;
+            acc[n][2 * i + 1] *= f;
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mb[i] = m[i] == -INFINITY ? 0.f : m[i] * sc;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         if (!on[g]) continue;
@@ -243,7 +250,7 @@ __device__ __forceinline__ void row_delta(float* sdelta, const bf16* dOs, const 
   }
 }
 
-template <int DP>
+template <int DP, bool VEC>
 __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Qs = reinterpret_cast<bf16*>(smem);
@@ -278,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
         return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
       };
     };
-    load_tile<DP>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
+    load_tile<DP, VEC>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP, VEC>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -297,8 +304,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
         return f < f1 && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
       };
     };
-    load_tile<DP>(Qs, q, T, threadIdx.x, kThreads, rows(q));
-    load_tile<DP>(Os, g_, T, threadIdx.x, kThreads, rows(g_));
+    load_tile<DP, VEC>(Qs, q, T, threadIdx.x, kThreads, rows(q));
+    load_tile<DP, VEC>(Os, g_, T, threadIdx.x, kThreads, rows(g_));
     load(0);
     cp_wait<0>();
     __syncthreads();
@@ -385,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
 }
 
 // dk and dv of one key tile over the rows of its window, or (sink jobs) over one chunk of the rows beyond it.
-template <int DP>
+template <int DP, bool VEC>
 __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Ks = reinterpret_cast<bf16*>(smem);
@@ -436,8 +443,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
         return f < fh && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
       };
     };
-    load_tile<DP>(Qs + st * kElems<DP>, q, T, threadIdx.x, kThreads, rows(q));
-    load_tile<DP>(Os + st * kElems<DP>, g_, T, threadIdx.x, kThreads, rows(g_));
+    load_tile<DP, VEC>(Qs + st * kElems<DP>, q, T, threadIdx.x, kThreads, rows(q));
+    load_tile<DP, VEC>(Os + st * kElems<DP>, g_, T, threadIdx.x, kThreads, rows(g_));
     cp_async_commit();
     if (threadIdx.x < T) {
       const int f = f0 + threadIdx.x, i = f / a.G;
@@ -463,8 +470,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
     auto keyed = [&](const Src& s) {
       return [&](int r) -> const bf16* { return j0 + r <= j1 && win_alive(a, b, j0 + r) ? s.p + (j0 + r) * s.sn : nullptr; };
     };
-    load_tile<DP>(Ks, k, T, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP>(Vs, v, T, threadIdx.x, kThreads, keyed(v));
+    load_tile<DP, VEC>(Ks, k, T, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP, VEC>(Vs, v, T, threadIdx.x, kThreads, keyed(v));
     load(0);
   }
   for (int t = 0; t < ntile; ++t) {
@@ -562,30 +569,39 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
   store_rows<DP>(dv, a.Dv, a.d_v, 1.f, lane, [&](int i, bool& keep) { return at(a.d_v, a.Dv, i, keep); });
 }
 
-template <int DP>
+template <int DP, bool VEC>
 cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
   const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
-  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_fwd_mma_kernel<DP>));
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_fwd_mma_kernel<DP, VEC>));
   if (e != cudaSuccess) return e;
-  win_fwd_mma_kernel<DP><<<(unsigned)grid, kThreads, 5 * kElems<DP> * sizeof(bf16), s>>>(a);
+  win_fwd_mma_kernel<DP, VEC><<<(unsigned)grid, kThreads, 5 * kElems<DP> * sizeof(bf16), s>>>(a);
   return cudaGetLastError();
 }
 
-template <int DP>
+template <int DP, bool VEC>
 cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
   const size_t smem = 6 * kElems<DP> * sizeof(bf16);
-  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP>));
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP, VEC>));
   if (e != cudaSuccess) return e;
-  e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP>));
+  e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP, VEC>));
   if (e != cudaSuccess) return e;
   const long long gq = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
-  win_bwd_q_mma_kernel<DP><<<(unsigned)gq, kThreads, smem, s>>>(a);
+  win_bwd_q_mma_kernel<DP, VEC><<<(unsigned)gq, kThreads, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int nsink = a.nchunk > 0 ? (a.sinks + T - 1) / T : 0;
   const long long gk = (long long)a.B * a.Hkv * ((a.Nk + T - 1) / T + (long long)nsink * a.nchunk);
-  win_bwd_k_mma_kernel<DP><<<(unsigned)gk, kThreads, smem, s>>>(a);
+  win_bwd_k_mma_kernel<DP, VEC><<<(unsigned)gk, kThreads, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return a.nchunk > 0 ? launch_win_sink_reduce(a, 0, s) : cudaSuccess;
+}
+
+template <int DP>
+cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
+  return win_vec(a) ? fwd<DP, true>(a, s) : fwd<DP, false>(a, s);
+}
+template <int DP>
+cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
+  return win_vec(a) && (reinterpret_cast<uintptr_t>(a.d_out) & 15) == 0 ? bwd<DP, true>(a, s) : bwd<DP, false>(a, s);
 }
 
 }  // namespace

@@ -10,6 +10,7 @@ namespace {
 
 typedef __nv_bfloat16 bf16;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kWinLag = 8.f;
 
 // Rows are padded by 16 bytes, so that eight neighbouring rows start in different banks.
 template <int DP>
@@ -46,10 +47,12 @@ struct Src {                               // one of the inputs, for one (b, hkv
   const bf16* p;
   long long sn, sh;
   int width;
-  bool vec;
 };
+// VEC: every load is on a 16-byte boundary.  The slow loads are instantiations
+// of their own: beside the fast ones they would fill the instruction cache.
+//
 // A tile of rows x width elements, by `threads` threads of which this is `me`; at(r) gives row r's elements, or null for a row of zeros.
-template <int DP, typename At>
+template <int DP, bool VEC, typename At>
 __device__ __forceinline__ void load_tile(bf16* dst, const Src& s, int rows, int me, int threads, At at) {
   constexpr int CH = DP / 8;
   for (int e = me; e < rows * CH; e += threads) {
@@ -57,7 +60,7 @@ __device__ __forceinline__ void load_tile(bf16* dst, const Src& s, int rows, int
     const bf16* p = at(r);
     bf16* d = dst + r * Tile<DP>::ld + c * 8;
     const bool on = p != nullptr && c * 8 < s.width;
-    if (s.vec) {
+    if (VEC) {
       cp16_zfill(smem_u32(d), on ? p + c * 8 : s.p, on);
     } else {
       uint16_t w[8];
@@ -74,7 +77,6 @@ __device__ __forceinline__ Src source(const void* base, long long sb, long long 
   s.sn = sn;
   s.sh = sh;
   s.width = width;
-  s.vec = ((reinterpret_cast<uintptr_t>(base) & 15) | ((sb | sn | sh | width) & 7)) == 0;
   return s;
 }
 // The 16 x 16 A operand at row r0, depth k0 of a tile; the 16 x 16 B operand of

@@ -31,7 +31,6 @@ namespace {
 namespace cg = cooperative_groups;
 constexpr int kWarps = 4;
 constexpr int kCols = 16;
-constexpr float kLag = 8.f;
 
 // N words (2 N channels) of a row from channel d0 on; channels at or beyond the width are 0.
 template <int N, bool VEC>
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP <= 16 ? 5 : (DP <= 64 ? 4 : 2)
       }
       // m follows the true maximum only when it would be left behind by 2^8: the
       // sums keep their relative precision, and most tiles rescale nothing
-      if (__any_sync(0xffffffffu, (mx[0] - m[0]) * sc > kLag || (mx[1] - m[1]) * sc > kLag)) {
+      if (__any_sync(0xffffffffu, (mx[0] - m[0]) * sc > kWinLag || (mx[1] - m[1]) * sc > kWinLag)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float mn = fmaxf(m[i], mx[i]), f = ex2_approx(mn == -INFINITY ? -INFINITY : (m[i] - mn) * sc);
