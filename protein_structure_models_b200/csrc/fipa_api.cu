@@ -842,12 +842,12 @@ fipa_status window_inputs(fipa_handle* h, const fipa_heads* q, const fipa_heads*
   return FIPA_OK;
 }
 
-// Workspace of the backward: delta [B,H,Nq], then the sinks' partial sums.
-size_t window_bwd_bytes(const fipa::WinArgs& a, fipa::WinSinkPlan* sp) {
-  *sp = fipa::win_sink_plan(a.B, a.Nq, a.Nk, a.Hkv, a.G, a.D, a.Dv, a.left, a.sinks, fipa::kWinSimtTile,
-                            fipa::kWinSimtTile);
+// Workspace of the backward: delta [B,H,Nq], then the sinks' partial sums, for
+// the key tile of whichever kernels take the call.
+size_t window_bwd_bytes(const fipa::WinArgs& a) {
+  const size_t x = fipa::win_sink_plan(a, fipa::kWinSimtTile).part_floats, y = fipa::win_sink_plan(a, fipa::kWinTcRows).part_floats;
   const size_t delta = ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256;
-  return delta + sp->part_floats * sizeof(float);
+  return delta + (x > y ? x : y) * sizeof(float);
 }
 
 }  // namespace
@@ -868,7 +868,7 @@ FIPA_API fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, 
   a.lse = lse;
   DeviceGuard g(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_fwd_simt(a, s) : fipa::launch_win_fwd_mma(a, s);
+  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_fwd_simt(a, s) : fipa::launch_win_fwd(a, s);
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention launch", e);
 }
 
@@ -879,8 +879,7 @@ FIPA_API fipa_status fipa_window_attention_backward_workspace_size(const fipa_ha
   fipa::WinArgs a;
   const fipa_status st = window_args(h, win, &a);
   if (st != FIPA_OK) return st;
-  fipa::WinSinkPlan sp;
-  *bytes = window_bwd_bytes(a, &sp);
+  *bytes = window_bwd_bytes(a);
   return FIPA_OK;
 }
 
@@ -902,8 +901,7 @@ FIPA_API fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_h
     if (req[i] == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, std::string(names[i]) + " is NULL");
     if (!aligned(req[i], i == 1 ? 4 : es)) return fail(h, FIPA_ERR_INVALID_ARG, std::string(names[i]) + " is misaligned");
   }
-  fipa::WinSinkPlan sp;
-  const size_t need = window_bwd_bytes(a, &sp);
+  const size_t need = window_bwd_bytes(a);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(h, FIPA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   if (!aligned(workspace, 256)) return fail(h, FIPA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -916,10 +914,8 @@ FIPA_API fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_h
   a.delta = static_cast<float*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                     ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256);
-  a.nchunk = sp.nchunk;
-  a.chunk_tiles = sp.chunk_tiles;
   DeviceGuard g(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_bwd_simt(a, s) : fipa::launch_win_bwd_mma(a, s);
+  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_bwd_simt(a, s) : fipa::launch_win_bwd(a, s);
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention backward launch", e);
 }

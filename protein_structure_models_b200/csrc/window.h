@@ -35,7 +35,8 @@ struct WinArgs {
   void *d_q, *d_k, *d_v;             // contiguous
   float* delta;                      // [B,H,Nq] workspace: sum_c d_out out
   float* part;                       // sink partials, see win_sink_plan
-  int nchunk, chunk_tiles;           // sink jobs of a key tile, row tiles of each
+  int nchunk, chunk_tiles;           // sink jobs: chunks, row tiles of 64 each
+  int sink_pos;                      // first position that belongs to them
   int* status;
   unsigned long long timeout_ns;
 };
@@ -45,25 +46,28 @@ constexpr int kWinMaxSinks = 128;
 constexpr int kWinStepRows = 32;       // up to here columns are split instead of rows (window_step.cu)
 
 // The gradient of a sink key sums over every later query, which one CTA would
-// walk alone: the queries beyond the window of the sinks' key tile are cut into
-// `nchunk` chunks of `chunk_tiles` row tiles, whose float32 partial sums (and
-// the window's own) are added in chunk order by win_sink_reduce.
+// walk alone: the queries beyond the window of the key tiles that hold sinks
+// (from position `sink_pos` on) are cut into `nchunk` chunks of `chunk_tiles`
+// tiles of 64 rows, whose float32 partial sums (and the window's own) are added
+// in chunk order by win_sink_reduce.
 struct WinSinkPlan {
-  int nchunk, chunk_tiles, nsink_tiles;
+  int nchunk, chunk_tiles, sink_pos;
   size_t part_floats;
 };
-inline WinSinkPlan win_sink_plan(int B, int Nq, int Nk, int Hkv, int G, int D, int Dv, int left, int sinks, int key_tile,
-                                 int row_tile) {
+inline WinSinkPlan win_sink_plan(const WinArgs& a, int key_tile) {
   WinSinkPlan s{0, 0, 0, 0};
-  if (sinks <= 0 || (long long)key_tile - 1 + left >= Nk - 1) return s;   // the window of tile 0 reaches every position
-  const long long tiles = ((long long)Nq * G + row_tile - 1) / row_tile;
-  s.nsink_tiles = (sinks + key_tile - 1) / key_tile;
-  s.chunk_tiles = 8;                                                     // about the window loop of the other key tiles
-  while ((tiles + s.chunk_tiles - 1) / s.chunk_tiles > 64) s.chunk_tiles *= 2;
+  const long long end = (long long)(a.sinks + key_tile - 1) / key_tile * key_tile;
+  s.sink_pos = (int)(end < a.Nk ? end : a.Nk) + a.left;
+  if (a.sinks <= 0 || s.sink_pos >= a.Nk) return s;          // the window reaches every position
+  const long long tiles = ((long long)a.Nq * a.G + 63) / 64;
+  s.chunk_tiles = 8;
+  while ((tiles + s.chunk_tiles - 1) / s.chunk_tiles > 256) s.chunk_tiles *= 2;
   s.nchunk = (int)((tiles + s.chunk_tiles - 1) / s.chunk_tiles);
-  s.part_floats = (size_t)B * Hkv * (s.nchunk + 1) * sinks * (D + Dv);
+  s.part_floats = (size_t)a.B * a.Hkv * (s.nchunk + 1) * a.sinks * (a.D + a.Dv);
   return s;
 }
+
+constexpr int kWinTcRows = 128, kWinTcCols = 64;      // tile of window_tc.cu
 
 // Whether q, k and v can be read 16 bytes at a time.
 inline bool win_vec(const WinArgs& a) {
@@ -112,9 +116,12 @@ __device__ __forceinline__ bool win_alive(const WinArgs& a, int b, int p) {
 
 cudaError_t launch_win_fwd_simt(const WinArgs& a, cudaStream_t s);       // float32 tensors
 cudaError_t launch_win_bwd_simt(const WinArgs& a, cudaStream_t s);
-cudaError_t launch_win_fwd_mma(const WinArgs& a, cudaStream_t s);        // bfloat16 tensors
+cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s);            // bfloat16 tensors: one of the following
+cudaError_t launch_win_bwd(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_step(const WinArgs& a, cudaStream_t s);           // few rows
-cudaError_t launch_win_bwd_mma(const WinArgs& a, cudaStream_t s);
+cudaError_t launch_win_fwd_tc(const WinArgs& a, cudaStream_t s);         // wide windows
+cudaError_t launch_win_bwd_q_tc(const WinArgs& a, cudaStream_t s);
+cudaError_t launch_win_bwd_k_tc(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s);
 
 constexpr int kWinSimtTile = 64;       // rows and keys of a tile

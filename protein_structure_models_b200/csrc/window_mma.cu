@@ -391,33 +391,31 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
   });
 }
 
-// dk and dv of one key tile over the rows of its window, or (sink jobs) over one chunk of the rows beyond it.
-template <int DP, bool VEC>
+// dk and dv.  SINK false: of one key tile over the rows of its window, a warp 16
+// keys.  SINK true: of 16 keys that hold sinks, over one chunk of the rows beyond
+// the window; the warps take every fourth 16 rows and are added in order.
+template <int DP, bool VEC, bool SINK>
 __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a) {
+  constexpr int KR = SINK ? 16 : T;                     // keys of the CTA
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Ks = reinterpret_cast<bf16*>(smem);
-  bf16* Vs = Ks + kElems<DP>;
-  bf16* Qs = Vs + kElems<DP>;
+  bf16* Vs = Ks + KR * Tile<DP>::ld;
+  bf16* Qs = Vs + KR * Tile<DP>::ld;
   bf16* Os = Qs + 2 * kElems<DP>;
   __shared__ float slse[2][T], sdel[2][T];
   __shared__ int spos[2][T];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
-  const int ktiles = (a.Nk + T - 1) / T;
-  const int nsink = a.nchunk > 0 ? (a.sinks + T - 1) / T : 0;
-  const int jobs = ktiles + nsink * a.nchunk;
-  const int job = blockIdx.x % jobs, bh = blockIdx.x / jobs, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
-  const bool sink_job = job >= ktiles;
-  const int kt = sink_job ? (job - ktiles) / a.nchunk : job;
-  const int chunk = sink_job ? (job - ktiles) % a.nchunk : -1;
-  const int q0 = win_q0(a, b);
-  const int j0 = kt * T, j1 = min(a.Nk, j0 + T) - 1;
-  const bool split = kt < nsink;
-  const int pl = sink_job ? j1 + a.left + 1 : max(0, j0 - a.right);
-  const int ph = sink_job || (j0 < a.sinks && !split) ? a.Nk - 1 : min(a.Nk - 1, j1 + a.left);
+  const int per = SINK ? (a.sinks + 15) / 16 * a.nchunk : (a.Nk + T - 1) / T;
+  const int job = blockIdx.x % per, bh = blockIdx.x / per, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
+  const int chunk = SINK ? job % a.nchunk : -1, q0 = win_q0(a, b);
+  const int j0 = SINK ? job / a.nchunk * 16 : job * T, j1 = min(a.Nk, j0 + KR) - 1, wj = SINK ? 0 : 16 * warp;
+  const bool split = !SINK && a.nchunk > 0 && j0 < a.sinks;
+  const int pl = SINK ? a.sink_pos : max(0, j0 - a.right);
+  const int ph = SINK || (j0 < a.sinks && !split) ? a.Nk - 1 : min(a.Nk - 1, split ? a.sink_pos - 1 : j1 + a.left);
   const int il = max(pl - q0, 0), ih = min(ph - q0, a.Nq - 1);
   int fl = il * a.G, fh = (ih + 1) * a.G;
   if (ih < il) fl = fh = 0;
-  if (sink_job) {
+  if (SINK) {
     fl = max(fl, chunk * a.chunk_tiles * T);
     fh = min(fh, (chunk + 1) * a.chunk_tiles * T);
   }
@@ -428,12 +426,12 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
   int plo[2], phi[2];                                   // positions that see this thread's keys
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int j = j0 + 16 * warp + (lane >> 2) + 8 * i;
+    const int j = j0 + wj + (lane >> 2) + 8 * i;
     alive[i] = j <= j1 && win_alive(a, b, j);
     plo[i] = j - a.right;
     phi[i] = j < a.sinks ? 0x7fffffff : j + a.left;
   }
-  const int ka = j0 + 16 * warp, kb = min(ka + 15, j1);   // keys of the warp
+  const int ka = j0 + wj, kb = min(ka + 15, j1);   // keys of the warp
   const int ntile = __syncthreads_or(alive[0] || alive[1]) && fh > fl ? (fh - fl + T - 1) / T : 0;
   auto load = [&](int t) {
     const int st = t & 1, f0 = fl + t * T;
@@ -470,8 +468,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
     auto keyed = [&](const Src& s) {
       return [&](int r) -> const bf16* { return j0 + r <= j1 && win_alive(a, b, j0 + r) ? s.p + (j0 + r) * s.sn : nullptr; };
     };
-    load_tile<DP, VEC>(Ks, k, T, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP, VEC>(Vs, v, T, threadIdx.x, kThreads, keyed(v));
+    load_tile<DP, VEC>(Ks, k, KR, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP, VEC>(Vs, v, KR, threadIdx.x, kThreads, keyed(v));
     load(0);
   }
   for (int t = 0; t < ntile; ++t) {
@@ -487,6 +485,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       if (fl + t * T + 16 * g >= fh) break;
+      if (SINK && g != warp) continue;
       const int pa = spos[st][16 * g], pb = spos[st][16 * g + 15];
       if (kb < ka || pb < ka - a.right || (pa > kb + a.left && ka >= a.sinks)) continue;
       const bool edge = pa < kb - a.right || pb > ka + a.left;
@@ -499,13 +498,13 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
       for (int kk = 0; kk < DP / 16; ++kk) {
         uint32_t af[4], bf[4];
         if (kk < kd) {
-          ldsm4(af, a_addr<DP>(smem_u32(Ks), 16 * warp, 16 * kk, lane));
+          ldsm4(af, a_addr<DP>(smem_u32(Ks), wj, 16 * kk, lane));
           ldsm4(bf, b_addr<DP>(qs, 16 * g, 16 * kk, lane));
           mma(s[0], af, bf[0], bf[1]);
           mma(s[1], af, bf[2], bf[3]);
         }
         if (kk < kv) {
-          ldsm4(af, a_addr<DP>(smem_u32(Vs), 16 * warp, 16 * kk, lane));
+          ldsm4(af, a_addr<DP>(smem_u32(Vs), wj, 16 * kk, lane));
           ldsm4(bf, b_addr<DP>(os, 16 * g, 16 * kk, lane));
           mma(dp[0], af, bf[0], bf[1]);
           mma(dp[1], af, bf[2], bf[3]);
@@ -543,12 +542,38 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
     }
     __syncthreads();
   }
+  if (SINK) {
+    // the warps' sums, in warp order, in the memory of the tiles
+    constexpr int OL = 2 * DP + 4;
+    float* red = reinterpret_cast<float*>(smem);
+    for (int w = 0; w < 4; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* o = red + ((lane >> 2) + 8 * (e >> 1)) * OL + 8 * n + col2 + (e & 1);
+            o[0] = dk[n][e] + (w == 0 ? 0.f : o[0]);
+            o[DP] = dv[n][e] + (w == 0 ? 0.f : o[DP]);
+          }
+      }
+      __syncthreads();
+    }
+    const int wd = a.D + a.Dv;
+    for (int e = threadIdx.x; e < 16 * wd; e += kThreads) {
+      const int r = e / wd, d = e - r * wd, j = j0 + r;
+      if (j > j1 || j >= a.sinks) continue;
+      const bool on = a.mask == nullptr || a.mask[(long long)b * a.Nk + j] != 0;
+      a.part[(((long long)bh * (a.nchunk + 1) + chunk + 1) * a.sinks + j) * wd + d] = on ? red[r * OL + (d < a.D ? d : DP + d - a.D)] : 0.f;
+    }
+    return;
+  }
   if (split) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int j = j0 + 16 * warp + (lane >> 2) + 8 * i;
+      const int j = j0 + wj + (lane >> 2) + 8 * i;
       if (j > j1 || j >= a.sinks) continue;
-      float* o = a.part + (((long long)bh * (a.nchunk + 1) + chunk + 1) * a.sinks + j) * (a.D + a.Dv);
+      float* o = a.part + ((long long)bh * (a.nchunk + 1) * a.sinks + j) * (a.D + a.Dv);
 #pragma unroll
       for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
@@ -558,10 +583,9 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
           if (d < a.Dv) o[a.D + d] = alive[i] ? dv[n][2 * i + e] : 0.f;
         }
     }
-    if (sink_job) return;
   }
   auto at = [&](void* base, int width, int i, bool& keep) -> bf16* {
-    const int j = j0 + 16 * warp + (lane >> 2) + 8 * i;
+    const int j = j0 + wj + (lane >> 2) + 8 * i;
     keep = alive[i];
     return j <= j1 && !(split && j < a.sinks) ? static_cast<bf16*>(base) + (((long long)b * a.Nk + j) * a.Hkv + hkv) * width : nullptr;
   };
@@ -579,41 +603,65 @@ cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
 }
 
 template <int DP, bool VEC>
-cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
-  const size_t smem = 6 * kElems<DP> * sizeof(bf16);
-  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP, VEC>));
+cudaError_t bwd_q(const WinArgs& a, cudaStream_t s) {
+  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP, VEC>));
   if (e != cudaSuccess) return e;
-  e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP, VEC>));
-  if (e != cudaSuccess) return e;
-  const long long gq = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
-  win_bwd_q_mma_kernel<DP, VEC><<<(unsigned)gq, kThreads, smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int nsink = a.nchunk > 0 ? (a.sinks + T - 1) / T : 0;
-  const long long gk = (long long)a.B * a.Hkv * ((a.Nk + T - 1) / T + (long long)nsink * a.nchunk);
-  win_bwd_k_mma_kernel<DP, VEC><<<(unsigned)gk, kThreads, smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return a.nchunk > 0 ? launch_win_sink_reduce(a, 0, s) : cudaSuccess;
+  const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
+  win_bwd_q_mma_kernel<DP, VEC><<<(unsigned)grid, kThreads, 6 * kElems<DP> * sizeof(bf16), s>>>(a);
+  return cudaGetLastError();
 }
-
+template <int DP, bool VEC, bool SINK>
+cudaError_t bwd_k(const WinArgs& a, cudaStream_t s) {
+  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP, VEC, SINK>));
+  if (e != cudaSuccess) return e;
+  const long long grid = (long long)a.B * a.Hkv * (SINK ? (long long)(a.sinks + 15) / 16 * a.nchunk : (a.Nk + T - 1) / T);
+  const size_t smem = (size_t)(2 * (SINK ? 16 : T) + 4 * T) * Tile<DP>::ld * sizeof(bf16);
+  win_bwd_k_mma_kernel<DP, VEC, SINK><<<(unsigned)grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <int DP, bool VEC>
+cudaError_t bwd(const WinArgs& a, bool tc, cudaStream_t s) {
+  cudaError_t e = tc ? launch_win_bwd_q_tc(a, s) : bwd_q<DP, VEC>(a, s);
+  if (e == cudaSuccess) e = tc ? launch_win_bwd_k_tc(a, s) : bwd_k<DP, VEC, false>(a, s);
+  if (e == cudaSuccess && a.nchunk > 0) e = bwd_k<DP, VEC, true>(a, s);
+  if (e == cudaSuccess && a.nchunk > 0) e = launch_win_sink_reduce(a, 0, s);
+  return e;
+}
 template <int DP>
 cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
   return win_vec(a) ? fwd<DP, true>(a, s) : fwd<DP, false>(a, s);
 }
 template <int DP>
-cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
-  return win_vec(a) && (reinterpret_cast<uintptr_t>(a.d_out) & 15) == 0 ? bwd<DP, true>(a, s) : bwd<DP, false>(a, s);
+cudaError_t bwd(const WinArgs& a, bool tc, cudaStream_t s) {
+  return win_vec(a) && (reinterpret_cast<uintptr_t>(a.d_out) & 15) == 0 ? bwd<DP, true>(a, tc, s) : bwd<DP, false>(a, false, s);
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Whether the tcgen05 kernels take a call.
+bool use_tc(const WinArgs& a, bool backward) {
+  if (!win_vec(a) || !on16(a.out)) return false;
+  if (backward && !(on16(a.d_out) && on16(a.d_q) && on16(a.d_k) && on16(a.d_v))) return false;
+  return true;
 }
 
 }  // namespace
 
-cudaError_t launch_win_fwd_mma(const WinArgs& a, cudaStream_t s) {
+cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s) {
   if ((long long)a.Nq * a.G <= kWinStepRows) return launch_win_step(a, s);
+  if (use_tc(a, false)) return launch_win_fwd_tc(a, s);
   const int w = a.D > a.Dv ? a.D : a.Dv;
   return w <= 16 ? fwd<16>(a, s) : (w <= 32 ? fwd<32>(a, s) : (w <= 64 ? fwd<64>(a, s) : fwd<128>(a, s)));
 }
-cudaError_t launch_win_bwd_mma(const WinArgs& a, cudaStream_t s) {
+cudaError_t launch_win_bwd(const WinArgs& in, cudaStream_t s) {
+  WinArgs a = in;
+  const bool tc = use_tc(a, true);
+  const WinSinkPlan sp = win_sink_plan(a, tc ? kWinTcRows : T);
+  a.nchunk = sp.nchunk;
+  a.chunk_tiles = sp.chunk_tiles;
+  a.sink_pos = sp.sink_pos;
   const int w = a.D > a.Dv ? a.D : a.Dv;
-  return w <= 16 ? bwd<16>(a, s) : (w <= 32 ? bwd<32>(a, s) : (w <= 64 ? bwd<64>(a, s) : bwd<128>(a, s)));
+  return w <= 16 ? bwd<16>(a, tc, s) : (w <= 32 ? bwd<32>(a, tc, s) : (w <= 64 ? bwd<64>(a, tc, s) : bwd<128>(a, tc, s)));
 }
 
 }  // namespace fipa

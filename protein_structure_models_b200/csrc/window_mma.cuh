@@ -95,14 +95,14 @@ __device__ __forceinline__ uint32_t bt_addr(uint32_t base, int k0, int n0, int l
   return base + 2 * ((k0 + (lane & 7) + (((lane >> 3) & 1) << 3)) * Tile<DP>::ld + n0 + ((lane >> 4) << 3));
 }
 
-// Columns that the 16 rows of a warp see: any of them, and all of them.
+// Columns that neighbouring rows see: any of them, and all of them (n columns from u on).
 struct Reach {
   int s_any, s_all, a_any, a_all, e_any, e_all;       // sinks [0, s), window [a, e)
-  __device__ __forceinline__ bool any(int u) const { return u < s_any || (u + 15 >= a_any && u < e_any); }
-  __device__ __forceinline__ bool all(int u) const { return u + 15 < s_all || (u >= a_all && u + 15 < e_all); }
+  __device__ __forceinline__ bool any(int u, int n = 16) const { return u < s_any || (u + n > a_any && u < e_any); }
+  __device__ __forceinline__ bool all(int u, int n = 16) const { return u + n <= s_all || (u >= a_all && u + n <= e_all); }
 };
-__device__ __forceinline__ Reach reach(const WinArgs& a, const WinCols& c, int q0, int f, int f1) {
-  const int lo = min(max(q0 + f / a.G, 0), a.Nk - 1), hi = min(max(q0 + (min(f + 16, f1) - 1) / a.G, 0), a.Nk - 1);
+__device__ __forceinline__ Reach reach(const WinArgs& a, const WinCols& c, int q0, int f, int f1, int rows = 16) {
+  const int lo = min(max(q0 + f / a.G, 0), a.Nk - 1), hi = min(max(q0 + (min(f + rows, f1) - 1) / a.G, 0), a.Nk - 1);
   const WinRow x = win_row(a, c, lo, true), y = win_row(a, c, hi, true);
   if (f >= f1) return Reach{0, 0, 0, 0, 0, 0};
   return Reach{y.s1, x.s1, x.w0, y.w0, y.w1, x.w1};

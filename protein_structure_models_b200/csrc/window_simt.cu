@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_simt_kernel(const WinArgs 
   const int j0 = kt * T, j1 = min(a.Nk, j0 + T) - 1;
   const bool split = kt < nsink;
   // positions whose rows this job sums over
-  int pl = sink_job ? j1 + a.left + 1 : max(0, j0 - a.right);
-  int ph = sink_job || (j0 < a.sinks && !split) ? a.Nk - 1 : min(a.Nk - 1, j1 + a.left);
+  const int pl = sink_job ? a.sink_pos : max(0, j0 - a.right);
+  const int ph = sink_job || (j0 < a.sinks && !split) ? a.Nk - 1 : min(a.Nk - 1, split ? a.sink_pos - 1 : j1 + a.left);
   const int il = max(pl - q0, 0), ih = min(ph - q0, a.Nq - 1);
   int fl = il * a.G, fh = (ih + 1) * a.G;
   if (ih < il) fl = fh = 0;
@@ -376,17 +376,26 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_simt_kernel(const WinArgs 
   }
 }
 
-// dk, dv of the sinks: the partial sums in chunk order.
+// dk, dv of the sinks: the partial sums in chunk order, in eight neighbouring stretches that are added in order.
 template <typename E>
-__global__ void win_sink_reduce_kernel(const WinArgs a) {
+__global__ void __launch_bounds__(256) win_sink_reduce_kernel(const WinArgs a) {
+  __shared__ float red[8][32];
   const int w = a.D + a.Dv, bh = blockIdx.x / a.sinks, j = blockIdx.x - bh * a.sinks, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
-  for (int d = threadIdx.x; d < w; d += blockDim.x) {
-    float x = 0.f;
-    for (int ch = 0; ch <= a.nchunk; ++ch) x += a.part[(((long long)bh * (a.nchunk + 1) + ch) * a.sinks + j) * w + d];
-    const long long r = ((long long)b * a.Nk + j) * a.Hkv + hkv;
-    if (d < a.D) stf(static_cast<E*>(a.d_k) + r * a.D + d, x * a.scale);
-    else stf(static_cast<E*>(a.d_v) + r * a.Dv + (d - a.D), x);
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, d = blockIdx.y * 32 + lane, per = (a.nchunk + 8) / 8;
+  float x = 0.f;
+  if (d < w) {
+    const float* p = a.part + ((long long)bh * (a.nchunk + 1) * a.sinks + j) * w + d;
+    const int hi = min((part + 1) * per, a.nchunk + 1);
+#pragma unroll 8
+    for (int ch = part * per; ch < hi; ++ch) x += p[(long long)ch * a.sinks * w];
   }
+  red[part][lane] = x;
+  __syncthreads();
+  if (part != 0 || d >= w) return;
+  for (int k = 1; k < 8; ++k) x += red[k][lane];
+  const long long r = ((long long)b * a.Nk + j) * a.Hkv + hkv;
+  if (d < a.D) stf(static_cast<E*>(a.d_k) + r * a.D + d, x * a.scale);
+  else stf(static_cast<E*>(a.d_v) + r * a.Dv + (d - a.D), x);
 }
 
 template <typename E, int NC>
@@ -419,16 +428,21 @@ cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s) {
-  const unsigned grid = (unsigned)(a.B * a.Hkv * a.sinks);
-  if (f32) win_sink_reduce_kernel<float><<<grid, 128, 0, s>>>(a);
-  else win_sink_reduce_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
+  const dim3 grid((unsigned)((long long)a.B * a.Hkv * a.sinks), (unsigned)((a.D + a.Dv + 31) / 32));
+  if (f32) win_sink_reduce_kernel<float><<<grid, 256, 0, s>>>(a);
+  else win_sink_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 cudaError_t launch_win_fwd_simt(const WinArgs& a, cudaStream_t s) {
   const int nc = (a.Dv + 15) / 16;
   return nc <= 2 ? fwd<float, 2>(a, s) : (nc <= 4 ? fwd<float, 4>(a, s) : fwd<float, 8>(a, s));
 }
-cudaError_t launch_win_bwd_simt(const WinArgs& a, cudaStream_t s) {
+cudaError_t launch_win_bwd_simt(const WinArgs& in, cudaStream_t s) {
+  WinArgs a = in;
+  const WinSinkPlan sp = win_sink_plan(a, T);
+  a.nchunk = sp.nchunk;
+  a.chunk_tiles = sp.chunk_tiles;
+  a.sink_pos = sp.sink_pos;
   const int nc = ((a.D > a.Dv ? a.D : a.Dv) + 15) / 16;
   return nc <= 2 ? bwd<float, 2>(a, s) : (nc <= 4 ? bwd<float, 4>(a, s) : bwd<float, 8>(a, s));
 }
