@@ -126,13 +126,12 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
         mma(s[2 * g + 1], qf[kk], bf[2], bf[3]);
       }
       if (wg != 0xffffu || !rc.all(u0 + 16 * g)) {
+        const uint32_t on[2] = {wg & row[0].sees(u0 + 16 * g), wg & row[1].sees(u0 + 16 * g)};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int u = 16 * g + 8 * h + col2 + (e & 1);
-            if (!((wg >> (u & 15)) & 1u) || !row[e >> 1].sees(u0 + u)) s[2 * g + h][e] = -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e)
+            s[2 * g + h][e] = (on[e >> 1] >> (8 * h + col2 + (e & 1))) & 1u ? s[2 * g + h][e] : -INFINITY;
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -360,18 +359,17 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
           mma(dp[1], af, bf[2], bf[3]);
         }
       }
-      const bool edge = wg != 0xffffu || !rc.all(u0 + 16 * g);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = e >> 1;
-          s[h][e] = ex2_approx(fmaf(s[h][e], sc, -lse2[i])) * (dp[h][e] - del[i]);
-          if (edge) {
-            const int u = 8 * h + col2 + (e & 1);
-            if (!((wg >> u) & 1u) || !row[i].sees(u0 + 16 * g + u)) s[h][e] = 0.f;
-          }
-        }
+        for (int e = 0; e < 4; ++e) s[h][e] = ex2_approx(fmaf(s[h][e], sc, -lse2[e >> 1])) * (dp[h][e] - del[e >> 1]);
+      if (wg != 0xffffu || !rc.all(u0 + 16 * g)) {
+        const uint32_t on[2] = {wg & row[0].sees(u0 + 16 * g), wg & row[1].sees(u0 + 16 * g)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[h][e] = (on[e >> 1] >> (8 * h + col2 + (e & 1))) & 1u ? s[h][e] : 0.f;
+      }
       const uint32_t pf[4] = {pack(s[0][0], s[0][1]), pack(s[0][2], s[0][3]), pack(s[1][0], s[1][1]), pack(s[1][2], s[1][3])};
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
@@ -423,13 +421,12 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
   const Src g_ = source(a.d_out, (long long)a.Nq * a.H * a.Dv, (long long)a.H * a.Dv, a.Dv, a.Dv, b, hkv * a.G);
   const Src k = source(a.k, a.kb, a.kn, a.kh, a.D, b, hkv), v = source(a.v, a.vb, a.vn, a.vh, a.Dv, b, hkv);
   bool alive[2];
-  int plo[2], phi[2];                                   // positions that see this thread's keys
+  int rlo[2], rhi[2];                                   // rows, counted from fl, that see this thread's keys
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int j = j0 + wj + (lane >> 2) + 8 * i;
     alive[i] = j <= j1 && win_alive(a, b, j);
-    plo[i] = j - a.right;
-    phi[i] = j < a.sinks ? 0x7fffffff : j + a.left;
+    key_rows(a, q0, j, fl, fh, rlo[i], rhi[i]);
   }
   const int ka = j0 + wj, kb = min(ka + 15, j1);   // keys of the warp
   const int ntile = __syncthreads_or(alive[0] || alive[1]) && fh > fl ? (fh - fl + T - 1) / T : 0;
@@ -488,7 +485,11 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
       if (SINK && g != warp) continue;
       const int pa = spos[st][16 * g], pb = spos[st][16 * g + 15];
       if (kb < ka || pb < ka - a.right || (pa > kb + a.left && ka >= a.sinks)) continue;
-      const bool edge = pa < kb - a.right || pb > ka + a.left;
+      uint32_t on[2] = {0xffffu, 0xffffu};
+      if (pa < kb - a.right || pb > ka + a.left) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) on[i] = win_span(rlo[i] - t * T - 16 * g, rhi[i] - t * T - 16 * g);
+      }
       float s[2][4], dp[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -515,11 +516,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 16 * g + 8 * h + col2 + (e & 1), i = e >> 1;
-          float p = ex2_approx(fmaf(s[h][e], sc, -slse[st][r]));
-          if (edge) {
-            const int pos = spos[st][r];
-            if (pos < plo[i] || pos > phi[i]) p = 0.f;
-          }
+          const float x = ex2_approx(fmaf(s[h][e], sc, -slse[st][r])), p = (on[i] >> (r - 16 * g)) & 1u ? x : 0.f;
           s[h][e] = p;
           dp[h][e] = p * (dp[h][e] - sdel[st][r]);
         }

@@ -108,6 +108,13 @@ __device__ __forceinline__ Reach reach(const WinArgs& a, const WinCols& c, int q
   return Reach{y.s1, x.s1, x.w0, y.w0, y.w1, x.w1};
 }
 
+// Rows f, counted from fl and at most to fh, of the positions that see key j.
+__device__ __forceinline__ void key_rows(const WinArgs& a, int q0, int j, int fl, int fh, int& lo, int& hi) {
+  const long long x = ((long long)j - a.right - q0) * a.G - fl, y = ((long long)j + a.left + 1 - q0) * a.G - fl, n = fh - fl;
+  lo = (int)(x < 0 ? 0 : (x < n ? x : n));
+  hi = (int)(j < a.sinks ? n : (y < 0 ? 0 : (y < n ? y : n)));
+}
+
 // Writes a warp's 16 x DP sums as bfloat16 rows; at(i) is the row of this thread's half i, null: not written.
 template <int DP, typename At>
 __device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], int width, const void* base, float f, int lane, At at) {

@@ -141,13 +141,16 @@ __global__ void __launch_bounds__(kThreads) win_fwd_simt_kernel(const WinArgs a)
     __syncthreads();
     float s[4][4];
     product(Qs, Ks, a.D, ty, tx, s);
+    uint32_t lv = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lv |= live[4 * tx + j] ? 1u << j : 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float mx = -INFINITY;
+      const uint32_t on = row[i].sees(u0 + 4 * tx) & lv;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int u = 4 * tx + j;
-        s[i][j] = live[u] && row[i].sees(u0 + u) ? s[i][j] * a.scale : -INFINITY;
+        s[i][j] = (on >> j) & 1u ? s[i][j] * a.scale : -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
       const float mn = fmaxf(m[i], max16(mx));
@@ -241,14 +244,16 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_simt_kernel(const WinArgs 
     __syncthreads();
     float s[4][4], dp[4][4];
     product(Qs, Ks, a.D, ty, tx, s);
+    uint32_t lv = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lv |= live[4 * tx + j] ? 1u << j : 0u;
     product(Os, Vs, a.Dv, ty, tx, dp);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const uint32_t on = row[i].sees(u0 + 4 * tx) & lv;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int u = 4 * tx + j;
-        const bool on_ = live[u] && row[i].sees(u0 + u);
-        s[i][j] = on_ ? expf(s[i][j] * a.scale - lse[i]) * (dp[i][j] - del[i]) : 0.f;
+        s[i][j] = (on >> j) & 1u ? expf(s[i][j] * a.scale - lse[i]) * (dp[i][j] - del[i]) : 0.f;
       }
       *reinterpret_cast<float4*>(Ps + (4 * ty + i) * LD + 4 * tx) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
     }

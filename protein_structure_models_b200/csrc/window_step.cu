@@ -168,13 +168,11 @@ __global__ void __launch_bounds__(kWarps * 32, DP <= 16 ? 5 : (DP <= 64 ? 4 : 2)
     load_k(kw, t + AHEAD, next);
     if (some) {
       if (now != 0xffffu || !rc.all(u0)) {
+        const uint32_t on[2] = {now & row[0].sees(u0), now & row[1].sees(u0)};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int u = 8 * h + 2 * c4 + (e & 1);
-            if (!((now >> u) & 1u) || !row[e >> 1].sees(u0 + u)) s[h][e] = -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e) s[h][e] = (on[e >> 1] >> (8 * h + 2 * c4 + (e & 1))) & 1u ? s[h][e] : -INFINITY;
       }
       float mb[2], mx[2];
 #pragma unroll

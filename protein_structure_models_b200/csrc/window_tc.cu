@@ -74,6 +74,24 @@ __device__ __forceinline__ void copy_rows(uint32_t d0, uint32_t d1, const bf16* 
   }
 }
 
+// mbar_wait without the sleep: a tile's chain has four hand-overs, and a warp
+// that sleeps through one comes back a microsecond late.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int site) {
+  uint64_t t0 = 0;
+  for (;;) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*w.abort) return false;
+    if (t0 == 0) t0 = global_timer_ns();
+    if (global_timer_ns() - t0 > w.timeout_ns) {
+      *w.abort = 1;
+      atomicCAS(w.status, 0, kDeviceTimeout | (site << 8));
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity))
@@ -203,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     for (int t = 0; t <= ntile; ++t) {
       if (t < ntile) {
         const int st = t % NS, u0 = t * kCols;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((t / NS) & 1) ^ 1u, wc, 81))) break;
+        if (!__all_sync(0xffffffffu, wait(&empty[st], ((t / NS) & 1) ^ 1u, wc, 81))) break;
         const uint32_t d0 = sB + st * 2 * L::B;
         uint8_t* inf = smem + L::info + st * (MODE == kKeySide ? 768 : 8);
         if (kRowsAreQueries) {
@@ -249,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       for (int t = 0; t < ntile; ++t) {
         const int st = t % NS;
         const uint32_t b0 = sB + st * 2 * L::B, b1 = b0 + L::B;
-        if (!mbar_wait(&full[st], (t / NS) & 1, wc, 82)) break;
-        if (t > 0 && !mbar_wait(pv_done, (t - 1) & 1, wc, 83)) break;      // S takes the place of the last P
+        if (!wait(&full[st], (t / NS) & 1, wc, 82)) break;
+        if (t > 0 && !wait(pv_done, (t - 1) & 1, wc, 83)) break;      // S takes the place of the last P
         tc_fence_after();
         for (int kk = 0; kk < kd; ++kk) {
           const uint32_t o = (kk & 3) * 32;
@@ -265,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           }
         }
         tc_commit(s_full);
-        if (!mbar_wait(p_full, t & 1, wc, 84)) break;
+        if (!wait(p_full, t & 1, wc, 84)) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kCols / 16; ++kk) {
@@ -287,14 +305,13 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
     WinRow row{0, 0, 0};
     Reach rc{0, 0, 0, 0, 0, 0};
-    int plo = 0, phi = 0;
+    int rlo = 0, rhi = 0;                                   // columns that see this thread's key
     const int first = r0 + 32 * warp, last = min(first + 31, r1 - 1);
     if (kRowsAreQueries) {
       row = win_row(a, c, pos, alive);
       if (first < r1) rc = reach(a, c, q0, first, last + 1, 32);
     } else {
-      plo = pos - a.right;
-      phi = pos < a.sinks ? 0x7fffffff : pos + a.left;
+      key_rows(a, q0, pos, fl, fl + n, rlo, rhi);
     }
     if (MODE == kRowSide && mine < r1) {
       const int i = mine / a.G, h = hkv * a.G + (mine - i * a.G);
@@ -319,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     for (int t = 0; t < ntile; ++t) {
       const int st = t % NS, u0 = t * kCols;
       const uint8_t* inf = smem + L::info + st * (MODE == kKeySide ? 768 : 8);
-      const bool there = mbar_wait(&full[st], (t / NS) & 1, wc, 85) && mbar_wait(s_full, t & 1, wc, 86);   // the tile's bits or row data; S
+      const bool there = wait(&full[st], (t / NS) & 1, wc, 85) && wait(s_full, t & 1, wc, 86);   // the tile's bits or row data; S
       if (!__all_sync(0xffffffffu, there)) break;
       tc_fence_after();
       if (MODE == kFwd) {
@@ -330,9 +347,9 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           tmem_ld32(trow + L::S + 32 * h, s);
           tmem_ld_wait();
           if (edge) {
+            const uint32_t on = w[h] & row.sees(u0 + 32 * h);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((w[h] >> e) & 1u) || !row.sees(u0 + 32 * h + e)) s[e] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e) s[e] = (on >> e) & 1u ? s[e] : __float_as_uint(-INFINITY);
           }
         };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -389,9 +406,9 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           for (int e = 0; e < 32; ++e)
             s[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(s[e]), sc, -lse2)) * (__uint_as_float(d[e]) - del));
           if (edge) {
+            const uint32_t on = w[h] & row.sees(u0 + 32 * h);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((w[h] >> e) & 1u) || !row.sees(u0 + 32 * h + e)) s[e] = 0u;
+            for (int e = 0; e < 32; ++e) s[e] = (on >> e) & 1u ? s[e] : 0u;
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) p[e] = pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
@@ -408,17 +425,14 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           tmem_ld32(trow + L::S + 32 * h, s);
           tmem_ld32(trow + L::dP + 32 * h, d);
           tmem_ld_wait();
+          const uint32_t on = edge ? win_span(rlo - u0 - 32 * h, rhi - u0 - 32 * h) : 0xffffffffu;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 x = *reinterpret_cast<const float4*>(sl + 32 * h + e), y = *reinterpret_cast<const float4*>(sl + 64 + 32 * h + e);
             const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-              float pr = ex2_approx(fmaf(__uint_as_float(s[e + z]), sc, -xs[z]));
-              if (edge) {
-                const int ps = sp[32 * h + e + z];
-                if (ps < plo || ps > phi) pr = 0.f;
-              }
+              const float ex = ex2_approx(fmaf(__uint_as_float(s[e + z]), sc, -xs[z])), pr = (on >> (e + z)) & 1u ? ex : 0.f;
               s[e + z] = __float_as_uint(pr);
               d[e + z] = __float_as_uint(pr * (__uint_as_float(d[e + z]) - ys[z]));
             }
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       tc_fence_before();
       mbar_arrive(p_full);
     }
-    bool done = ntile > 0 && mbar_wait(pv_done, (ntile - 1) & 1, wc, 87);
+    bool done = ntile > 0 && wait(pv_done, (ntile - 1) & 1, wc, 87);
     done = __all_sync(0xffffffffu, done);
     tc_fence_after();
     const bool ok = done || ntile == 0;                     // after a wait that ran out nothing is written
