@@ -55,40 +55,86 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-// Copies rows of two tensors (widths w0, w1, multiples of 8) into swizzled tiles;
-// neighbouring threads take neighbouring 16-byte pieces.  at(r, p0, p1) gives the
-// rows, or false for rows of zeros.  Channels up to the next multiple of 16 are zeros.
-template <typename At>
-__device__ __forceinline__ void copy_rows(uint32_t d0, uint32_t d1, const bf16* any, int w0, int w1, int rows, int me, int threads, At at) {
-  const int w = w0 > w1 ? w0 : w1;
-  const int lg = w <= 16 ? 1 : (w <= 32 ? 2 : (w <= 64 ? 3 : 4)), c = me & ((1 << lg) - 1);
-  const bool in0 = c * 8 < w0, in1 = c * 8 < w1;
-  const bool z0 = c * 8 < ((w0 + 15) & ~15), z1 = c * 8 < ((w1 + 15) & ~15);
-  const uint32_t chunk = (uint32_t)(c >> 3) * rows * 128;
-  for (int r = me >> lg; r < rows; r += threads >> lg) {
-    const bf16 *p0, *p1;
-    const bool on = at(r, p0, p1);
-    const uint32_t o = chunk + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-    if (z0) cp16_zfill(d0 + o, on && in0 ? p0 + c * 8 : any, on && in0);
-    if (z1) cp16_zfill(d1 + o, on && in1 ? p1 + c * 8 : any, on && in1);
+// A walk over rows of two tensors: the row that this thread copies next.  Keys
+// step by a fixed distance; the row f = i G + h of the queries carries from h to
+// i.  Additions only: a division a row kept the copies behind the products.
+struct Walk {
+  const bf16 *p0, *p1;
+  long long d0, d1, c0, c1;               // a step, and what a carry adds
+  int i, h, di, dh, G;
+  __device__ __forceinline__ void next() {
+    p0 += d0;
+    p1 += d1;
+    i += di;
+    h += dh;
+    if (h >= G) {
+      h -= G;
+      ++i;
+      p0 += c0;
+      p1 += c1;
+    }
   }
+};
+__device__ __forceinline__ Walk walk_queries(const WinArgs& a, const Src& q, const Src& g, int f, int step) {
+  Walk w;
+  w.G = a.G;
+  w.i = f / a.G;
+  w.h = f - w.i * a.G;
+  w.di = step / a.G;
+  w.dh = step - w.di * a.G;
+  w.p0 = q.p + w.i * q.sn + w.h * q.sh;
+  w.p1 = g.p + w.i * g.sn + w.h * g.sh;
+  w.d0 = w.di * q.sn + w.dh * q.sh;
+  w.d1 = w.di * g.sn + w.dh * g.sh;
+  w.c0 = q.sn - a.G * q.sh;
+  w.c1 = g.sn - a.G * g.sh;
+  return w;
+}
+__device__ __forceinline__ Walk walk_keys(const Src& k, const Src& v, int j, int step) {
+  Walk w;
+  w.G = 0x7fffffff;
+  w.h = 0;
+  w.dh = 0;
+  w.i = j;
+  w.di = step;
+  w.p0 = k.p + j * k.sn;
+  w.p1 = v.p + j * v.sn;
+  w.d0 = step * k.sn;
+  w.d1 = step * v.sn;
+  w.c0 = w.c1 = 0;
+  return w;
 }
 
-// mbar_wait without the sleep: a tile's chain has four hand-overs, and a warp
-// that sleeps through one comes back a microsecond late.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int site) {
-  uint64_t t0 = 0;
-  for (;;) {
-#pragma unroll 1
-    for (int k = 0; k < 64; ++k)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*w.abort) return false;
-    if (t0 == 0) t0 = global_timer_ns();
-    if (global_timer_ns() - t0 > w.timeout_ns) {
-      *w.abort = 1;
-      atomicCAS(w.status, 0, kDeviceTimeout | (site << 8));
-      return false;
-    }
+// This thread's part of a tile of rows: neighbouring threads take neighbouring
+// 16-byte pieces (2^lg a row), so that a thread's piece and its place in the
+// swizzle stay the same from row to row.
+struct Piece {
+  int lg, c, first, step;                  // pieces a row, this one, first row, rows between two of this thread's
+  bool in0, in1, z0, z1;                   // inside the tensors' widths; inside them rounded up to 16 channels
+  __device__ __forceinline__ Piece(int w0, int w1, int me, int threads) {
+    const int w = w0 > w1 ? w0 : w1;
+    lg = w <= 16 ? 1 : (w <= 32 ? 2 : (w <= 64 ? 3 : 4));
+    c = me & ((1 << lg) - 1);
+    first = me >> lg;
+    step = threads >> lg;
+    in0 = c * 8 < w0;
+    in1 = c * 8 < w1;
+    z0 = c * 8 < ((w0 + 15) & ~15);
+    z1 = c * 8 < ((w1 + 15) & ~15);
+  }
+};
+// Rows first, first + step, ... below `end` of a tile of `rows`, of which those below n exist; valid(i): row i is not masked.
+template <typename Valid>
+__device__ __forceinline__ void copy_rows(uint32_t d0, uint32_t d1, const Piece& pc, Walk w, int rows, int end, int n, Valid valid) {
+  const uint32_t chunk = (uint32_t)(pc.c >> 3) * rows * 128;
+  const bf16 *a0 = w.p0, *a1 = w.p1;       // somewhere readable
+#pragma unroll 4
+  for (int r = pc.first; r < end; r += pc.step) {
+    const bool on = r < n && valid(w.i);
+    const uint32_t o = chunk + (uint32_t)r * 128 + (uint32_t)(((pc.c & 7) ^ (r & 7)) << 4);
+    if (pc.z0) cp16_zfill(d0 + o, on && pc.in0 ? w.p0 + pc.c * 8 : a0, on && pc.in0);
+    if (pc.z1) cp16_zfill(d1 + o, on && pc.in1 ? w.p1 + pc.c * 8 : a1, on && pc.in1);
+    w.next();
   }
 }
 
@@ -157,17 +203,9 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
   const Src q = source(a.q, a.qb, a.qn, a.qh, a.D, b, hkv * a.G);
   const Src g = source(a.d_out, (long long)a.Nq * a.H * a.Dv, (long long)a.H * a.Dv, a.Dv, a.Dv, b, hkv * a.G);
   const Src k = source(a.k, a.kb, a.kn, a.kh, a.D, b, hkv), v = source(a.v, a.vb, a.vn, a.vh, a.Dv, b, hkv);
-  auto query = [&](int f, const bf16*& p0, const bf16*& p1) -> bool {
-    const int i = f / a.G, h = f - i * a.G;
-    p0 = q.p + i * q.sn + h * q.sh;
-    p1 = g.p + i * g.sn + h * g.sh;
-    return win_alive(a, b, q0 + i);
-  };
-  auto key = [&](int j, const bf16*& p0, const bf16*& p1) -> bool {
-    p0 = k.p + j * k.sn;
-    p1 = v.p + j * v.sn;
-    return a.mask == nullptr || a.mask[(long long)b * a.Nk + j] != 0;
-  };
+  const uint8_t* mask = a.mask == nullptr ? nullptr : a.mask + (long long)b * a.Nk;
+  auto key_valid = [&](int j) { return mask == nullptr || mask[j] != 0; };
+  auto query_valid = [&](int i) { return q0 + i >= 0 && q0 + i < a.Nk && key_valid(q0 + i); };
   // this thread's row
   bool alive = false;
   int mine = r0 + (int)threadIdx.x, pos = 0;
@@ -194,16 +232,11 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     tmem_relinquish();
   }
   if (ntile > 0) {
-    if (MODE == kFwd) {
-      copy_rows(sA, sA, q.p, a.D, 0, kRows, threadIdx.x < 128 ? threadIdx.x : 1 << 20, 128, [&](int r, const bf16*& p0, const bf16*& p1) {
-        return r0 + r < r1 && query(r0 + r, p0, p1);
-      });
-    } else {
-      copy_rows(sA, sA + L::A, kRowsAreQueries ? q.p : k.p, a.D, a.Dv, kRows, threadIdx.x < 128 ? threadIdx.x : 1 << 20, 128,
-                [&](int r, const bf16*& p0, const bf16*& p1) {
-                  return r0 + r < r1 && (kRowsAreQueries ? query(r0 + r, p0, p1) : key(r0 + r, p0, p1));
-                });
-    }
+    const int me = threadIdx.x < 128 ? (int)threadIdx.x : 1 << 20;        // the first 128 threads
+    const Piece pc(a.D, MODE == kFwd ? 0 : a.Dv, me, 128);
+    const int r = min(r0 + pc.first, r1 - 1);
+    if (kRowsAreQueries) copy_rows(sA, sA + L::A, pc, walk_queries(a, q, MODE == kFwd ? q : g, r, pc.step), kRows, kRows, r1 - r0, query_valid);
+    else copy_rows(sA, sA + L::A, pc, walk_keys(k, v, r, pc.step), kRows, kRows, r1 - r0, key_valid);
     cp_async_wait_all();
     fence_proxy_async_smem();
   }
@@ -218,24 +251,28 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
   if (warp >= 5) {
     // ------------------------------------------------------------- copies
     const int me = threadIdx.x - 160;
+    const Piece pc(a.D, a.Dv, me, kLoaders);
     for (int t = 0; t <= ntile; ++t) {
       if (t < ntile) {
         const int st = t % NS, u0 = t * kCols;
-        if (!__all_sync(0xffffffffu, wait(&empty[st], ((t / NS) & 1) ^ 1u, wc, 81))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((t / NS) & 1) ^ 1u, wc, 81))) break;
         const uint32_t d0 = sB + st * 2 * L::B;
         uint8_t* inf = smem + L::info + st * (MODE == kKeySide ? 768 : 8);
         if (kRowsAreQueries) {
-          copy_rows(d0, d0 + L::B, k.p, a.D, a.Dv, kCols, me, kLoaders, [&](int r, const bf16*& p0, const bf16*& p1) {
-            return u0 + r < n && key(c.key(u0 + r), p0, p1);
-          });
+          // sinks first, then the window; a tile may hold the seam
+          const int ns = min(max(c.s - u0, 0), kCols);
+          if (ns > 0) copy_rows(d0, d0 + L::B, pc, walk_keys(k, v, min(u0 + pc.first, a.Nk - 1), pc.step), kCols, ns, ns, key_valid);
+          if (ns < kCols) {
+            Piece pw = pc;
+            while (pw.first < ns) pw.first += pw.step;
+            copy_rows(d0, d0 + L::B, pw, walk_keys(k, v, min(c.key(u0 + pw.first), a.Nk - 1), pw.step), kCols, kCols, n - u0, key_valid);
+          }
           const int u = u0 + me;
-          const bool on = u < n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0);
+          const bool on = u < n && key_valid(c.key(u));
           const uint32_t w = __ballot_sync(0xffffffffu, on);
           if (lane == 0) reinterpret_cast<uint32_t*>(inf)[me >> 5] = w;
         } else {
-          copy_rows(d0, d0 + L::B, q.p, a.D, a.Dv, kCols, me, kLoaders, [&](int r, const bf16*& p0, const bf16*& p1) {
-            return u0 + r < n && query(fl + u0 + r, p0, p1);
-          });
+          copy_rows(d0, d0 + L::B, pc, walk_queries(a, q, g, min(fl + u0 + pc.first, fl + n - 1), pc.step), kCols, kCols, n - u0, query_valid);
           const int f = fl + u0 + me, i = f / a.G;
           float x = -INFINITY, d = 0.f;
           if (u0 + me < n && win_alive(a, b, q0 + i)) {
@@ -267,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       for (int t = 0; t < ntile; ++t) {
         const int st = t % NS;
         const uint32_t b0 = sB + st * 2 * L::B, b1 = b0 + L::B;
-        if (!wait(&full[st], (t / NS) & 1, wc, 82)) break;
-        if (t > 0 && !wait(pv_done, (t - 1) & 1, wc, 83)) break;      // S takes the place of the last P
+        if (!mbar_wait(&full[st], (t / NS) & 1, wc, 82)) break;
+        if (t > 0 && !mbar_wait(pv_done, (t - 1) & 1, wc, 83)) break;      // S takes the place of the last P
         tc_fence_after();
         for (int kk = 0; kk < kd; ++kk) {
           const uint32_t o = (kk & 3) * 32;
@@ -283,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           }
         }
         tc_commit(s_full);
-        if (!wait(p_full, t & 1, wc, 84)) break;
+        if (!mbar_wait(p_full, t & 1, wc, 84)) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kCols / 16; ++kk) {
@@ -336,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     for (int t = 0; t < ntile; ++t) {
       const int st = t % NS, u0 = t * kCols;
       const uint8_t* inf = smem + L::info + st * (MODE == kKeySide ? 768 : 8);
-      const bool there = wait(&full[st], (t / NS) & 1, wc, 85) && wait(s_full, t & 1, wc, 86);   // the tile's bits or row data; S
+      const bool there = mbar_wait(&full[st], (t / NS) & 1, wc, 85) && mbar_wait(s_full, t & 1, wc, 86);   // the tile's bits or row data; S
       if (!__all_sync(0xffffffffu, there)) break;
       tc_fence_after();
       if (MODE == kFwd) {
@@ -449,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       tc_fence_before();
       mbar_arrive(p_full);
     }
-    bool done = ntile > 0 && wait(pv_done, (ntile - 1) & 1, wc, 87);
+    bool done = ntile > 0 && mbar_wait(pv_done, (ntile - 1) & 1, wc, 87);
     done = __all_sync(0xffffffffu, done);
     tc_fence_after();
     const bool ok = done || ntile == 0;                     // after a wait that ran out nothing is written
