@@ -42,10 +42,14 @@ struct Lay {
   static constexpr int tail = NA * A + NS * 2 * B;
   static constexpr int bars = tail, info = tail + 128;   // info: per stage 64 x {lse, delta, position} or two words of column bits
   static constexpr int smem = info + NS * (MODE == kKeySide ? 768 : 8) + 1024;
-  static constexpr int S = 0, dP = 64, acc0 = MODE == kFwd ? 64 : 128, acc1 = acc0 + DP;
+  // Tensor memory.  Forward: S of even and odd tiles, P in place of S.  Row side:
+  // S, dP, dS of even and odd tiles.  Key side: S and dP, P and dS in their places.
+  static constexpr int S = 0, dP = 64, acc0 = MODE == kRowSide ? 192 : 128, acc1 = acc0 + DP;
   static constexpr int need = MODE == kKeySide ? acc1 + DP : acc0 + DP;
-  static constexpr int cols = need <= 128 ? 128 : (need <= 256 ? 256 : 512);
-  static constexpr int per_sm = DP == 64 ? (MODE == kFwd ? 3 : 2) : (MODE == kFwd ? 2 : 1);
+  static constexpr int cols = need <= 256 ? 256 : 512;
+  static constexpr int per_sm = DP == 64 || MODE == kFwd ? 2 : 1;
+  static __device__ __forceinline__ int s_of(int t) { return MODE == kFwd ? S + 64 * (t & 1) : S; }
+  static __device__ __forceinline__ int p_of(int t) { return MODE == kRowSide ? 128 + 32 * (t & 1) : s_of(t); }
 };
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -138,6 +142,19 @@ __device__ __forceinline__ void copy_rows(uint32_t d0, uint32_t d1, const Piece&
   }
 }
 
+// Whether the phase is over, without waiting for it.
+__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity))
@@ -173,10 +190,10 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
   uint64_t* empty = full + NS;
-  uint64_t* s_full = empty + NS;
-  uint64_t* p_full = s_full + 1;
-  uint64_t* pv_done = p_full + 1;
-  uint64_t* drained = pv_done + 1;
+  uint64_t* s_full = empty + NS;             // two: even and odd tiles, as the products run up to a tile ahead of the rows
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 1;            // two, likewise
+  uint64_t* drained = pv_done + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(drained + 1);
   int* abort_flag = reinterpret_cast<int*>(slot + 1);
   const uint32_t sA = smem_u32(smem), sB = sA + L::NA * L::A;
@@ -220,9 +237,11 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       mbar_init(&full[s], kLoaders);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(s_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&pv_done[s], 1);
+    }
     mbar_init(p_full, kFinish);
-    mbar_init(pv_done, 1);
     mbar_init(drained, 1);
     fence_mbar_init();
     *abort_flag = 0;
@@ -252,10 +271,24 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     // ------------------------------------------------------------- copies
     const int me = threadIdx.x - 160;
     const Piece pc(a.D, a.Dv, me, kLoaders);
+    auto landed = [&](int t) {                              // this thread's part of tile t is in place
+      fence_proxy_async_smem();
+      mbar_arrive(&full[t % NS]);
+    };
     for (int t = 0; t <= ntile; ++t) {
+      bool told = t == 0;
       if (t < ntile) {
         const int st = t % NS, u0 = t * kCols;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ((t / NS) & 1) ^ 1u, wc, 81))) break;
+        const uint32_t ph = ((t / NS) & 1) ^ 1u;
+        if (!__all_sync(0xffffffffu, test(&empty[st], ph))) {
+          // the products may need the last tile before they give this place back
+          if (!told) {
+            cp_wait<0>();
+            landed(t - 1);
+            told = true;
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], ph, wc, 81))) break;
+        }
         const uint32_t d0 = sB + st * 2 * L::B;
         uint8_t* inf = smem + L::info + st * (MODE == kKeySide ? 768 : 8);
         if (kRowsAreQueries) {
@@ -285,15 +318,12 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           reinterpret_cast<int*>(inf)[128 + me] = q0 + i;
         }
         cp_async_commit();
-        if (t == 0) continue;
+        if (told) continue;
         cp_wait<1>();
       } else {
         cp_wait<0>();
       }
-      if (t > 0) {
-        fence_proxy_async_smem();
-        mbar_arrive(&full[(t - 1) % NS]);
-      }
+      if (!told) landed(t - 1);
     }
     cp_async_wait_all();
   } else if (warp == 4) {
@@ -301,16 +331,15 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     if (lane == 0 && ntile > 0) {
       const int kd = (a.D + 15) / 16, kv = (a.Dv + 15) / 16;
       const uint32_t idS = idesc_bf16(128, kCols, 0, 0), idD = idesc_bf16(128, 16 * kd, 0, 1), idV = idesc_bf16(128, 16 * kv, 0, 1);
-      for (int t = 0; t < ntile; ++t) {
+      auto scores = [&](int t) -> bool {
         const int st = t % NS;
         const uint32_t b0 = sB + st * 2 * L::B, b1 = b0 + L::B;
-        if (!mbar_wait(&full[st], (t / NS) & 1, wc, 82)) break;
-        if (t > 0 && !mbar_wait(pv_done, (t - 1) & 1, wc, 83)) break;      // S takes the place of the last P
+        if (!mbar_wait(&full[st], (t / NS) & 1, wc, 82)) return false;
         tc_fence_after();
         for (int kk = 0; kk < kd; ++kk) {
           const uint32_t o = (kk & 3) * 32;
-          mma_ss(tmem + L::S, desc_kmajor_sw128(sA + (kk >> 2) * (kRows * 128) + o), desc_kmajor_sw128(b0 + (kk >> 2) * (kCols * 128) + o), idS,
-                 kk > 0);
+          mma_ss(tmem + L::s_of(t), desc_kmajor_sw128(sA + (kk >> 2) * (kRows * 128) + o), desc_kmajor_sw128(b0 + (kk >> 2) * (kCols * 128) + o),
+                 idS, kk > 0);
         }
         if (MODE != kFwd) {
           for (int kk = 0; kk < kv; ++kk) {
@@ -319,18 +348,34 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
                    desc_kmajor_sw128(b1 + (kk >> 2) * (kCols * 128) + o), idS, kk > 0);
           }
         }
-        tc_commit(s_full);
-        if (!mbar_wait(p_full, t & 1, wc, 84)) break;
+        tc_commit(&s_full[t & 1]);
+        return true;
+      };
+      auto done = [&](int t) { return t < 0 || mbar_wait(&pv_done[t & 1], (t >> 1) & 1, wc, 83); };
+      bool go = scores(0);
+      for (int t = 0; t < ntile && go; ++t) {
+        const int st = t % NS;
+        const uint32_t b0 = sB + st * 2 * L::B, b1 = b0 + L::B;
+        // the next scores as early as their place is free: at once (forward: P(t - 1)
+        // has been used), when this tile's were read (row side), or when this tile's
+        // P and dS have been used (key side)
+        if (MODE == kFwd && t + 1 < ntile) go = done(t - 1) && scores(t + 1);
+        if (!go || !mbar_wait(p_full, t & 1, wc, 84)) break;
         tc_fence_after();
+        if (MODE == kRowSide && t + 1 < ntile) {
+          go = scores(t + 1);
+          if (!go) break;
+        }
 #pragma unroll
         for (int kk = 0; kk < kCols / 16; ++kk) {
-          const uint32_t acc = t > 0 || kk > 0;
-          if (MODE != kRowSide) mma_ts(tmem + L::acc0, tmem + L::S + 8 * kk, desc_mnmajor_sw128(b1 + kk * 2048, kCols * 128), idV, acc);
-          if (MODE == kRowSide) mma_ts(tmem + L::acc0, tmem + L::S + 8 * kk, desc_mnmajor_sw128(b0 + kk * 2048, kCols * 128), idD, acc);
+          const uint32_t acc = t > 0 || kk > 0, p = tmem + L::p_of(t) + 8 * kk;
+          if (MODE != kRowSide) mma_ts(tmem + L::acc0, p, desc_mnmajor_sw128(b1 + kk * 2048, kCols * 128), idV, acc);
+          if (MODE == kRowSide) mma_ts(tmem + L::acc0, p, desc_mnmajor_sw128(b0 + kk * 2048, kCols * 128), idD, acc);
           if (MODE == kKeySide) mma_ts(tmem + L::acc1, tmem + L::dP + 8 * kk, desc_mnmajor_sw128(b0 + kk * 2048, kCols * 128), idD, acc);
         }
         tc_commit(&empty[st]);
-        tc_commit(pv_done);
+        tc_commit(&pv_done[t & 1]);
+        if (MODE == kKeySide && t + 1 < ntile) go = done(t) && scores(t + 1);
       }
       if (*abort_flag) {                                    // what is in flight ends before the memory is given back
         tc_commit(drained);
@@ -373,37 +418,38 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     for (int t = 0; t < ntile; ++t) {
       const int st = t % NS, u0 = t * kCols;
       const uint8_t* inf = smem + L::info + st * (MODE == kKeySide ? 768 : 8);
-      const bool there = mbar_wait(&full[st], (t / NS) & 1, wc, 85) && mbar_wait(s_full, t & 1, wc, 86);   // the tile's bits or row data; S
+      const bool there = mbar_wait(&full[st], (t / NS) & 1, wc, 85) && mbar_wait(&s_full[t & 1], (t >> 1) & 1, wc, 86);   // the tile's bits or row data; S
       if (!__all_sync(0xffffffffu, there)) break;
       tc_fence_after();
       if (MODE == kFwd) {
         const uint32_t w[2] = {reinterpret_cast<const uint32_t*>(inf)[0], reinterpret_cast<const uint32_t*>(inf)[1]};
         const bool edge = (w[0] & w[1]) != 0xffffffffu || !rc.all(u0, kCols);
-        // 32 scores at a time, read twice: all 64 at once would cost a third of the warps
-        auto scores = [&](int h, uint32_t (&s)[32]) {
-          tmem_ld32(trow + L::S + 32 * h, s);
-          tmem_ld_wait();
-          if (edge) {
+        uint32_t s[2][32];
+        tmem_ld32(trow + L::s_of(t), s[0]);
+        tmem_ld32(trow + L::s_of(t) + 32, s[1]);
+        tmem_ld_wait();
+        if (edge) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
             const uint32_t on = w[h] & row.sees(u0 + 32 * h);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = (on >> e) & 1u ? s[e] : __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e) s[h][e] = (on >> e) & 1u ? s[h][e] : __float_as_uint(-INFINITY);
           }
-        };
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s[32];
-          scores(h, s);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
-        }
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[h][e]));
         mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         // m follows the true maximum only when it would be left behind by 2^8
         if (__any_sync(0xffffffffu, (mx[0] - m) * sc > kWinLag)) {
           const float mn = fmaxf(m, mx[0]), f = ex2_approx(mn == -INFINITY ? -INFINITY : (m - mn) * sc);
           m = mn;
           l *= f;
-          if (t > 0) {                                      // O is complete up to the last tile: S follows it
+          if (t > 0) {                                      // O with the last tile in it
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 88))) break;
+            tc_fence_after();
             for (int c0 = 0; c0 < a.Dv; c0 += 32) {
               uint32_t o[32];
               tmem_ld32(trow + (uint32_t)(L::acc0 + c0), o);
@@ -418,21 +464,23 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t s[32], p[16];
-          scores(h, s);
+          uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float x = ex2_approx(fmaf(__uint_as_float(s[e]), sc, -mb)), y = ex2_approx(fmaf(__uint_as_float(s[e + 1]), sc, -mb));
+            const float x = ex2_approx(fmaf(__uint_as_float(s[h][e]), sc, -mb)), y = ex2_approx(fmaf(__uint_as_float(s[h][e + 1]), sc, -mb));
             sum[e & 2] += x;
             sum[(e & 2) + 1] += y;
             p[e / 2] = pack(x, y);
           }
-          tmem_st16(trow + L::S + 16 * h, p);
+          tmem_st16(trow + L::p_of(t) + 16 * h, p);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       } else if (MODE == kRowSide) {
         const uint32_t w[2] = {reinterpret_cast<const uint32_t*>(inf)[0], reinterpret_cast<const uint32_t*>(inf)[1]};
         const bool edge = (w[0] & w[1]) != 0xffffffffu || !rc.all(u0, kCols);
+        // dS of the tile before the last has been used
+        if (t > 1 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[t & 1], ((t >> 1) - 1) & 1, wc, 89))) break;
+        tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t s[32], d[32], p[16];
@@ -449,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) p[e] = pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-          tmem_st16(trow + L::S + 16 * h, p);
+          tmem_st16(trow + L::p_of(t) + 16 * h, p);
         }
       } else {
         const float* sl = reinterpret_cast<const float*>(inf);
@@ -486,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       tc_fence_before();
       mbar_arrive(p_full);
     }
-    bool done = ntile > 0 && mbar_wait(pv_done, (ntile - 1) & 1, wc, 87);
+    bool done = ntile > 0 && mbar_wait(&pv_done[(ntile - 1) & 1], ((ntile - 1) >> 1) & 1, wc, 87);
     done = __all_sync(0xffffffffu, done);
     tc_fence_after();
     const bool ok = done || ntile == 0;                     // after a wait that ran out nothing is written
