@@ -69,6 +69,13 @@ inline WinSinkPlan win_sink_plan(const WinArgs& a, int key_tile) {
 
 constexpr int kWinTcRows = 128, kWinTcCols = 64;      // tile of window_tc.cu
 
+// Sequences that one CTA holds as a whole (window_short.cu): rows (with the heads of a group) and keys.
+constexpr int kWinShortRows = 512;
+inline size_t win_short_smem(const WinArgs& a, int dp, bool backward) {
+  const size_t F = ((size_t)a.Nq * a.G + 15) / 16 * 16, K = ((size_t)a.Nk + 15) / 16 * 16;
+  return (2 * K + (backward ? 2 : 1) * F) * (dp + 8) * 2;
+}
+
 // Whether q, k and v can be read 16 bytes at a time.
 inline bool win_vec(const WinArgs& a) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
@@ -127,6 +134,7 @@ cudaError_t launch_win_bwd_simt(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s);            // bfloat16 tensors: one of the following
 cudaError_t launch_win_bwd(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_step(const WinArgs& a, cudaStream_t s);           // few rows
+cudaError_t launch_win_short(const WinArgs& a, bool backward, cudaStream_t s);   // many short sequences
 cudaError_t launch_win_fwd_tc(const WinArgs& a, cudaStream_t s);         // wide windows
 cudaError_t launch_win_bwd_q_tc(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_bwd_k_tc(const WinArgs& a, cudaStream_t s);

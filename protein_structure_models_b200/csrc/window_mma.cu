@@ -642,16 +642,24 @@ bool use_tc(const WinArgs& a, bool backward) {
   return true;
 }
 
+bool use_short(const WinArgs& a, bool backward) {
+  const int w = a.D > a.Dv ? a.D : a.Dv;
+  if (w > 64 || a.Nk > kWinShortRows || (long long)a.Nq * a.G > kWinShortRows) return false;
+  return use_tc(a, backward) && win_short_smem(a, w <= 16 ? 16 : (w <= 32 ? 32 : 64), backward) <= 160 * 1024;
+}
+
 }  // namespace
 
 cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s) {
   if ((long long)a.Nq * a.G <= kWinStepRows) return launch_win_step(a, s);
+  if (use_short(a, false)) return launch_win_short(a, false, s);
   if (use_tc(a, false)) return launch_win_fwd_tc(a, s);
   const int w = a.D > a.Dv ? a.D : a.Dv;
   return w <= 16 ? fwd<16>(a, s) : (w <= 32 ? fwd<32>(a, s) : (w <= 64 ? fwd<64>(a, s) : fwd<128>(a, s)));
 }
 cudaError_t launch_win_bwd(const WinArgs& in, cudaStream_t s) {
   WinArgs a = in;
+  if (use_short(a, true)) return launch_win_short(a, true, s);
   const bool tc = use_tc(a, true);
   const WinSinkPlan sp = win_sink_plan(a, tc ? kWinTcRows : T);
   a.nchunk = sp.nchunk;

@@ -38,7 +38,7 @@ struct Lay {
   static constexpr int CH = DP / 64;                     // 128-byte chunks of a row
   static constexpr int A = kRows * 128 * CH, B = kCols * 128 * CH;
   static constexpr int NA = MODE == kFwd ? 1 : 2;
-  static constexpr int NS = DP == 64 ? 3 : 2;            // stages of the stream
+  static constexpr int NS = DP == 128 && MODE == kFwd ? 2 : 4;   // stages of the stream
   static constexpr int tail = NA * A + NS * 2 * B;
   static constexpr int bars = tail, info = tail + 128;   // info: per stage 64 x {lse, delta, position} or two words of column bits
   static constexpr int smem = info + NS * (MODE == kKeySide ? 768 : 8) + 1024;
