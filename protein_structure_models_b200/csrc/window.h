@@ -72,7 +72,7 @@ constexpr int kWinTcRows = 128, kWinTcCols = 64;      // tile of window_tc.cu
 // Sequences that one CTA holds as a whole (window_short.cu): rows (with the heads of a group) and keys.
 constexpr int kWinShortRows = 512;
 inline size_t win_short_smem(const WinArgs& a, int dp, bool backward) {
-  const size_t F = ((size_t)a.Nq * a.G + 15) / 16 * 16, K = ((size_t)a.Nk + 15) / 16 * 16;
+  const size_t F = ((size_t)a.Nq * a.G + 15) / 16 * 16, K = ((size_t)a.Nk + 31) / 32 * 32;
   return (2 * K + (backward ? 2 : 1) * F) * (dp + 8) * 2;
 }
 
@@ -103,12 +103,13 @@ __device__ __forceinline__ WinCols win_cols(const WinArgs& a, int q0, int f0, in
   c.n = c.s + c.hi - c.lo + 1;
   return c;
 }
-// The columns lo .. hi-1 of 32, as bits.
-__device__ __forceinline__ uint32_t win_span(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 32);
-  return hi > lo ? (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo) : 0u;
+// The columns lo .. hi-1 of 32, as bits (a shift by 32 or more leaves nothing in PTX).
+__device__ __forceinline__ uint32_t win_from(int x) {
+  uint32_t r;
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(0xffffffffu), "r"(max(x, 0)));
+  return r;
 }
+__device__ __forceinline__ uint32_t win_span(int lo, int hi) { return win_from(lo) & ~win_from(hi); }
 // The two column ranges of the row at position p: [0, s1) and [w0, w1).  Masks of
 // 32 columns from u0 on: element by element the compiler makes a branch of each
 // comparison, which took ten times as long as the rest of a tile.

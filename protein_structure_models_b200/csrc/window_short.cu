@@ -16,10 +16,11 @@ namespace fipa {
 namespace {
 
 constexpr int kMaxWords = kWinShortRows / 32;
+constexpr int kNowhere = -(1 << 30);       // position of a row that sees nothing
 
 // Everything of one (b, hkv): padded tiles of queries (and dO) and of keys and values.
 struct Seq {
-  int b, hkv, q0, F, Fp, Kp;               // rows, rows and keys rounded up to 16
+  int b, hkv, q0, F, Fp, Kp;               // rows, rows rounded up to 16, keys to 32
   uint32_t q, g, k, v;                     // shared-memory addresses
 };
 template <int DP>
@@ -30,7 +31,7 @@ __device__ __forceinline__ Seq seq_of(const WinArgs& a, uint8_t* smem, bool back
   s.q0 = win_q0(a, s.b);
   s.F = a.Nq * a.G;
   s.Fp = (s.F + 15) & ~15;
-  s.Kp = (a.Nk + 15) & ~15;
+  s.Kp = (a.Nk + 31) & ~31;
   constexpr int row = Tile<DP>::ld * 2;
   s.k = smem_u32(smem);
   s.v = s.k + s.Kp * row;
@@ -80,29 +81,22 @@ __device__ __forceinline__ void load_seq(const WinArgs& a, const Seq& s, uint32_
   }
 }
 
-// The columns of 16 rows f0 .. f0+15 in groups of 16 neighbouring keys from a
-// multiple of 16 on: first the sinks before the window's first group, then the window.
-struct Groups {
-  int lo, hi, s, ns, n;
-  __device__ __forceinline__ int first(int g) const { return g < ns ? 16 * g : lo + 16 * (g - ns); }
-  __device__ __forceinline__ int end(int g) const { return g < ns ? s : hi + 1; }
+// The columns of 16 rows in units of 32 neighbouring keys from a multiple of 32
+// on: those of the sinks before the window's first unit, then the window's.
+struct Units {
+  int lo, hi, s;                           // first window unit, last key, sinks before the window (0: go there at once)
+  __device__ __forceinline__ int first() const { return s > 0 ? 0 : lo; }
+  __device__ __forceinline__ int next(int j0) const { return j0 < lo && j0 + 32 >= s ? lo : j0 + 32; }
 };
-__device__ __forceinline__ Groups groups_of(const WinArgs& a, const WinCols& c) {
-  Groups g;
-  g.lo = c.lo & ~15;
-  g.hi = c.hi;
-  g.s = min(a.sinks, g.lo);
-  g.ns = (g.s + 15) / 16;
-  g.n = c.n == 0 ? 0 : g.ns + (c.hi - g.lo + 16) / 16;
-  return g;
+__device__ __forceinline__ Units units_of(const WinArgs& a, const WinCols& c) {
+  const int lo = c.lo & ~31;
+  return Units{c.n == 0 ? 0 : lo, c.n == 0 ? -1 : c.hi, c.n == 0 ? 0 : min(a.sinks, lo)};
 }
-// Bits of keys j0 .. j0+15 (j0 a multiple of 16) below `end` that exist.
-__device__ __forceinline__ uint32_t group_bits(const uint32_t* bits, int j0, int end) {
-  return (bits[j0 >> 5] >> (j0 & 16)) & win_span(0, end - j0) & 0xffffu;
-}
-// What a row at position p sees of keys j0 .. (sinks, window).
-__device__ __forceinline__ uint32_t row_bits(const WinArgs& a, int p, bool alive, int j0) {
-  return alive ? win_span(0, min(a.sinks, p + a.right + 1) - j0) | win_span(p - a.left - j0, p + a.right + 1 - j0) : 0u;
+// What the row at position p sees of keys j0 .. j0+31, which exist as `there` says.
+__device__ __forceinline__ uint32_t row_bits(const WinArgs& a, uint32_t there, int p, int j0) {
+  uint32_t w = win_span(p - a.left - j0, p + a.right + 1 - j0);
+  if (j0 < a.sinks) w |= win_span(0, min(a.sinks, p + a.right + 1) - j0);
+  return w & there;
 }
 
 template <int DP>
@@ -118,8 +112,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
   const float sc = a.scale * kLog2e;
   for (int f0 = 16 * warp; f0 < s.F; f0 += 64) {
     const int f1 = min(s.F, f0 + 16);
-    const WinCols c = win_cols(a, s.q0, f0, f1);
-    const Groups gr = groups_of(a, c);
+    const Units un = units_of(a, win_cols(a, s.q0, f0, f1));
     bool alive[2];
     int pos[2];
 #pragma unroll
@@ -127,6 +120,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
       const int f = f0 + (lane >> 2) + 8 * i;
       pos[i] = s.q0 + (a.G == 1 ? f : f / a.G);
       alive[i] = f < f1 && pos[i] >= 0 && pos[i] < a.Nk && ((bits[pos[i] >> 5] >> (pos[i] & 31)) & 1u);
+      if (!alive[i]) pos[i] = kNowhere;
     }
     const bool any = __any_sync(0xffffffffu, alive[0] || alive[1]);
     float acc[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -137,15 +131,16 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
     uint32_t qf[DP / 16][4];
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) ldsm4(qf[kk], a_addr<DP>(s.q, f0, 16 * kk, lane));
-    for (int g0 = 0; any && g0 < gr.n; g0 += 2) {
+    for (int j0 = un.first(); any && j0 <= un.hi; j0 = un.next(j0)) {
+      const uint32_t there = bits[j0 >> 5];
+      const uint32_t on[2] = {row_bits(a, there, pos[0], j0), row_bits(a, there, pos[1], j0)};
+      const uint32_t ob[2] = {on[0] >> col2, on[1] >> col2};
       float sc_[4][4], mx[2] = {-INFINITY, -INFINITY};
-      const int ng = min(2, gr.n - g0);
+      bool go[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        if (g >= ng) break;
-        const int j0 = gr.first(g0 + g);
-        const uint32_t w = group_bits(bits, j0, gr.end(g0 + g));
-        const uint32_t on[2] = {w & row_bits(a, pos[0], alive[0], j0), w & row_bits(a, pos[1], alive[1], j0)};
+        go[g] = __any_sync(0xffffffffu, ((on[0] | on[1]) >> (16 * g) & 0xffffu) != 0u);
+        if (!go[g]) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -154,7 +149,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
         for (int kk = 0; kk < DP / 16; ++kk) {
           if (kk >= kd) break;
           uint32_t bf[4];
-          ldsm4(bf, b_addr<DP>(s.k, j0, 16 * kk, lane));
+          ldsm4(bf, b_addr<DP>(s.k, j0 + 16 * g, 16 * kk, lane));
           mma(sc_[2 * g], qf[kk], bf[0], bf[1]);
           mma(sc_[2 * g + 1], qf[kk], bf[2], bf[3]);
         }
@@ -162,7 +157,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc_[2 * g + h][e] = (on[e >> 1] >> (8 * h + col2 + (e & 1))) & 1u ? sc_[2 * g + h][e] : -INFINITY;
+            sc_[2 * g + h][e] = ob[e >> 1] & (1u << (16 * g + 8 * h + (e & 1))) ? sc_[2 * g + h][e] : -INFINITY;
             mx[e >> 1] = fmaxf(mx[e >> 1], sc_[2 * g + h][e]);
           }
       }
@@ -187,8 +182,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
       const float mb[2] = {m[0] == -INFINITY ? 0.f : m[0] * sc, m[1] == -INFINITY ? 0.f : m[1] * sc};
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        if (g >= ng) break;
-        const int j0 = gr.first(g0 + g);
+        if (!go[g]) continue;
         float p[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -202,7 +196,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
         for (int n = 0; n < DP / 16; ++n) {
           if (n >= kv) break;
           uint32_t bf[4];
-          ldsm4t(bf, bt_addr<DP>(s.v, j0, 16 * n, lane));
+          ldsm4t(bf, bt_addr<DP>(s.v, j0 + 16 * g, 16 * n, lane));
           mma(acc[2 * n], pf, bf[0], bf[1]);
           mma(acc[2 * n + 1], pf, bf[2], bf[3]);
         }
@@ -275,7 +269,7 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
   // ---- dq
   for (int f0 = 16 * warp; f0 < s.F; f0 += 64) {
     const int f1 = min(s.F, f0 + 16);
-    const Groups gr = groups_of(a, win_cols(a, s.q0, f0, f1));
+    const Units un = units_of(a, win_cols(a, s.q0, f0, f1));
     float lse2[2], del[2], acc[DP / 8][4];
     int pos[2];
 #pragma unroll
@@ -283,7 +277,7 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
       const int f = f0 + (lane >> 2) + 8 * i;
       lse2[i] = slse[f];
       del[i] = sdel[f];
-      pos[i] = spos[f];
+      pos[i] = lse2[i] == INFINITY ? kNowhere : spos[f];
     }
     const bool any = __any_sync(0xffffffffu, lse2[0] != INFINITY || lse2[1] != INFINITY);
 #pragma unroll
@@ -296,44 +290,48 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
       ldsm4(qf[kk], a_addr<DP>(s.q, f0, 16 * kk, lane));
       ldsm4(gf[kk], a_addr<DP>(s.g, f0, 16 * kk, lane));
     }
-    for (int g = 0; any && g < gr.n; ++g) {
-      const int j0 = gr.first(g);
-      const uint32_t w = group_bits(bits, j0, gr.end(g));
-      const uint32_t on[2] = {w & row_bits(a, pos[0], lse2[0] != INFINITY, j0), w & row_bits(a, pos[1], lse2[1] != INFINITY, j0)};
-      float x[2][4], dp[2][4];
+    for (int j0 = un.first(); any && j0 <= un.hi; j0 = un.next(j0)) {
+      const uint32_t there = bits[j0 >> 5];
+      const uint32_t on[2] = {row_bits(a, there, pos[0], j0), row_bits(a, there, pos[1], j0)};
+      const uint32_t ob[2] = {on[0] >> col2, on[1] >> col2};
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int g = 0; g < 2; ++g) {
+        if (!__any_sync(0xffffffffu, ((on[0] | on[1]) >> (16 * g) & 0xffffu) != 0u)) continue;
+        float x[2][4], dp[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[h][e] = dp[h][e] = 0.f;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-        uint32_t bf[4];
-        if (kk < kd) {
-          ldsm4(bf, b_addr<DP>(s.k, j0, 16 * kk, lane));
-          mma(x[0], qf[kk], bf[0], bf[1]);
-          mma(x[1], qf[kk], bf[2], bf[3]);
+          for (int e = 0; e < 4; ++e) x[h][e] = dp[h][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          uint32_t bf[4];
+          if (kk < kd) {
+            ldsm4(bf, b_addr<DP>(s.k, j0 + 16 * g, 16 * kk, lane));
+            mma(x[0], qf[kk], bf[0], bf[1]);
+            mma(x[1], qf[kk], bf[2], bf[3]);
+          }
+          if (kk < kv) {
+            ldsm4(bf, b_addr<DP>(s.v, j0 + 16 * g, 16 * kk, lane));
+            mma(dp[0], gf[kk], bf[0], bf[1]);
+            mma(dp[1], gf[kk], bf[2], bf[3]);
+          }
         }
-        if (kk < kv) {
-          ldsm4(bf, b_addr<DP>(s.v, j0, 16 * kk, lane));
-          mma(dp[0], gf[kk], bf[0], bf[1]);
-          mma(dp[1], gf[kk], bf[2], bf[3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = ex2_approx(fmaf(x[h][e], sc, -lse2[e >> 1])) * (dp[h][e] - del[e >> 1]);
+            x[h][e] = ob[e >> 1] & (1u << (16 * g + 8 * h + (e & 1))) ? y : 0.f;
+          }
+        const uint32_t pf[4] = {pack(x[0][0], x[0][1]), pack(x[0][2], x[0][3]), pack(x[1][0], x[1][1]), pack(x[1][2], x[1][3])};
+#pragma unroll
+        for (int n = 0; n < DP / 16; ++n) {
+          if (n >= kd) break;
+          uint32_t bf[4];
+          ldsm4t(bf, bt_addr<DP>(s.k, j0 + 16 * g, 16 * n, lane));
+          mma(acc[2 * n], pf, bf[0], bf[1]);
+          mma(acc[2 * n + 1], pf, bf[2], bf[3]);
         }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = ex2_approx(fmaf(x[h][e], sc, -lse2[e >> 1])) * (dp[h][e] - del[e >> 1]);
-          x[h][e] = (on[e >> 1] >> (8 * h + col2 + (e & 1))) & 1u ? y : 0.f;
-        }
-      const uint32_t pf[4] = {pack(x[0][0], x[0][1]), pack(x[0][2], x[0][3]), pack(x[1][0], x[1][1]), pack(x[1][2], x[1][3])};
-#pragma unroll
-      for (int n = 0; n < DP / 16; ++n) {
-        if (n >= kd) break;
-        uint32_t bf[4];
-        ldsm4t(bf, bt_addr<DP>(s.k, j0, 16 * n, lane));
-        mma(acc[2 * n], pf, bf[0], bf[1]);
-        mma(acc[2 * n + 1], pf, bf[2], bf[3]);
       }
     }
     store_rows<DP>(acc, a.D, a.d_q, a.scale, lane, [&](int i, bool& keep) -> bf16* {
@@ -371,6 +369,7 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
     for (int f0 = fl; any && f0 < fh; f0 += 16) {
       const uint32_t on[2] = {win_span(rlo[0] - f0, rhi[0] - f0), win_span(rlo[1] - f0, rhi[1] - f0)};
       if (!__any_sync(0xffffffffu, ((on[0] | on[1]) & 0xffffu) != 0u)) continue;
+      const uint32_t ob[2] = {on[0] >> col2, on[1] >> col2};
       float x[2][4], dp[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float y = ex2_approx(fmaf(x[h][e], sc, -(e & 1 ? ls.y : ls.x)));
-          x[h][e] = (on[e >> 1] >> (8 * h + col2 + (e & 1))) & 1u ? y : 0.f;
+          x[h][e] = ob[e >> 1] & (1u << (8 * h + (e & 1))) ? y : 0.f;
           dp[h][e] = x[h][e] * (dp[h][e] - (e & 1 ? de.y : de.x));
         }
       }
