@@ -60,7 +60,7 @@ inline WinSinkPlan win_sink_plan(const WinArgs& a, int key_tile) {
   s.sink_pos = (int)(end < a.Nk ? end : a.Nk) + a.left;
   if (a.sinks <= 0 || s.sink_pos >= a.Nk) return s;          // the window reaches every position
   const long long tiles = ((long long)a.Nq * a.G + 63) / 64;
-  s.chunk_tiles = 8;
+  s.chunk_tiles = 2;
   while ((tiles + s.chunk_tiles - 1) / s.chunk_tiles > 256) s.chunk_tiles *= 2;
   s.nchunk = (int)((tiles + s.chunk_tiles - 1) / s.chunk_tiles);
   s.part_floats = (size_t)a.B * a.Hkv * (s.nchunk + 1) * a.sinks * (a.D + a.Dv);

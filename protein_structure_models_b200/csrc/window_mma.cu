@@ -430,6 +430,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
   }
   const int ka = j0 + wj, kb = min(ka + 15, j1);   // keys of the warp
   const int ntile = __syncthreads_or(alive[0] || alive[1]) && fh > fl ? (fh - fl + T - 1) / T : 0;
+  float rl = 0.f, rd = 0.f;
+  int rp = 0;
   auto load = [&](int t) {
     const int st = t & 1, f0 = fl + t * T;
     auto rows = [&](const Src& s) {
@@ -441,17 +443,24 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
     load_tile<DP, VEC>(Qs + st * kElems<DP>, q, T, threadIdx.x, kThreads, rows(q));
     load_tile<DP, VEC>(Os + st * kElems<DP>, g_, T, threadIdx.x, kThreads, rows(g_));
     cp_async_commit();
+    // a row's lse, delta and position wait in registers until the tile before is done
     if (threadIdx.x < T) {
       const int f = f0 + threadIdx.x, i = f / a.G;
-      float x = -INFINITY, d = 0.f;
-      if (f < fh && win_alive(a, b, q0 + i)) {
+      rl = -INFINITY;
+      rd = 0.f;
+      rp = q0 + i;
+      if (f < fh && win_alive(a, b, rp)) {
         const long long o = ((long long)b * a.H + hkv * a.G + (f - i * a.G)) * a.Nq + i;
-        x = a.lse[o];
-        d = a.delta[o];
+        rl = a.lse[o];
+        rd = a.delta[o];
       }
-      slse[st][threadIdx.x] = x == -INFINITY ? INFINITY : x * kLog2e;
-      sdel[st][threadIdx.x] = d;
-      spos[st][threadIdx.x] = q0 + i;
+    }
+  };
+  auto put = [&](int st) {
+    if (threadIdx.x < T) {
+      slse[st][threadIdx.x] = rl == -INFINITY ? INFINITY : rl * kLog2e;   // not there, or sees nothing: every p is 0
+      sdel[st][threadIdx.x] = rd;
+      spos[st][threadIdx.x] = rp;
     }
   };
   const int kd = (a.D + 15) / 16, kv = (a.Dv + 15) / 16;
@@ -468,6 +477,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
     load_tile<DP, VEC>(Ks, k, KR, threadIdx.x, kThreads, keyed(k));
     load_tile<DP, VEC>(Vs, v, KR, threadIdx.x, kThreads, keyed(v));
     load(0);
+    put(0);
   }
   for (int t = 0; t < ntile; ++t) {
     const int st = t & 1;
@@ -537,6 +547,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
         }
       }
     }
+    if (t + 1 < ntile) put(st ^ 1);
     __syncthreads();
   }
   if (SINK) {
@@ -635,17 +646,27 @@ cudaError_t bwd(const WinArgs& a, bool tc, cudaStream_t s) {
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Whether the tcgen05 kernels take a call.
-bool use_tc(const WinArgs& a, bool backward) {
-  if (!win_vec(a) || !on16(a.out)) return false;
-  if (backward && !(on16(a.d_out) && on16(a.d_q) && on16(a.d_k) && on16(a.d_v))) return false;
-  return true;
+// Whether every tensor of a call is on 16-byte boundaries.
+bool vectors(const WinArgs& a, bool backward) {
+  return win_vec(a) && on16(a.out) && (!backward || (on16(a.d_out) && on16(a.d_q) && on16(a.d_k) && on16(a.d_v)));
 }
-
+// Whether the tcgen05 kernels take a call: their tile of 128 rows and 64 columns
+// pays when the window is wide and the rows long, and when there are rows to fill
+// it.  Forward / backward in us, matrix instructions per warp against tcgen05:
+//   16384 x 8 heads of 64, window 256: 91 / 334 against 56 / 165; 63: 44 / 170 against 41 / 118
+//   2048 x 8 of 32, window 256: 16.5 / 56 against 14.8 / 55; 63: 10.0 / 40 against 12.3 / 46
+//   2048 x 8 of 16, window 1001: 33 / 77 against 23 / 77; 256: 13.5 / 41 against 14.2 / 47
+//   512 x 40 x 8 of 128: 113 / 341 against 120 / 503
+bool use_tc(const WinArgs& a, bool backward) {
+  const long long w = a.D > a.Dv ? a.D : a.Dv, all = (long long)a.left + a.right + 1, win = all < a.Nk ? all : a.Nk;
+  return win * w * w >= 200000 && (long long)a.Nq * a.G >= 64 && a.Nk >= 64 && vectors(a, backward);
+}
+// Whether a CTA takes a whole sequence: two of them fit an SM, and there are that many.
+//   64 x 128 x 8 heads of 16, window 63: 11.7 / 21 us against 14.0 / 38; 8 x 256 x 8: 14.5 / 27 against 8.9 / 24
 bool use_short(const WinArgs& a, bool backward) {
   const int w = a.D > a.Dv ? a.D : a.Dv;
-  if (w > 64 || a.Nk > kWinShortRows || (long long)a.Nq * a.G > kWinShortRows) return false;
-  return use_tc(a, backward) && win_short_smem(a, w <= 16 ? 16 : (w <= 32 ? 32 : 64), backward) <= 160 * 1024;
+  if (w > 64 || a.Nk > kWinShortRows || (long long)a.Nq * a.G > kWinShortRows || (long long)a.B * a.Hkv < 296) return false;
+  return win_short_smem(a, w <= 16 ? 16 : (w <= 32 ? 32 : 64), backward) <= 100 * 1024 && vectors(a, backward);
 }
 
 }  // namespace
