@@ -38,6 +38,47 @@ __device__ __forceinline__ void column_bits(uint32_t* bits, const WinArgs& a, in
   }
 }
 
+// Rows f0 .. f0+63 (those below fh) of the queries and of dO, and columns u0 .. u0+63 of keys and values.
+template <int DP, bool VEC>
+__device__ __forceinline__ void load_queries(bf16* Qs, bf16* Os, const WinArgs& a, int b, int q0, const Src& q, const Src& g, int f0, int fh) {
+  if (VEC) {
+    constexpr int step = kThreads / (DP / 8);
+    const int first = threadIdx.x / (DP / 8);
+    copy_padded<DP>(Qs, Os, a.D, a.Dv, walk_queries(a, q, g, min(f0 + first, fh - 1), step), first, step, T, fh - f0,
+                    [&](int i) { return win_alive(a, b, q0 + i); });
+  } else {
+    auto rows = [&](const Src& s) {
+      return [&](int r) -> const bf16* {
+        const int f = f0 + r, i = f / a.G;
+        return f < fh && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
+      };
+    };
+    load_tile<DP, VEC>(Qs, q, T, threadIdx.x, kThreads, rows(q));
+    load_tile<DP, VEC>(Os, g, T, threadIdx.x, kThreads, rows(g));
+  }
+}
+template <int DP, bool VEC>
+__device__ __forceinline__ void load_keys(bf16* Ks, bf16* Vs, const WinArgs& a, int b, const Src& k, const Src& v, const WinCols& c, int u0) {
+  auto valid = [&](int j) { return a.mask == nullptr || a.mask[(long long)b * a.Nk + j] != 0; };
+  if (VEC) {
+    constexpr int step = kThreads / (DP / 8);
+    int first = threadIdx.x / (DP / 8);
+    const int ns = min(max(c.s - u0, 0), T);                  // sinks first, then the window; a tile may hold the seam
+    if (ns > 0) copy_padded<DP>(Ks, Vs, a.D, a.Dv, walk_keys(k, v, min(u0 + first, a.Nk - 1), step), first, step, ns, ns, valid);
+    while (first < ns) first += step;
+    if (first < T) copy_padded<DP>(Ks, Vs, a.D, a.Dv, walk_keys(k, v, min(c.key(u0 + first), a.Nk - 1), step), first, step, T, c.n - u0, valid);
+  } else {
+    auto keyed = [&](const Src& s) {
+      return [&](int r) -> const bf16* {
+        const int u = u0 + r;
+        return u < c.n && valid(c.key(u)) ? s.p + c.key(u) * s.sn : nullptr;
+      };
+    };
+    load_tile<DP, VEC>(Ks, k, T, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP, VEC>(Vs, v, T, threadIdx.x, kThreads, keyed(v));
+  }
+}
+
 template <int DP, bool VEC>
 __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -64,14 +105,7 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
   const Reach rc = reach(a, c, q0, f0 + 16 * warp, f1);
   auto load = [&](int t) {
     const int st = t & 1, u0 = t * T;
-    auto keyed = [&](const Src& s) {
-      return [&, u0](int r) -> const bf16* {
-        const int u = u0 + r;
-        return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
-      };
-    };
-    load_tile<DP, VEC>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP, VEC>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
+    load_keys<DP, VEC>(Ks + st * kElems<DP>, Vs + st * kElems<DP>, a, b, k, v, c, u0);
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -278,14 +312,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
   const Reach rc = reach(a, c, q0, f0 + 16 * warp, f1);
   auto load = [&](int t) {
     const int st = t & 1, u0 = t * T;
-    auto keyed = [&](const Src& s) {
-      return [&, u0](int r) -> const bf16* {
-        const int u = u0 + r;
-        return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
-      };
-    };
-    load_tile<DP, VEC>(Ks + st * kElems<DP>, k, T, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP, VEC>(Vs + st * kElems<DP>, v, T, threadIdx.x, kThreads, keyed(v));
+    load_keys<DP, VEC>(Ks + st * kElems<DP>, Vs + st * kElems<DP>, a, b, k, v, c, u0);
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -297,14 +324,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
   const float sc = a.scale * kLog2e;
   if (ntile > 0) {
-    auto rows = [&](const Src& s) {
-      return [&](int r) -> const bf16* {
-        const int f = f0 + r, i = f / a.G;
-        return f < f1 && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
-      };
-    };
-    load_tile<DP, VEC>(Qs, q, T, threadIdx.x, kThreads, rows(q));
-    load_tile<DP, VEC>(Os, g_, T, threadIdx.x, kThreads, rows(g_));
+    load_queries<DP, VEC>(Qs, Os, a, b, q0, q, g_, f0, f1);
     load(0);
     cp_wait<0>();
     __syncthreads();
@@ -434,14 +454,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
   int rp = 0;
   auto load = [&](int t) {
     const int st = t & 1, f0 = fl + t * T;
-    auto rows = [&](const Src& s) {
-      return [&, f0](int r) -> const bf16* {
-        const int f = f0 + r, i = f / a.G;
-        return f < fh && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
-      };
-    };
-    load_tile<DP, VEC>(Qs + st * kElems<DP>, q, T, threadIdx.x, kThreads, rows(q));
-    load_tile<DP, VEC>(Os + st * kElems<DP>, g_, T, threadIdx.x, kThreads, rows(g_));
+    load_queries<DP, VEC>(Qs + st * kElems<DP>, Os + st * kElems<DP>, a, b, q0, q, g_, f0, fh);
     cp_async_commit();
     // a row's lse, delta and position wait in registers until the tile before is done
     if (threadIdx.x < T) {

@@ -79,6 +79,75 @@ __device__ __forceinline__ Src source(const void* base, long long sb, long long 
   s.width = width;
   return s;
 }
+// A walk over rows of two tensors: the row that this thread copies next.  Keys
+// step by a fixed distance; the row f = i G + h of the queries carries from h to
+// i.  Additions only: a division a row kept the copies behind the products.
+struct Walk {
+  const bf16 *p0, *p1;
+  long long d0, d1, c0, c1;               // a step, and what a carry adds
+  int i, h, di, dh, G;
+  __device__ __forceinline__ void next() {
+    p0 += d0;
+    p1 += d1;
+    i += di;
+    h += dh;
+    if (h >= G) {
+      h -= G;
+      ++i;
+      p0 += c0;
+      p1 += c1;
+    }
+  }
+};
+__device__ __forceinline__ Walk walk_queries(const WinArgs& a, const Src& q, const Src& g, int f, int step) {
+  Walk w;
+  w.G = a.G;
+  w.i = f / a.G;
+  w.h = f - w.i * a.G;
+  w.di = step / a.G;
+  w.dh = step - w.di * a.G;
+  w.p0 = q.p + w.i * q.sn + w.h * q.sh;
+  w.p1 = g.p + w.i * g.sn + w.h * g.sh;
+  w.d0 = w.di * q.sn + w.dh * q.sh;
+  w.d1 = w.di * g.sn + w.dh * g.sh;
+  w.c0 = q.sn - a.G * q.sh;
+  w.c1 = g.sn - a.G * g.sh;
+  return w;
+}
+__device__ __forceinline__ Walk walk_keys(const Src& k, const Src& v, int j, int step) {
+  Walk w;
+  w.G = 0x7fffffff;
+  w.h = 0;
+  w.dh = 0;
+  w.i = j;
+  w.di = step;
+  w.p0 = k.p + j * k.sn;
+  w.p1 = v.p + j * v.sn;
+  w.d0 = step * k.sn;
+  w.d1 = step * v.sn;
+  w.c0 = w.c1 = 0;
+  return w;
+}
+
+// Rows first, first + step, ... below `end` of a padded tile (step = threads / pieces
+// a row), of which those below n exist; valid(i): row i is not masked.
+template <int DP, typename Valid>
+__device__ __forceinline__ void copy_padded(bf16* d0, bf16* d1, int w0, int w1, Walk w, int first, int step, int end, int n, Valid valid) {
+  const int c = threadIdx.x % (DP / 8) * 8;
+  const bool in0 = c < w0, in1 = c < w1;
+  const bf16 *a0 = w.p0, *a1 = w.p1;       // somewhere readable
+  uint32_t o0 = smem_u32(d0) + (first * Tile<DP>::ld + c) * 2, o1 = smem_u32(d1) + (first * Tile<DP>::ld + c) * 2;
+#pragma unroll 4
+  for (int r = first; r < end; r += step) {
+    const bool on = r < n && valid(w.i);
+    cp16_zfill(o0, on && in0 ? w.p0 + c : a0, on && in0);
+    cp16_zfill(o1, on && in1 ? w.p1 + c : a1, on && in1);
+    o0 += step * Tile<DP>::ld * 2;
+    o1 += step * Tile<DP>::ld * 2;
+    w.next();
+  }
+}
+
 // The 16 x 16 A operand at row r0, depth k0 of a tile; the 16 x 16 B operand of
 // columns n0 .. n0+15 at depth k0 (rows = columns of the product), and the one
 // whose rows are the product's depth.

@@ -381,12 +381,12 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_simt_kernel(const WinArgs 
   }
 }
 
-// dk, dv of the sinks: the partial sums in chunk order, in eight neighbouring stretches that are added in order.
+// dk, dv of the sinks: the partial sums in chunk order, in 32 neighbouring stretches that are added in order.
 template <typename E>
-__global__ void __launch_bounds__(256) win_sink_reduce_kernel(const WinArgs a) {
-  __shared__ float red[8][32];
+__global__ void __launch_bounds__(1024) win_sink_reduce_kernel(const WinArgs a) {
+  __shared__ float red[32][32];
   const int w = a.D + a.Dv, bh = blockIdx.x / a.sinks, j = blockIdx.x - bh * a.sinks, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
-  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, d = blockIdx.y * 32 + lane, per = (a.nchunk + 8) / 8;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, d = blockIdx.y * 32 + lane, per = (a.nchunk + 32) / 32;
   float x = 0.f;
   if (d < w) {
     const float* p = a.part + ((long long)bh * (a.nchunk + 1) * a.sinks + j) * w + d;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(256) win_sink_reduce_kernel(const WinArgs a) {
   red[part][lane] = x;
   __syncthreads();
   if (part != 0 || d >= w) return;
-  for (int k = 1; k < 8; ++k) x += red[k][lane];
+  for (int k = 1; k < 32; ++k) x += red[k][lane];
   const long long r = ((long long)b * a.Nk + j) * a.Hkv + hkv;
   if (d < a.D) stf(static_cast<E*>(a.d_k) + r * a.D + d, x * a.scale);
   else stf(static_cast<E*>(a.d_v) + r * a.Dv + (d - a.D), x);
@@ -434,8 +434,8 @@ cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
 
 cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s) {
   const dim3 grid((unsigned)((long long)a.B * a.Hkv * a.sinks), (unsigned)((a.D + a.Dv + 31) / 32));
-  if (f32) win_sink_reduce_kernel<float><<<grid, 256, 0, s>>>(a);
-  else win_sink_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+  if (f32) win_sink_reduce_kernel<float><<<grid, 1024, 0, s>>>(a);
+  else win_sink_reduce_kernel<__nv_bfloat16><<<grid, 1024, 0, s>>>(a);
   return cudaGetLastError();
 }
 cudaError_t launch_win_fwd_simt(const WinArgs& a, cudaStream_t s) {

@@ -59,56 +59,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-// A walk over rows of two tensors: the row that this thread copies next.  Keys
-// step by a fixed distance; the row f = i G + h of the queries carries from h to
-// i.  Additions only: a division a row kept the copies behind the products.
-struct Walk {
-  const bf16 *p0, *p1;
-  long long d0, d1, c0, c1;               // a step, and what a carry adds
-  int i, h, di, dh, G;
-  __device__ __forceinline__ void next() {
-    p0 += d0;
-    p1 += d1;
-    i += di;
-    h += dh;
-    if (h >= G) {
-      h -= G;
-      ++i;
-      p0 += c0;
-      p1 += c1;
-    }
-  }
-};
-__device__ __forceinline__ Walk walk_queries(const WinArgs& a, const Src& q, const Src& g, int f, int step) {
-  Walk w;
-  w.G = a.G;
-  w.i = f / a.G;
-  w.h = f - w.i * a.G;
-  w.di = step / a.G;
-  w.dh = step - w.di * a.G;
-  w.p0 = q.p + w.i * q.sn + w.h * q.sh;
-  w.p1 = g.p + w.i * g.sn + w.h * g.sh;
-  w.d0 = w.di * q.sn + w.dh * q.sh;
-  w.d1 = w.di * g.sn + w.dh * g.sh;
-  w.c0 = q.sn - a.G * q.sh;
-  w.c1 = g.sn - a.G * g.sh;
-  return w;
-}
-__device__ __forceinline__ Walk walk_keys(const Src& k, const Src& v, int j, int step) {
-  Walk w;
-  w.G = 0x7fffffff;
-  w.h = 0;
-  w.dh = 0;
-  w.i = j;
-  w.di = step;
-  w.p0 = k.p + j * k.sn;
-  w.p1 = v.p + j * v.sn;
-  w.d0 = step * k.sn;
-  w.d1 = step * v.sn;
-  w.c0 = w.c1 = 0;
-  return w;
-}
-
 // This thread's part of a tile of rows: neighbouring threads take neighbouring
 // 16-byte pieces (2^lg a row), so that a thread's piece and its place in the
 // swizzle stay the same from row to row.
