@@ -29,34 +29,45 @@ __device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat16
 __device__ __forceinline__ void stf(float* p, float x) { *p = x; }
 __device__ __forceinline__ void stf(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Rows [f0, f0 + 64) of (b, hkv) into dst[width][64]; rows at or beyond f1 and rows that see nothing are zero.
+// Row threadIdx.x % 64 of a tile into dst[width][64], zeros where p is null: a
+// thread keeps its row and takes every fourth run of four channels, so that a
+// warp's 32 stores of one channel lie side by side.
 template <typename E>
-__device__ void load_rows(float* dst, const E* base, long long sb, long long sn, long long sh, const WinArgs& a, int b,
-                          int hkv, int q0, int f0, int f1, int width) {
-  for (int e = threadIdx.x; e < T * width; e += kThreads) {
-    const int r = e / width, d = e - r * width, f = f0 + r;
-    float x = 0.f;
-    if (f < f1) {
-      const int i = f / a.G, g = f - i * a.G;
-      if (win_alive(a, b, q0 + i)) x = ldf(base + b * sb + (long long)i * sn + (long long)(hkv * a.G + g) * sh + d);
+__device__ __forceinline__ void load_row(float* dst, const E* p, int width) {
+  const int r = threadIdx.x & (T - 1);
+  const bool vec = sizeof(E) == 4 && (width & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+  for (int d = (threadIdx.x / T) * 4; d < width; d += kThreads / T * 4) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p != nullptr) {
+      if (vec) {
+        const float4 y = __ldg(reinterpret_cast<const float4*>(p + d));
+        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (d + k < width) x[k] = ldf(p + d + k);
+      }
     }
-    dst[d * LD + r] = x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (d + k < width) dst[(d + k) * LD + r] = x[k];
   }
 }
-// Keys of columns [u0, u0 + 64) into dst[width][64]; masked keys and columns beyond the last are zero.
+// Rows [f0, f0 + 64) of (b, hkv); rows at or beyond f1 and rows that see nothing are zero.
 template <typename E>
-__device__ void load_cols(float* dst, const E* base, long long sb, long long sn, long long sh, const WinArgs& a, int b,
+__device__ __forceinline__ void load_rows(float* dst, const E* base, long long sb, long long sn, long long sh, const WinArgs& a, int b,
+                          int hkv, int q0, int f0, int f1, int width) {
+  const int f = f0 + (threadIdx.x & (T - 1)), i = f / a.G;
+  const bool on = f < f1 && win_alive(a, b, q0 + i);
+  load_row(dst, on ? base + b * sb + i * sn + (hkv * a.G + (f - i * a.G)) * sh : nullptr, width);
+}
+// Keys of columns [u0, u0 + 64); masked keys and columns beyond the last are zero.
+template <typename E>
+__device__ __forceinline__ void load_cols(float* dst, const E* base, long long sb, long long sn, long long sh, const WinArgs& a, int b,
                           int hkv, const WinCols& c, int u0, int width) {
-  for (int e = threadIdx.x; e < T * width; e += kThreads) {
-    const int r = e / width, d = e - r * width, u = u0 + r;
-    float x = 0.f;
-    if (u < c.n) {
-      const int j = c.key(u);
-      if (a.mask == nullptr || a.mask[(long long)b * a.Nk + j] != 0)
-        x = ldf(base + b * sb + (long long)j * sn + (long long)hkv * sh + d);
-    }
-    dst[d * LD + r] = x;
-  }
+  const int u = u0 + (threadIdx.x & (T - 1)), j = c.key(u);
+  const bool on = u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + j] != 0);
+  load_row(dst, on ? base + b * sb + j * sn + hkv * sh : nullptr, width);
 }
 
 // acc[i][j] = sum_d A[d][4 ty + i] B[d][4 tx + j]
