@@ -150,54 +150,79 @@ __device__ __forceinline__ void get_param(const float* p, float none, int t, int
   }
 }
 
-// Sums of two values over the tpr threads of a row, the same in all of them.
-// Every thread of the CTA calls it (rows of more than a warp meet in shared
-// memory, in two places in turn, so that one barrier a sum is enough).
+// Sums over the tpr threads of a row, the same in all of them.  Every thread of
+// the CTA calls it (rows of more than a warp meet in shared memory, in two places
+// in turn, so that one barrier a sum is enough).
 struct RowSum {
   float2 (*red)[32];
   int turn;
+  __device__ __forceinline__ float operator()(float v, int tpr) {
+    const int w = tpr < 32 ? tpr : 32;
+    for (int o = w >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tpr > 32) v = across(make_float2(v, 0.f), tpr).x;
+    return v;
+  }
   __device__ __forceinline__ float2 operator()(float2 v, int tpr) {
     const int w = tpr < 32 ? tpr : 32;
     for (int o = w >> 1; o > 0; o >>= 1) {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
       v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
-    if (tpr > 32) {
-      const int nw = tpr >> 5, warp = threadIdx.x >> 5, first = warp / nw * nw;
-      if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
-      __syncthreads();
-      v = make_float2(0.f, 0.f);
-      for (int k = 0; k < nw; ++k) {
-        v.x += red[turn][first + k].x;
-        v.y += red[turn][first + k].y;
-      }
-      turn ^= 1;
+    return tpr > 32 ? across(v, tpr) : v;
+  }
+  __device__ __forceinline__ float2 across(float2 v, int tpr) {
+    const int nw = tpr >> 5, warp = threadIdx.x >> 5, first = warp / nw * nw;
+    if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
+    __syncthreads();
+    v = make_float2(0.f, 0.f);
+    for (int k = 0; k < nw; ++k) {
+      v.x += red[turn][first + k].x;
+      v.y += red[turn][first + k].y;
     }
+    turn ^= 1;
     return v;
   }
 };
 
-// mean and rstd of the row (elements beyond C hold 0 and are left out)
+// Elements of a row that this thread has: its first n (all or none with VEC).  The
+// others hold 0, their parameters are 0 (see get_param) and they are never stored,
+// so that only the sums of what is not 0 by itself have to leave them out.
 template <bool VEC>
-__device__ __forceinline__ float2 moments(const float (&z)[E], int t, const NormArgs& a, RowSum& sum) {
-  const float inv = 1.f / (float)a.C;
-  float mean = 0.f;
-  if (!a.rms) {
-    float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v.x += z[e];
-    mean = sum(v, a.tpr).x * inv;
-  }
-  float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float d = col<VEC>(t, a.tpr, e) < a.C ? z[e] - mean : 0.f;
-    v.x = fmaf(d, d, v.x);
-  }
-  return make_float2(mean, rsqrtf(sum(v, a.tpr).x * inv + a.eps));
+__device__ __forceinline__ int mine(int t, int tpr, int C) {
+  if (VEC) return t * E < C ? E : 0;
+  const int n = (C - t + tpr - 1) / tpr;
+  return t < C ? (n < E ? n : E) : 0;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+// mean and rstd of the row
+template <bool VEC>
+__device__ __forceinline__ float2 moments(const float (&z)[E], int n, const NormArgs& a, float inv, RowSum& sum) {
+  float mean = 0.f;
+  if (!a.rms) {
+    float v = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v += z[e];
+    mean = sum(v, a.tpr) * inv;
+  }
+  float v = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float d = VEC || e < n ? z[e] - mean : 0.f;
+    v = fmaf(d, d, v);
+  }
+  if (VEC && n == 0) v = 0.f;
+  return make_float2(mean, rsqrtf(sum(v, a.tpr) * inv + a.eps));
+}
+
+// 1 / (1 + 2^(-x log2 e)); the rounding of x log2 e, which 2^() would pass on
+// multiplied by ln 2, is put back.
+__device__ __forceinline__ float sigmoid(float x) {
+  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+  const float y = -x * kLog2e, r = fmaf(-x, kLog2e, -y);
+  float p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(y));
+  return __fdividef(1.f, 1.f + fmaf(p, r * kLn2, p));
+}
 
 template <typename TS, typename TB, bool VEC, int BLOCK>
 __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const NormArgs a) {
@@ -209,6 +234,8 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
   RowSum sum{red, 0};
   const int t = threadIdx.x & (a.tpr - 1), rpb = BLOCK / a.tpr;
   const bool branch = a.u != nullptr, gated = a.gate != nullptr;
+  const int n = mine<VEC>(t, a.tpr, a.C);
+  const float inv = 1.f / (float)a.C;
   const long long step = (long long)gridDim.x * rpb;
   const long long first = (long long)blockIdx.x * rpb + threadIdx.x / a.tpr;     // this thread's rows: first, first + step, ...
   bool soon;                                                                     // whether the row to be fetched next is valid
@@ -239,7 +266,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
     if (branch) {
       if (a.post_w != nullptr) {
         float w[E], b[E];
-        mu = moments<VEC>(u, t, a, sum);
+        mu = moments<VEC>(u, n, a, inv, sum);
         get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
         get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, b);
 #pragma unroll
@@ -250,7 +277,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (gated) u[e] *= sigmoid(g[e]);
-        if (live && col<VEC>(t, a.tpr, e) < a.C) s[e] = fmaf(ga[e], u[e], s[e]);
+        if (live) s[e] = fmaf(ga[e], u[e], s[e]);
       }
       if (in) put_row<VEC>(static_cast<TS*>(a.r) + o, t, a.tpr, a.C, s);
     }
@@ -258,7 +285,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
       float w[E], b[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) s[e] = live ? s[e] : 0.f;
-      mr = moments<VEC>(s, t, a, sum);
+      mr = moments<VEC>(s, n, a, inv, sum);
       get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, w);
       get_param<VEC>(a.pre_b, 0.f, t, a.tpr, a.C, b);
 #pragma unroll
@@ -289,6 +316,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
   const int t = threadIdx.x & (a.tpr - 1), rpb = BLOCK / a.tpr;
   const float inv = 1.f / (float)a.C;
   const bool branch = a.u != nullptr, gated = a.gate != nullptr, pre = a.d_x != nullptr, thru = a.d_r != nullptr;
+  const int n = mine<VEC>(t, a.tpr, a.C);
   float dga[E], dpw[E], dpb[E], dqw[E], dqb[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) dga[e] = dpw[e] = dpb[e] = dqw[e] = dqb[e] = 0.f;
@@ -342,9 +370,8 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
       get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const bool cin = col<VEC>(t, a.tpr, e) < a.C;
         if (a.post_w != nullptr) {
-          u[e] = cin ? (u[e] - st.x) * st.y : 0.f;
+          u[e] = (u[e] - st.x) * st.y;
           w[e] = fmaf(u[e], w[e], pb[e]);
         } else {
           w[e] = u[e];
@@ -359,7 +386,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
       float2 m = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        s[e] = col<VEC>(t, a.tpr, e) < a.C ? (s[e] - st.z) * st.w : 0.f;      // rhat
+        s[e] = (s[e] - st.z) * st.w;                              // rhat
         dqw[e] = fmaf(dx[e], s[e], dqw[e]);
         dqb[e] += dx[e];
         dx[e] *= qw[e];
@@ -367,10 +394,10 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
         m.y = fmaf(dx[e], s[e], m.y);
       }
       m = sums(m, a.tpr);
-      const float c1 = a.rms ? 0.f : m.x * inv, c2 = m.y * inv;
+      const float c1 = a.rms || (VEC && n == 0) ? 0.f : m.x * inv, c2 = VEC && n == 0 ? 0.f : m.y * inv;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (live) dr[e] = fmaf(st.w, dx[e] - c1 - s[e] * c2, dr[e]);
+      for (int e = 0; e < E; ++e)                                 // a masked row has st.w = 0
+        if (VEC || e < n) dr[e] = fmaf(st.w, dx[e] - c1 - s[e] * c2, dr[e]);
     }
     if (a.d_s != nullptr && in) put_row<VEC>(static_cast<TS*>(a.d_s) + o, t, a.tpr, a.C, dr);
     if (branch) {
@@ -380,8 +407,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
       float2 m = make_float2(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const bool cin = live && col<VEC>(t, a.tpr, e) < a.C;
-        const float d = cin ? dr[e] : 0.f;
+        const float d = live ? dr[e] : 0.f;
         dga[e] = fmaf(d, g[e] * w[e], dga[e]);
         const float dgy = d * ga[e], dy = dgy * g[e];
         g[e] = dgy * w[e] * g[e] * (1.f - g[e]);
@@ -437,21 +463,23 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
   for (int c = threadIdx.x; c < 5 * a.C; c += blockDim.x) out[c] = acc_s[c];
 }
 
-// Sums over the CTAs' lines: 8 interleaved partial sums a column, added in order.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* part, int lines, int C, float* const o0, float* const o1,
-                                                          float* const o2, float* const o3, float* const o4) {
-  __shared__ float red[8][32];
+// Sums over the CTAs' lines: 32 interleaved partial sums a column, added in order.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, int lines, int C, float* const o0, float* const o1,
+                                                           float* const o2, float* const o3, float* const o4) {
+  __shared__ float red[32][32];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5, n = 5 * C;
   float x = 0.f;
-  if (c < n)
-    for (int l = k; l < lines; l += 8) x += part[(size_t)l * n + c];
+  if (c < n) {
+#pragma unroll 8
+    for (int l = k; l < lines; l += 32) x += part[(size_t)l * n + c];
+  }
   red[k][threadIdx.x & 31] = x;
   __syncthreads();
   if (k == 0 && c < n) {
-    for (int q = 1; q < 8; ++q) x += red[q][threadIdx.x];
-    float* const o[5] = {o0, o1, o2, o3, o4};
-    float* p = o[c / C];
-    if (p != nullptr) p[c % C] = x;
+    for (int q = 1; q < 32; ++q) x += red[q][threadIdx.x];
+    const int which = c / C;
+    float* p = which == 0 ? o0 : (which == 1 ? o1 : (which == 2 ? o2 : (which == 3 ? o3 : o4)));
+    if (p != nullptr) p[c - which * C] = x;
   }
 }
 
@@ -603,7 +631,7 @@ FIPA_API fipa_status fipa_norm_residual_backward(const fipa_norm_dims* d, const 
   const int grid = norm_bwd_grid(d->rows, d->C);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (grid > 0 && norm_dispatch(d, a, vec, true, grid, s) != cudaSuccess) return FIPA_ERR_CUDA;
-  norm_reduce_kernel<<<(5 * d->C + 31) / 32, 256, 0, s>>>(a.part, grid, d->C, g->res_scale, g->post_w, g->post_b, g->pre_w,
+  norm_reduce_kernel<<<(5 * d->C + 31) / 32, 1024, 0, s>>>(a.part, grid, d->C, g->res_scale, g->post_w, g->post_b, g->pre_w,
                                                          g->pre_b);
   return cudaGetLastError() == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
 }
