@@ -45,6 +45,36 @@ __device__ __forceinline__ float cvt(__nv_bfloat16 x) { return __bfloat162float(
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Two float32 operations an instruction: a row's arithmetic is what bounds these
+// kernels beside the memory.
+__device__ __forceinline__ unsigned long long bits2(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair2(unsigned long long a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+constexpr int H = E / 2;                   // pairs of a row per thread
+
 // The thread's elements of a row: 8 neighbours by 16-byte accesses (VEC), or
 // every tpr-th element, so that a warp's accesses are contiguous at any width.
 template <bool VEC>
@@ -79,74 +109,79 @@ struct Slot {
       }
     }
   }
-  static __device__ __forceinline__ void get(const uint8_t* slot, const T* p, int t, int tpr, int C, bool on, float (&x)[E]) {
+  static __device__ __forceinline__ void get(const uint8_t* slot, const T* p, int t, int tpr, int C, bool on, float2 (&x)[H]) {
     if (VEC && sizeof(T) == 2) {
       const uint4 w = *reinterpret_cast<const uint4*>(slot + threadIdx.x * 16);
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(ww[e] << 16);
-        x[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
-      }
+      for (int e = 0; e < H; ++e) x[e] = make_float2(__uint_as_float(ww[e] << 16), __uint_as_float(ww[e] & 0xffff0000u));
     } else if (VEC) {
       const float4 lo = *reinterpret_cast<const float4*>(slot + threadIdx.x * 16);
       const float4 hi = *reinterpret_cast<const float4*>(slot + (BLOCK + threadIdx.x) * 16);
-      x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-      x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+      x[0] = make_float2(lo.x, lo.y); x[1] = make_float2(lo.z, lo.w);
+      x[2] = make_float2(hi.x, hi.y); x[3] = make_float2(hi.z, hi.w);
     } else if (sizeof(T) == 4) {
+      const float* f = reinterpret_cast<const float*>(slot) + threadIdx.x;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = *reinterpret_cast<const float*>(slot + (e * BLOCK + threadIdx.x) * 4);
+      for (int e = 0; e < H; ++e) x[e] = make_float2(f[2 * e * BLOCK], f[(2 * e + 1) * BLOCK]);
     } else {
+      float f[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int c = t + e * tpr;
-        x[e] = on && c < C ? cvt(p[c]) : 0.f;
+        f[e] = on && c < C ? cvt(p[c]) : 0.f;
       }
+#pragma unroll
+      for (int e = 0; e < H; ++e) x[e] = make_float2(f[2 * e], f[2 * e + 1]);
     }
   }
 };
 template <bool VEC, typename T>
-__device__ __forceinline__ void put_row(T* p, int t, int tpr, int C, const float (&v)[E]) {
+__device__ __forceinline__ void put_row(T* p, int t, int tpr, int C, const float2 (&v)[H]) {
   if (VEC) {
     if (t * E >= C) return;
     if (sizeof(T) == 2) {
       uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+      for (int e = 0; e < H; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[e].x, v[e].y);
         w[e] = *reinterpret_cast<const uint32_t*>(&h);
       }
       *reinterpret_cast<uint4*>(p + t * E) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       float4* q = reinterpret_cast<float4*>(p + t * E);
-      q[0] = make_float4(v[0], v[1], v[2], v[3]);
-      q[1] = make_float4(v[4], v[5], v[6], v[7]);
+      q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = t + e * tpr;
-      if (c < C) put(p + c, v[e]);
+    for (int e = 0; e < H; ++e) {
+      const int c = t + 2 * e * tpr;
+      if (c < C) put(p + c, v[e].x);
+      if (c + tpr < C) put(p + c + tpr, v[e].y);
     }
   }
 }
 // Parameters are read anew for every row: they stay in L1, and the registers go to rows in flight.
 template <bool VEC>
-__device__ __forceinline__ void get_param(const float* p, float none, int t, int tpr, int C, float (&v)[E]) {
+__device__ __forceinline__ void get_param(const float* p, float none, int t, int tpr, int C, float2 (&v)[H]) {
   if (p == nullptr) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = none;
+    for (int e = 0; e < H; ++e) v[e] = both(none);
   } else if (VEC) {
     float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
     if (t * E < C) {
       lo = __ldg(reinterpret_cast<const float4*>(p + t * E));
       hi = __ldg(reinterpret_cast<const float4*>(p + t * E) + 1);
     }
-    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    v[0] = make_float2(lo.x, lo.y); v[1] = make_float2(lo.z, lo.w);
+    v[2] = make_float2(hi.x, hi.y); v[3] = make_float2(hi.z, hi.w);
   } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = t + e * tpr < C ? __ldg(p + t + e * tpr) : 0.f;
+    for (int e = 0; e < H; ++e) {
+      const int c = t + 2 * e * tpr;
+      v[e] = make_float2(c < C ? __ldg(p + c) : 0.f, c + tpr < C ? __ldg(p + c + tpr) : 0.f);
+    }
   }
 }
 
@@ -194,34 +229,43 @@ __device__ __forceinline__ int mine(int t, int tpr, int C) {
   return t < C ? (n < E ? n : E) : 0;
 }
 
-// mean and rstd of the row
+// Element pairs that exist, as factors 1 or 0 of what would not be 0 by itself (VEC: all or none).
 template <bool VEC>
-__device__ __forceinline__ float2 moments(const float (&z)[E], int n, const NormArgs& a, float inv, RowSum& sum) {
+__device__ __forceinline__ float2 there(int e, int n) {
+  return VEC ? both(1.f) : make_float2(2 * e < n ? 1.f : 0.f, 2 * e + 1 < n ? 1.f : 0.f);
+}
+
+// mean and rstd of the row; z becomes z - mean
+template <bool VEC>
+__device__ __forceinline__ float2 moments(float2 (&z)[H], int n, const NormArgs& a, float inv, RowSum& sum) {
   float mean = 0.f;
   if (!a.rms) {
-    float v = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v += z[e];
-    mean = sum(v, a.tpr) * inv;
+    const float2 v = add2(add2(z[0], z[1]), add2(z[2], z[3]));
+    mean = sum(v.x + v.y, a.tpr) * inv;
   }
-  float v = 0.f;
+  float2 v = both(0.f);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float d = VEC || e < n ? z[e] - mean : 0.f;
-    v = fmaf(d, d, v);
+  for (int e = 0; e < H; ++e) {
+    z[e] = add2(z[e], both(-mean));
+    if (!VEC) z[e] = mul2(z[e], there<VEC>(e, n));
+    v = fma2(z[e], z[e], v);
   }
-  if (VEC && n == 0) v = 0.f;
-  return make_float2(mean, rsqrtf(sum(v, a.tpr) * inv + a.eps));
+  const float q = VEC && n == 0 ? 0.f : v.x + v.y;
+  return make_float2(mean, rsqrtf(sum(q, a.tpr) * inv + a.eps));
 }
 
 // 1 / (1 + 2^(-x log2 e)); the rounding of x log2 e, which 2^() would pass on
 // multiplied by ln 2, is put back.
-__device__ __forceinline__ float sigmoid(float x) {
+__device__ __forceinline__ float2 sigmoid(float2 x) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-  const float y = -x * kLog2e, r = fmaf(-x, kLog2e, -y);
-  float p;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(y));
-  return __fdividef(1.f, 1.f + fmaf(p, r * kLn2, p));
+  const float2 y = mul2(x, both(-kLog2e)), r = fma2(x, both(-kLog2e), make_float2(-y.x, -y.y));
+  float2 p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(y.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(y.y));
+  p = add2(fma2(p, mul2(r, both(kLn2)), p), both(1.f));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(p.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(p.y));
+  return p;
 }
 
 template <typename TS, typename TB, bool VEC, int BLOCK>
@@ -257,7 +301,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
     const bool in = row < a.rows, live = live0;
     const long long o = (in ? row : 0) * a.C;
     const uint8_t* slot = ring + (k & 1) * kStage;
-    float s[E], u[E], g[E];
+    float2 s[H], u[H], g[H];
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     SS::get(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, in, s);
     if (branch) SB::get(slot + SS::kBytes, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
@@ -265,31 +309,35 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
     float2 mu = make_float2(0.f, 0.f), mr = mu;
     if (branch) {
       if (a.post_w != nullptr) {
-        float w[E], b[E];
+        float2 w[H], b[H];
         mu = moments<VEC>(u, n, a, inv, sum);
         get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
         get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, b);
 #pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = fmaf((u[e] - mu.x) * mu.y, w[e], b[e]);
+        for (int e = 0; e < H; ++e) u[e] = fma2(mul2(u[e], both(mu.y)), w[e], b[e]);
       }
-      float ga[E];
+      float2 ga[H];
       get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (gated) u[e] *= sigmoid(g[e]);
-        if (live) s[e] = fmaf(ga[e], u[e], s[e]);
+      for (int e = 0; e < H; ++e) {
+        if (gated) u[e] = mul2(u[e], sigmoid(g[e]));
+        const float2 r = fma2(ga[e], u[e], s[e]);
+        s[e] = live ? r : s[e];
       }
       if (in) put_row<VEC>(static_cast<TS*>(a.r) + o, t, a.tpr, a.C, s);
     }
     if (a.pre_w != nullptr) {
-      float w[E], b[E];
+      float2 w[H], b[H];
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[e] = live ? s[e] : 0.f;
+      for (int e = 0; e < H; ++e) s[e] = live ? s[e] : both(0.f);
       mr = moments<VEC>(s, n, a, inv, sum);
       get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, w);
       get_param<VEC>(a.pre_b, 0.f, t, a.tpr, a.C, b);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[e] = live ? fmaf((s[e] - mr.x) * mr.y, w[e], b[e]) : 0.f;
+      for (int e = 0; e < H; ++e) {
+        const float2 x = fma2(mul2(s[e], both(mr.y)), w[e], b[e]);
+        s[e] = live ? x : both(0.f);
+      }
       if (in) put_row<VEC>(static_cast<TB*>(a.x) + o, t, a.tpr, a.C, s);
     }
     if (a.stats != nullptr && in && t == 0)
@@ -317,9 +365,9 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
   const float inv = 1.f / (float)a.C;
   const bool branch = a.u != nullptr, gated = a.gate != nullptr, pre = a.d_x != nullptr, thru = a.d_r != nullptr;
   const int n = mine<VEC>(t, a.tpr, a.C);
-  float dga[E], dpw[E], dpb[E], dqw[E], dqb[E];
+  float2 dga[H], dpw[H], dpb[H], dqw[H], dqb[H];
 #pragma unroll
-  for (int e = 0; e < E; ++e) dga[e] = dpw[e] = dpb[e] = dqw[e] = dqb[e] = 0.f;
+  for (int e = 0; e < H; ++e) dga[e] = dpw[e] = dpb[e] = dqw[e] = dqb[e] = both(0.f);
   const long long step = (long long)gridDim.x * rpb;
   const long long first = (long long)blockIdx.x * rpb + threadIdx.x / a.tpr;     // this thread's rows: first, first + step, ...
   bool soon;                                                                     // whether the row to be fetched next is valid
@@ -345,14 +393,14 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
     const bool in = row < a.rows, live = live0;
     const long long o = (in ? row : 0) * a.C;
     const uint8_t* slot = ring + (k % NS) * kStage;
-    float s[E], u[E], g[E], dr[E], dx[E];
+    float2 s[H], u[H], g[H], dr[H], dx[H];
     asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
     SS::get(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, live, s);
     if (thru) {
       SS::get(slot + SS::kBytes, static_cast<const TS*>(a.d_r) + o, t, a.tpr, a.C, in, dr);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) dr[e] = 0.f;
+      for (int e = 0; e < H; ++e) dr[e] = both(0.f);
     }
     slot += 2 * SS::kBytes;
     if (branch) SB::get(slot, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
@@ -361,68 +409,69 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
     const float4 st = nst;
     if (live1) nst = *reinterpret_cast<const float4*>(a.stats + 4 * (row + step));
     else nst = make_float4(0.f, 0.f, 0.f, 0.f);
-    float w[E];
+    float2 w[H];
     // u -> uhat; y in w; s -> r; gate -> sigmoid
     if (branch) {
-      float pb[E], ga[E];
+      float2 pb[H], ga[H];
       get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
       get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, pb);
       get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int e = 0; e < H; ++e) {
         if (a.post_w != nullptr) {
-          u[e] = (u[e] - st.x) * st.y;
-          w[e] = fmaf(u[e], w[e], pb[e]);
+          u[e] = mul2(add2(u[e], both(-st.x)), both(st.y));
+          w[e] = fma2(u[e], w[e], pb[e]);
         } else {
           w[e] = u[e];
         }
-        g[e] = gated ? sigmoid(g[e]) : 1.f;
-        s[e] = fmaf(ga[e], g[e] * w[e], s[e]);
+        g[e] = gated ? sigmoid(g[e]) : both(1.f);
+        s[e] = fma2(ga[e], mul2(g[e], w[e]), s[e]);
       }
     }
     if (pre) {
-      float qw[E];
+      float2 qw[H], mx = both(0.f), my = both(0.f);
       get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, qw);
-      float2 m = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        s[e] = (s[e] - st.z) * st.w;                              // rhat
-        dqw[e] = fmaf(dx[e], s[e], dqw[e]);
-        dqb[e] += dx[e];
-        dx[e] *= qw[e];
-        m.x += dx[e];
-        m.y = fmaf(dx[e], s[e], m.y);
+      for (int e = 0; e < H; ++e) {
+        s[e] = mul2(add2(s[e], both(-st.z)), both(st.w));         // rhat
+        dqw[e] = fma2(dx[e], s[e], dqw[e]);
+        dqb[e] = add2(dqb[e], dx[e]);
+        dx[e] = mul2(dx[e], qw[e]);
+        mx = add2(mx, dx[e]);
+        my = fma2(dx[e], s[e], my);
       }
-      m = sums(m, a.tpr);
+      const float2 m = sums(make_float2(mx.x + mx.y, my.x + my.y), a.tpr);
       const float c1 = a.rms || (VEC && n == 0) ? 0.f : m.x * inv, c2 = VEC && n == 0 ? 0.f : m.y * inv;
 #pragma unroll
-      for (int e = 0; e < E; ++e)                                 // a masked row has st.w = 0
-        if (VEC || e < n) dr[e] = fmaf(st.w, dx[e] - c1 - s[e] * c2, dr[e]);
+      for (int e = 0; e < H; ++e) {                               // a masked row has st.w = 0
+        float2 d = fma2(s[e], both(-c2), add2(dx[e], both(-c1)));
+        if (!VEC) d = mul2(d, there<VEC>(e, n));
+        dr[e] = fma2(both(st.w), d, dr[e]);
+      }
     }
     if (a.d_s != nullptr && in) put_row<VEC>(static_cast<TS*>(a.d_s) + o, t, a.tpr, a.C, dr);
     if (branch) {
-      float ga[E], pw[E];
+      float2 ga[H], pw[H], mx = both(0.f), my = both(0.f);
       get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
       get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, pw);
-      float2 m = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = live ? dr[e] : 0.f;
-        dga[e] = fmaf(d, g[e] * w[e], dga[e]);
-        const float dgy = d * ga[e], dy = dgy * g[e];
-        g[e] = dgy * w[e] * g[e] * (1.f - g[e]);
-        dpw[e] = fmaf(dy, u[e], dpw[e]);
-        dpb[e] += dy;
-        w[e] = a.post_w != nullptr ? dy * pw[e] : dy;
-        m.x += w[e];
-        m.y = fmaf(w[e], u[e], m.y);
+      for (int e = 0; e < H; ++e) {
+        const float2 d = live ? dr[e] : both(0.f), gy = mul2(g[e], w[e]);
+        dga[e] = fma2(d, gy, dga[e]);
+        const float2 dgy = mul2(d, ga[e]), dy = mul2(dgy, g[e]);
+        g[e] = mul2(mul2(dgy, gy), add2(both(1.f), make_float2(-g[e].x, -g[e].y)));
+        dpw[e] = fma2(dy, u[e], dpw[e]);
+        dpb[e] = add2(dpb[e], dy);
+        w[e] = a.post_w != nullptr ? mul2(dy, pw[e]) : dy;
+        mx = add2(mx, w[e]);
+        my = fma2(w[e], u[e], my);
       }
       if (a.d_gate != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_gate) + o, t, a.tpr, a.C, g);
       if (a.post_w != nullptr) {
-        m = sums(m, a.tpr);
+        const float2 m = sums(make_float2(mx.x + mx.y, my.x + my.y), a.tpr);
         const float e1 = a.rms ? 0.f : m.x * inv, e2 = m.y * inv;
 #pragma unroll
-        for (int e = 0; e < E; ++e) w[e] = st.y * (w[e] - e1 - u[e] * e2);
+        for (int e = 0; e < H; ++e) w[e] = mul2(both(st.y), fma2(u[e], both(-e2), add2(w[e], both(-e1))));
       }
       if (a.d_u != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_u) + o, t, a.tpr, a.C, w);
     }
@@ -436,14 +485,14 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
   __syncthreads();                           // the ring's memory now takes the sums
   // the CTA's rows in order, then one line of sums per CTA
   float* out = a.part + (size_t)blockIdx.x * 5 * a.C;
-  float* sum[5] = {dga, dpw, dpb, dqw, dqb};
+  float2* sum[5] = {dga, dpw, dpb, dqw, dqb};
   if (rpb == 1) {
 #pragma unroll
     for (int k = 0; k < 5; ++k)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int c = col<VEC>(t, a.tpr, e);
-        if (c < a.C) out[k * a.C + c] = sum[k][e];
+        if (c < a.C) out[k * a.C + c] = e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x;
       }
     return;
   }
@@ -455,7 +504,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const int c = col<VEC>(t, a.tpr, e);
-          if (c < a.C) acc_s[k * a.C + c] = sum[k][e] + (q == 0 ? 0.f : acc_s[k * a.C + c]);
+          if (c < a.C) acc_s[k * a.C + c] = (e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x) + (q == 0 ? 0.f : acc_s[k * a.C + c]);
         }
     }
     __syncthreads();
