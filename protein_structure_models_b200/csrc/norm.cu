@@ -328,8 +328,6 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
     }
     if (a.pre_w != nullptr) {
       float2 w[H], b[H];
-#pragma unroll
-      for (int e = 0; e < H; ++e) s[e] = live ? s[e] : both(0.f);
       mr = moments<VEC>(s, n, a, inv, sum);
       get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, w);
       get_param<VEC>(a.pre_b, 0.f, t, a.tpr, a.C, b);
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
   typedef Slot<TB, VEC, BLOCK> SB;
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kStage = 2 * SS::kBytes + 3 * SB::kBytes, NS = bwd_slots(BLOCK);
-  float* acc_s = reinterpret_cast<float*>(ring);          // [5][C] when several rows share a CTA
+  float* acc_s = reinterpret_cast<float*>(ring);          // [rows of the CTA][5][C] when several share it
   __shared__ float2 red[2][32];
   RowSum sums{red, 0};
   const int t = threadIdx.x & (a.tpr - 1), rpb = BLOCK / a.tpr;
@@ -496,20 +494,21 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
       }
     return;
   }
-  const int mine = threadIdx.x / a.tpr;
-  for (int q = 0; q < rpb; ++q) {
-    if (mine == q) {
+  // every row's sums side by side, then one thread a column adds them in row order
+  const int q = threadIdx.x / a.tpr, line = 5 * a.C;
 #pragma unroll
-      for (int k = 0; k < 5; ++k)
+  for (int k = 0; k < 5; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int c = col<VEC>(t, a.tpr, e);
-          if (c < a.C) acc_s[k * a.C + c] = (e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x) + (q == 0 ? 0.f : acc_s[k * a.C + c]);
-        }
+    for (int e = 0; e < E; ++e) {
+      const int c = col<VEC>(t, a.tpr, e);
+      if (c < a.C) acc_s[q * line + k * a.C + c] = e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x;
     }
-    __syncthreads();
+  __syncthreads();
+  for (int c = threadIdx.x; c < line; c += BLOCK) {
+    float x = acc_s[c];
+    for (int r = 1; r < rpb; ++r) x += acc_s[r * line + c];
+    out[c] = x;
   }
-  for (int c = threadIdx.x; c < 5 * a.C; c += blockDim.x) out[c] = acc_s[c];
 }
 
 // Sums over the CTAs' lines: 32 interleaved partial sums a column, added in order.
@@ -558,7 +557,8 @@ template <typename TS, typename TB, bool VEC, int BLOCK>
 cudaError_t norm_launch(const NormArgs& a, bool bwd, int grid, cudaStream_t st) {
   const int ks = Slot<TS, VEC, BLOCK>::kBytes, kb = Slot<TB, VEC, BLOCK>::kBytes;
   size_t smem = bwd ? (size_t)bwd_slots(BLOCK) * (2 * ks + 3 * kb) : 2 * (size_t)(ks + 2 * kb);
-  if (bwd && BLOCK > a.tpr && smem < (size_t)5 * a.C * sizeof(float)) smem = (size_t)5 * a.C * sizeof(float);
+  const size_t sums = bwd && BLOCK > a.tpr ? (size_t)(BLOCK / a.tpr) * 5 * a.C * sizeof(float) : 0;
+  if (smem < sums) smem = sums;
   const cudaError_t e = allow_max_smem(bwd ? reinterpret_cast<const void*>(&norm_bwd_kernel<TS, TB, VEC, BLOCK>)
                                            : reinterpret_cast<const void*>(&norm_fwd_kernel<TS, TB, VEC, BLOCK>));
   if (e != cudaSuccess) return e;
