@@ -449,9 +449,9 @@ class Fipa:
         (+ "lse" [B,H,Nq] float32, which the backward needs)."""
         w, hd = self._window_problem(q, k, v, window, sinks, mask, q_start, scale)
         if out is None:
-            out = {"out": torch.empty((w.B, w.Nq, w.H, w.Dv), dtype=q.dtype, device=q.device)}
+            out = {"out": q.new_empty((w.B, w.Nq, w.H, w.Dv))}
             if want_lse:
-                out["lse"] = torch.empty((w.B, w.H, w.Nq), dtype=torch.float32, device=q.device)
+                out["lse"] = q.new_empty((w.B, w.H, w.Nq), dtype=torch.float32)
         else:
             self._check_buffers(out, {"out": ((w.B, w.Nq, w.H, w.Dv), q.dtype),
                                       "lse": ((w.B, w.H, w.Nq), torch.float32)}, q.device, ("out",))
@@ -486,11 +486,11 @@ class Fipa:
         shapes = {"q": ((w.B, w.Nq, w.H, w.D), td), "k": ((w.B, w.Nk, w.Hkv, w.D), td),
                   "v": ((w.B, w.Nk, w.Hkv, w.Dv), td)}
         if grads is None:
-            grads = {key: torch.empty(s, dtype=dt, device=dev) for key, (s, dt) in shapes.items()}
+            grads = {key: q.new_empty(s) for key, (s, _) in shapes.items()}
         else:
             self._check_buffers(grads, shapes, dev, ("q", "k", "v"))
         if workspace is None:
-            workspace = torch.empty(self._window_workspace(w), dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(self._window_workspace(w), dtype=torch.uint8)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
         self._check(self.lib.fipa_window_attention_backward(
@@ -623,29 +623,32 @@ def _code(t: torch.Tensor) -> int:
 
 def _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype):
     """Checks the inputs of the junction; returns its dims, inputs, branch type and parameters."""
-    dev = s.device
-    if dev.type != "cuda" or s.dim() < 1:
+    dev, shape, ts = s.device, s.shape, s.dtype
+    if dev.type != "cuda" or not shape:
         raise ValueError("s: need a CUDA tensor [..., C]")
-    C = s.shape[-1]
-    _need("s", s, s.shape, _FLOATS, dev)
-    tb = u.dtype if u is not None else (branch_dtype or s.dtype)
-    if u is not None:
-        _need("u", u, s.shape, _FLOATS, dev)
-    if gate is not None:
-        _need("gate", gate, s.shape, (tb,), dev)
+    C = shape[-1]
+    tb = u.dtype if u is not None else (branch_dtype or ts)
+    if ts not in _FLOATS or tb not in _FLOATS:
+        raise ValueError("s, u, branch_dtype: float32 or bfloat16")
+    at = s.get_device()
+    for name, t, dt in (("s", s, ts), ("u", u, tb), ("gate", gate, tb)):
+        if t is not None and (t.dtype != dt or t.shape != shape or not t.is_contiguous() or t.get_device() != at):
+            raise ValueError(f"{name}: need a contiguous {dt} tensor {tuple(shape)} on {dev}")
     if mask is not None:
-        _need("mask", mask, s.shape[:-1], _BYTES, dev)
-    par = dict(zip(NORM_PARAMS, (res_scale, *(post or (None, None)), *(pre or (None, None)))))
+        _need("mask", mask, shape[:-1], _BYTES, dev)
+    post_w, post_b = post or (None, None)
+    pre_w, pre_b = pre or (None, None)
+    par = {"res_scale": res_scale, "post_w": post_w, "post_b": post_b, "pre_w": pre_w, "pre_b": pre_b}
     for name, t in par.items():
-        if t is not None:
-            _need(name, t, (C,), (torch.float32,), dev)
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.numel() != C or not t.is_contiguous()
+                              or t.get_device() != at):
+            raise ValueError(f"{name}: need a contiguous float32 tensor ({C},) on {dev}")
     if norm not in ("layer", "rms"):
         raise ValueError('norm: "layer" or "rms"')
-    if tb not in _FLOATS:
-        raise ValueError("branch_dtype: float32 or bfloat16")
-    rows = s.numel() // C if C else 0
-    d = FipaNormDims(rows, C, _code(s), F32 if tb == torch.float32 else BF16, 0 if norm == "layer" else 1, float(eps))
-    i = FipaNormInputs(*[None if t is None else t.data_ptr() for t in (s, u, gate, mask, *par.values())])
+    d = FipaNormDims(s.numel() // C if C else 0, C, F32 if ts == torch.float32 else BF16,
+                     F32 if tb == torch.float32 else BF16, 0 if norm == "layer" else 1, eps)
+    i = FipaNormInputs(s.data_ptr(), _addr(u), _addr(gate), _addr(mask), _addr(res_scale), _addr(post_w), _addr(post_b),
+                       _addr(pre_w), _addr(pre_b))
     return d, i, tb, par
 
 
@@ -670,20 +673,21 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
     d, i, tb, _ = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
     dev = s.device
     with _OnDevice(dev):
-        want = {}
-        if u is not None:
-            want["r"] = (s.shape, s.dtype)
-        if pre is not None:
-            want["x"] = (s.shape, tb)
         if out is None:
+            out = {}
+            if u is not None:
+                out["r"] = torch.empty_like(s)
+            if pre is not None:
+                out["x"] = torch.empty_like(s, dtype=tb) if u is None else torch.empty_like(u)
             if want_stats:
-                want["stats"] = ((d.rows, 4), torch.float32)
-            out = {k: torch.empty(sh, dtype=dt, device=dev) for k, (sh, dt) in want.items()}
+                out["stats"] = s.new_empty((d.rows, 4), dtype=torch.float32)
         else:
-            for k, (sh, dt) in (want | {"stats": ((d.rows, 4), torch.float32)}).items():
+            want = {"stats": ((d.rows, 4), torch.float32, False), "r": (s.shape, s.dtype, u is not None),
+                    "x": (s.shape, tb, pre is not None)}
+            for k, (sh, dt, needed) in want.items():
                 if k in out:
                     _need(k, out[k], sh, (dt,), dev)
-                elif k in want:
+                elif needed:
                     raise ValueError(f"{k}: buffer missing")
         st = _raw_stream(stream, dev.index)
         _ok(lib.fipa_norm_residual(d, i, _addr(out.get("r")), _addr(out.get("x")),
@@ -724,7 +728,7 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
             n = ctypes.c_size_t()
             _ok(lib.fipa_norm_residual_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)),
                 "fipa_norm_residual_backward_workspace_size")
-            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=dev)
+            workspace = s.new_empty(int(n.value), dtype=torch.uint8)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
         g = FipaNormGrads(*[None if grads.get(f) is None else grads[f].data_ptr() for f, _ in FipaNormGrads._fields_])
@@ -749,7 +753,7 @@ def embedding(idx: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: O
     V, C = table.shape
     with _OnDevice(dev):
         if out is None:
-            out = {"out": torch.empty((*idx.shape, C), dtype=table.dtype, device=dev)}
+            out = {"out": table.new_empty((*idx.shape, C))}
         else:
             _need("out", out["out"], (*idx.shape, C), (table.dtype,), dev)
         st = _raw_stream(stream, dev.index)
@@ -779,11 +783,11 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
     _need("idx", idx, d_out.shape[:-1], (torch.int32,), dev)
     with _OnDevice(dev):
         if grads is None:
-            grads = {"table": torch.empty((V, C), dtype=torch.float32, device=dev)}
+            grads = {"table": d_out.new_empty((V, C), dtype=torch.float32)}
         else:
             _need("table", grads["table"], (V, C), (torch.float32,), dev)
         if workspace is None:
-            workspace = torch.empty(embedding_backward_workspace_size(idx.numel(), V, C), dtype=torch.uint8, device=dev)
+            workspace = d_out.new_empty(embedding_backward_workspace_size(idx.numel(), V, C), dtype=torch.uint8)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
         st = _raw_stream(stream, dev.index)
