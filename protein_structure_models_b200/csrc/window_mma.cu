@@ -276,10 +276,7 @@ __device__ __forceinline__ void row_delta(float* sdelta, const bf16* dOs, const 
     }
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     x += __shfl_xor_sync(0xffffffffu, x, 2);
-    if ((threadIdx.x & 3) == 0) {
-      sdelta[r] = x;
-      if (f < f1) a.delta[((long long)b * a.H + h) * a.Nq + i] = x;
-    }
+    if ((threadIdx.x & 3) == 0) sdelta[r] = x;
   }
 }
 
@@ -317,11 +314,11 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
     cp_async_commit();
   };
   const int kd = (a.D + 15) / 16, kv = (a.Dv + 15) / 16;
-  float acc[DP / 8][4], lse2[2] = {INFINITY, INFINITY}, del[2] = {0.f, 0.f};
+  float acc[DP / 8][4], avg[DP / 8][4], lse2[2] = {INFINITY, INFINITY}, del[2] = {0.f, 0.f}, eps[2] = {0.f, 0.f};
 #pragma unroll
   for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[n][e] = avg[n][e] = 0.f;
   const float sc = a.scale * kLog2e;
   if (ntile > 0) {
     load_queries<DP, VEC>(Qs, Os, a, b, q0, q, g_, f0, f1);
@@ -339,9 +336,6 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
         lse2[i] = x == -INFINITY ? INFINITY : x * kLog2e;     // a row that sees nothing: every p is 0
       }
     }
-  } else if (threadIdx.x < T && f0 + (int)threadIdx.x < f1) {
-    const int f = f0 + threadIdx.x, i = f / a.G;
-    a.delta[((long long)b * a.H + hkv * a.G + (f - i * a.G)) * a.Nq + i] = 0.f;
   }
   for (int t = 0; t < ntile; ++t) {
     const int st = t & 1, u0 = t * T;
@@ -382,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[h][e] = ex2_approx(fmaf(s[h][e], sc, -lse2[e >> 1])) * (dp[h][e] - del[e >> 1]);
+        for (int e = 0; e < 4; ++e) s[h][e] = ex2_approx(fmaf(s[h][e], sc, -lse2[e >> 1]));
       if (wg != 0xffffu || !rc.all(u0 + 16 * g)) {
         const uint32_t on[2] = {wg & row[0].sees(u0 + 16 * g), wg & row[1].sees(u0 + 16 * g)};
 #pragma unroll
@@ -390,17 +384,33 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[h][e] = (on[e >> 1] >> (8 * h + col2 + (e & 1))) & 1u ? s[h][e] : 0.f;
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dp[h][e] = s[h][e] * (dp[h][e] - del[e >> 1]);
+          eps[e >> 1] += dp[h][e];
+        }
       const uint32_t pf[4] = {pack(s[0][0], s[0][1]), pack(s[0][2], s[0][3]), pack(s[1][0], s[1][1]), pack(s[1][2], s[1][3])};
+      const uint32_t df[4] = {pack(dp[0][0], dp[0][1]), pack(dp[0][2], dp[0][3]), pack(dp[1][0], dp[1][1]), pack(dp[1][2], dp[1][3])};
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
         if (n >= kd) break;
         uint32_t bf[4];
         ldsm4t(bf, bt_addr<DP>(ks, 16 * g, 16 * n, lane));
-        mma(acc[2 * n], pf, bf[0], bf[1]);
-        mma(acc[2 * n + 1], pf, bf[2], bf[3]);
+        mma(acc[2 * n], df, bf[0], bf[1]);
+        mma(acc[2 * n + 1], df, bf[2], bf[3]);
+        mma(avg[2 * n], pf, bf[0], bf[1]);
+        mma(avg[2 * n + 1], pf, bf[2], bf[3]);
       }
     }
     __syncthreads();
+  }
+  take_back<DP>(acc, avg, eps);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int f = f0 + 16 * warp + (lane >> 2) + 8 * i, qi = f / a.G;
+    if ((lane & 3) == 0 && f < f1) a.delta[((long long)b * a.H + hkv * a.G + (f - qi * a.G)) * a.Nq + qi] = del[i] + eps[i];
   }
   store_rows<DP>(acc, a.D, a.d_q, a.scale, lane, [&](int i, bool& keep) -> bf16* {
     const int f = f0 + 16 * warp + (lane >> 2) + 8 * i, qi = f / a.G;

@@ -184,6 +184,24 @@ __device__ __forceinline__ void key_rows(const WinArgs& a, int q0, int j, int fl
   hi = (int)(j < a.sinks ? n : (y < 0 ? 0 : (y < n ? y : n)));
 }
 
+// delta = dO.out comes from the rounded out and is off by eps = sum_j ds_j, which
+// is 0 for the right delta; sum_j ds_j k_j is then off by eps sum_j p_j k_j.  Under
+// windows of a few keys that error would be as large as all other roundings
+// together.  Adds up eps over the four lanes of a row and takes the error back.
+template <int DP>
+__device__ __forceinline__ void take_back(float (&acc)[DP / 8][4], const float (&avg)[DP / 8][4], float (&eps)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    eps[i] += __shfl_xor_sync(0xffffffffu, eps[i], 1);
+    eps[i] += __shfl_xor_sync(0xffffffffu, eps[i], 2);
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) {
+      acc[n][2 * i] = fmaf(-eps[i], avg[n][2 * i], acc[n][2 * i]);
+      acc[n][2 * i + 1] = fmaf(-eps[i], avg[n][2 * i + 1], acc[n][2 * i + 1]);
+    }
+  }
+}
+
 // Writes a warp's 16 x DP sums as bfloat16 rows; at(i) is the row of this thread's half i, null: not written.
 template <int DP, typename At>
 __device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], int width, const void* base, float f, int lane, At at) {

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
   for (int f0 = 16 * warp; f0 < s.F; f0 += 64) {
     const int f1 = min(s.F, f0 + 16);
     const Units un = units_of(a, win_cols(a, s.q0, f0, f1));
-    float lse2[2], del[2], acc[DP / 8][4];
+    float lse2[2], del[2], eps[2] = {0.f, 0.f}, acc[DP / 8][4], avg[DP / 8][4];
     int pos[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[n][e] = avg[n][e] = 0.f;
     uint32_t qf[DP / 16][4], gf[DP / 16][4];
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
@@ -320,26 +320,36 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float y = ex2_approx(fmaf(x[h][e], sc, -lse2[e >> 1])) * (dp[h][e] - del[e >> 1]);
+            const float y = ex2_approx(fmaf(x[h][e], sc, -lse2[e >> 1]));
             x[h][e] = ob[e >> 1] & (1u << (16 * g + 8 * h + (e & 1))) ? y : 0.f;
+            dp[h][e] = x[h][e] * (dp[h][e] - del[e >> 1]);
+            eps[e >> 1] += dp[h][e];
           }
         const uint32_t pf[4] = {pack(x[0][0], x[0][1]), pack(x[0][2], x[0][3]), pack(x[1][0], x[1][1]), pack(x[1][2], x[1][3])};
+        const uint32_t df[4] = {pack(dp[0][0], dp[0][1]), pack(dp[0][2], dp[0][3]), pack(dp[1][0], dp[1][1]), pack(dp[1][2], dp[1][3])};
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
           if (n >= kd) break;
           uint32_t bf[4];
           ldsm4t(bf, bt_addr<DP>(s.k, j0 + 16 * g, 16 * n, lane));
-          mma(acc[2 * n], pf, bf[0], bf[1]);
-          mma(acc[2 * n + 1], pf, bf[2], bf[3]);
+          mma(acc[2 * n], df, bf[0], bf[1]);
+          mma(acc[2 * n + 1], df, bf[2], bf[3]);
+          mma(avg[2 * n], pf, bf[0], bf[1]);
+          mma(avg[2 * n + 1], pf, bf[2], bf[3]);
         }
       }
     }
+    take_back<DP>(acc, avg, eps);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if ((lane & 3) == 0) sdel[f0 + (lane >> 2) + 8 * i] = del[i] + eps[i];
     store_rows<DP>(acc, a.D, a.d_q, a.scale, lane, [&](int i, bool& keep) -> bf16* {
       const int f = f0 + (lane >> 2) + 8 * i, qi = a.G == 1 ? f : f / a.G;
       keep = lse2[i] != INFINITY;
       return f < f1 ? static_cast<bf16*>(a.d_q) + (((long long)s.b * a.Nq + qi) * a.H + s.hkv * a.G + (f - qi * a.G)) * a.D : nullptr;
     });
   }
+  __syncthreads();                           // delta
   // ---- dk, dv
   for (int k0 = 16 * warp; k0 < a.Nk; k0 += 64) {
     const int k1 = min(a.Nk, k0 + 16) - 1;

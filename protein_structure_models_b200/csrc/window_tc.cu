@@ -42,14 +42,14 @@ struct Lay {
   static constexpr int tail = NA * A + NS * 2 * B;
   static constexpr int bars = tail, info = tail + 128;   // info: per stage 64 x {lse, delta, position} or two words of column bits
   static constexpr int smem = info + NS * (MODE == kKeySide ? 768 : 8) + 1024;
-  // Tensor memory.  Forward: S of even and odd tiles, P in place of S.  Row side:
-  // S, dP, dS of even and odd tiles.  Key side: S and dP, P and dS in their places.
+  // Tensor memory.  Forward: S of even and odd tiles, P in place of S.  Row side: S,
+  // dP, dS and what its rounding left.  Key side: S and dP, P and dS in their places.
   static constexpr int S = 0, dP = 64, acc0 = MODE == kRowSide ? 192 : 128, acc1 = acc0 + DP;
   static constexpr int need = MODE == kKeySide ? acc1 + DP : acc0 + DP;
   static constexpr int cols = need <= 256 ? 256 : 512;
   static constexpr int per_sm = DP == 64 || MODE == kFwd ? 2 : 1;
   static __device__ __forceinline__ int s_of(int t) { return MODE == kFwd ? S + 64 * (t & 1) : S; }
-  static __device__ __forceinline__ int p_of(int t) { return MODE == kRowSide ? 128 + 32 * (t & 1) : s_of(t); }
+  static __device__ __forceinline__ int p_of(int t) { return MODE == kRowSide ? 128 : s_of(t); }
 };
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
   const uint32_t tmem = *slot;
   const WaitCtx wc{abort_flag, a.status, a.timeout_ns};
   const float sc = a.scale * kLog2e;
-  float m = -INFINITY, l = 0.f, lse2 = INFINITY, del = 0.f;
+  float m = -INFINITY, l = 0.f, lse2 = INFINITY, del = 0.f, eps = 0.f;
 
   if (warp >= 5) {
     // ------------------------------------------------------------- copies
@@ -320,7 +320,10 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
         for (int kk = 0; kk < kCols / 16; ++kk) {
           const uint32_t acc = t > 0 || kk > 0, p = tmem + L::p_of(t) + 8 * kk;
           if (MODE != kRowSide) mma_ts(tmem + L::acc0, p, desc_mnmajor_sw128(b1 + kk * 2048, kCols * 128), idV, acc);
-          if (MODE == kRowSide) mma_ts(tmem + L::acc0, p, desc_mnmajor_sw128(b0 + kk * 2048, kCols * 128), idD, acc);
+          if (MODE == kRowSide) {
+            mma_ts(tmem + L::acc0, p, desc_mnmajor_sw128(b0 + kk * 2048, kCols * 128), idD, acc);
+            mma_ts(tmem + L::acc0, p + 32, desc_mnmajor_sw128(b0 + kk * 2048, kCols * 128), idD, 1u);
+          }
           if (MODE == kKeySide) mma_ts(tmem + L::acc1, tmem + L::dP + 8 * kk, desc_mnmajor_sw128(b0 + kk * 2048, kCols * 128), idD, acc);
         }
         tc_commit(&empty[st]);
@@ -363,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
         const float z = a.lse[o];
         lse2 = z == -INFINITY ? INFINITY : z * kLog2e;
       }
-      a.delta[o] = del;
     }
     for (int t = 0; t < ntile; ++t) {
       const int st = t % NS, u0 = t * kCols;
@@ -428,12 +430,10 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       } else if (MODE == kRowSide) {
         const uint32_t w[2] = {reinterpret_cast<const uint32_t*>(inf)[0], reinterpret_cast<const uint32_t*>(inf)[1]};
         const bool edge = (w[0] & w[1]) != 0xffffffffu || !rc.all(u0, kCols);
-        // dS of the tile before the last has been used
-        if (t > 1 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[t & 1], ((t >> 1) - 1) & 1, wc, 89))) break;
-        tc_fence_after();
+        bool free = t == 0;                                 // the last tile's dS has been used
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t s[32], d[32], p[16];
+          uint32_t s[32], d[32], p[16], o[16];
           tmem_ld32(trow + L::S + 32 * h, s);
           tmem_ld32(trow + L::dP + 32 * h, d);
           tmem_ld_wait();
@@ -445,10 +445,23 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[e] = (on >> e) & 1u ? s[e] : 0u;
           }
+          // dS as two bfloat16 numbers: with one, its rounding would weigh as much as that of d_q itself
 #pragma unroll
-          for (int e = 0; e < 16; ++e) p[e] = pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+          for (int e = 0; e < 16; ++e) {
+            const float x = __uint_as_float(s[2 * e]), y = __uint_as_float(s[2 * e + 1]);
+            eps += x + y;
+            p[e] = pack(x, y);
+            o[e] = pack(x - __uint_as_float(p[e] << 16), y - __uint_as_float(p[e] & 0xffff0000u));
+          }
+          if (!free) {
+            free = __all_sync(0xffffffffu, mbar_wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 89));
+            if (!free) break;
+            tc_fence_after();
+          }
           tmem_st16(trow + L::p_of(t) + 16 * h, p);
+          tmem_st16(trow + L::p_of(t) + 32 + 16 * h, o);
         }
+        if (!free) break;
       } else {
         const float* sl = reinterpret_cast<const float*>(inf);
         const int* sp = reinterpret_cast<const int*>(inf) + 128;
@@ -497,6 +510,8 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
         write_row(trow, L::acc0, a.Dv, some ? 1.f / l : 0.f, done, done && some, in ? static_cast<bf16*>(a.out) + o * a.Dv : nullptr);
         if (a.lse != nullptr && in) a.lse[((long long)b * a.H + h) * a.Nq + i] = some ? fmaf(m, a.scale, logf(l)) : -INFINITY;
       } else {
+        // delta from the rounded out is off by the sum of dS, which is 0 for the right one: for the key side
+        if (in) a.delta[((long long)b * a.H + h) * a.Nq + i] = del + eps;
         write_row(trow, L::acc0, a.D, a.scale, done, done && alive && lse2 != INFINITY, in ? static_cast<bf16*>(a.d_q) + o * a.D : nullptr);
       }
     } else if (split && first < a.sinks) {
