@@ -187,8 +187,8 @@ class _OnDevice:
     """torch.cuda.device(dev), at no cost when dev is current already."""
     __slots__ = ("guard",)
 
-    def __init__(self, dev):
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    def __init__(self, index):
+        self.guard = None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
     def __enter__(self):
         if self.guard is not None:
@@ -412,28 +412,29 @@ class Fipa:
 
     def _window_problem(self, q, k, v, window, sinks, mask, q_start, scale):
         """Checks the tensors of a window attention call; returns its sizes and head views."""
-        dev, td = q.device, self.torch_dtype
-        if dev.type != "cuda" or dev.index != self.device:
-            raise ValueError(f"q: need a tensor on cuda:{self.device}")
-        heads, shapes = [], []
-        for name, t in (("q", q), ("k", k), ("v", v)):
-            sh, st = t.shape, t.stride()
-            if len(sh) != 4 or t.dtype != td or t.device != dev or (st[3] != 1 and sh[3] > 1):
-                raise ValueError(f"{name}: need a {td} tensor [B, N, heads, width] on {dev}, its width contiguous")
+        at, td = self.device, self.torch_dtype
+        B, Nq, H, D = q.shape if q.dim() == 4 else (-1,) * 4
+        Bk, Nk, Hkv, Dk = k.shape if k.dim() == 4 else (-1,) * 4
+        Bv, Nv, Hv, Dv = v.shape if v.dim() == 4 else (-1,) * 4
+        heads = []
+        for t, width in ((q, D), (k, Dk), (v, Dv)):
+            if width < 0 or t.dtype != td or t.get_device() != at or not t.is_cuda:
+                raise ValueError(f"q, k, v: need {td} tensors [B, N, heads, width] on cuda:{at}")
+            st = t.stride()
+            if st[3] != 1 and width > 1:
+                raise ValueError("q, k, v: need a contiguous width")
             heads.append(FipaHeads(t.data_ptr(), st[0], st[1], st[2]))
-            shapes.append(sh)
-        B, Nq, H, D = shapes[0]
-        Bv, Nk, Hkv, Dv = shapes[2]
-        if shapes[1] != (B, Nk, Hkv, D) or Bv != B:
+        if Bk != B or Bv != B or Nv != Nk or Hv != Hkv or Dk != D:
             raise ValueError("q [B,Nq,H,D], k [B,Nk,Hkv,D], v [B,Nk,Hkv,Dv] do not fit together")
-        if mask is not None and (mask.dtype not in _BYTES or mask.device != dev
+        if mask is not None and (mask.dtype not in _BYTES or mask.get_device() != at
                                  or mask.shape != (B, Nk) or not mask.is_contiguous()):
-            raise ValueError(f"mask: need a contiguous bool/uint8 tensor [B, Nk] on {dev}")
-        if q_start is not None and (q_start.dtype != torch.int32 or q_start.device != dev
+            raise ValueError(f"mask: need a contiguous bool/uint8 tensor [B, Nk] on cuda:{at}")
+        if q_start is not None and (q_start.dtype != torch.int32 or q_start.get_device() != at
                                     or q_start.shape != (B,) or not q_start.is_contiguous()):
-            raise ValueError(f"q_start: need a contiguous int32 tensor [B] on {dev}")
-        left, right = (-1 if w is None else min(int(w), 0x7fffffff) for w in window)
-        return FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, left, right, int(sinks),
+            raise ValueError(f"q_start: need a contiguous int32 tensor [B] on cuda:{at}")
+        left, right = window
+        return FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, -1 if left is None else min(int(left), 0x7fffffff),
+                          -1 if right is None else min(int(right), 0x7fffffff), sinks,
                           D ** -0.5 if scale is None and D > 0 else float(scale or 0.0)), heads
 
     def window_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: tuple, sinks: int = 0,
@@ -448,16 +449,21 @@ class Fipa:
         window = (left, 0) and its position in q_start.  Returns {"out": [B,Nq,H,Dv]}
         (+ "lse" [B,H,Nq] float32, which the backward needs)."""
         w, hd = self._window_problem(q, k, v, window, sinks, mask, q_start, scale)
+        B, Nq, H = w.B, w.Nq, w.H
+        lse = None
         if out is None:
-            out = {"out": q.new_empty((w.B, w.Nq, w.H, w.Dv))}
+            o = q.new_empty((B, Nq, H, w.Dv))
+            out = {"out": o}
             if want_lse:
-                out["lse"] = q.new_empty((w.B, w.H, w.Nq), dtype=torch.float32)
+                out["lse"] = lse = q.new_empty((B, H, Nq), dtype=torch.float32)
         else:
-            self._check_buffers(out, {"out": ((w.B, w.Nq, w.H, w.Dv), q.dtype),
-                                      "lse": ((w.B, w.H, w.Nq), torch.float32)}, q.device, ("out",))
-        self._check(self.lib.fipa_window_attention(self.handle, hd[0], hd[1], hd[2], _addr(mask), _addr(q_start), w,
-                                                   out["out"].data_ptr(), _addr(out.get("lse")),
-                                                   _raw_stream(stream, self.device)))
+            self._check_buffers(out, {"out": ((B, Nq, H, w.Dv), q.dtype), "lse": ((B, H, Nq), torch.float32)}, q.device,
+                                ("out",))
+            o, lse = out["out"], out.get("lse")
+        st = self.lib.fipa_window_attention(self.handle, hd[0], hd[1], hd[2], _addr(mask), _addr(q_start), w,
+                                            o.data_ptr(), _addr(lse), _raw_stream(stream, self.device))
+        if st != FIPA_OK:
+            self._check(st)
         return out
 
     @staticmethod
@@ -672,7 +678,7 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
     lib = load_library()
     d, i, tb, _ = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
     dev = s.device
-    with _OnDevice(dev):
+    with _OnDevice(dev.index):
         if out is None:
             out = {}
             if u is not None:
@@ -715,7 +721,7 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
     if d_x is not None:
         _need("d_x", d_x, s.shape, (tb,), dev)
     have = {"s": s, "u": u, "gate": gate, **par}
-    with _OnDevice(dev):
+    with _OnDevice(dev.index):
         if grads is None:
             grads = {k: None if t is None else torch.empty_like(t) for k, t in have.items()}
         else:
@@ -744,21 +750,23 @@ def embedding(idx: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: O
               stream: Optional[torch.cuda.Stream] = None) -> dict:
     """fipa_embedding: {"out": scale * table[idx]} for idx [...] int32 and table [V, C]
     float32/bfloat16; an index outside [0, V) gives a zero row."""
-    lib = load_library()
-    dev = table.device
-    if dev.type != "cuda" or table.dim() != 2:
-        raise ValueError("table: need a CUDA tensor [V, C]")
-    _need("table", table, table.shape, _FLOATS, dev)
-    _need("idx", idx, idx.shape, (torch.int32,), dev)
+    lib, at, td = _lib or load_library(), table.get_device(), table.dtype
+    if not table.is_cuda or table.dim() != 2 or td not in _FLOATS or not table.is_contiguous():
+        raise ValueError("table: need a contiguous float32 or bfloat16 CUDA tensor [V, C]")
+    if idx.dtype != torch.int32 or idx.get_device() != at or not idx.is_contiguous():
+        raise ValueError(f"idx: need a contiguous int32 tensor on cuda:{at}")
     V, C = table.shape
-    with _OnDevice(dev):
+    with _OnDevice(at):
         if out is None:
-            out = {"out": table.new_empty((*idx.shape, C))}
+            o = table.new_empty((*idx.shape, C))
+            out = {"out": o}
         else:
-            _need("out", out["out"], (*idx.shape, C), (table.dtype,), dev)
-        st = _raw_stream(stream, dev.index)
-        _ok(lib.fipa_embedding(_code(table), _addr(idx), _addr(table), idx.numel(), V, C, float(scale), _addr(out["out"]),
-                               st), "fipa_embedding")
+            o = out["out"]
+            _need("out", o, (*idx.shape, C), (td,), table.device)
+        st = lib.fipa_embedding(F32 if td == torch.float32 else BF16, idx.data_ptr(), table.data_ptr(), idx.numel(), V, C,
+                                scale, o.data_ptr(), _raw_stream(stream, at))
+    if st != FIPA_OK:
+        _ok(st, "fipa_embedding")
     return out
 
 
@@ -781,7 +789,7 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
     C = d_out.shape[-1]
     _need("d_out", d_out, d_out.shape, _FLOATS, dev)
     _need("idx", idx, d_out.shape[:-1], (torch.int32,), dev)
-    with _OnDevice(dev):
+    with _OnDevice(dev.index):
         if grads is None:
             grads = {"table": d_out.new_empty((V, C), dtype=torch.float32)}
         else:
