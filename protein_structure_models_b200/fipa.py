@@ -57,8 +57,11 @@ class FipaNormInputs(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in ("s", "u", "gate", "mask") + NORM_PARAMS]
 
 
+NORM_GRADS = ("s", "u", "gate") + NORM_PARAMS
+
+
 class FipaNormGrads(ctypes.Structure):
-    _fields_ = [(f, ctypes.c_void_p) for f in ("s", "u", "gate") + NORM_PARAMS]
+    _fields_ = [(f, ctypes.c_void_p) for f in NORM_GRADS]
 
 
 class FipaError(RuntimeError):
@@ -484,25 +487,29 @@ class Fipa:
         """fipa_window_attention_backward: gradients "q", "k", "v" (handle's dtype) of
         <d_out, out>, from the forward's out and lse."""
         w, hd = self._window_problem(q, k, v, window, sinks, mask, q_start, scale)
-        dev, td = q.device, q.dtype
-        o = ((w.B, w.Nq, w.H, w.Dv), td)
-        self._check_buffers({"out": out, "lse": lse, "d_out": d_out},
-                            {"out": o, "lse": ((w.B, w.H, w.Nq), torch.float32), "d_out": o}, dev,
-                            ("out", "lse", "d_out"))
-        shapes = {"q": ((w.B, w.Nq, w.H, w.D), td), "k": ((w.B, w.Nk, w.Hkv, w.D), td),
-                  "v": ((w.B, w.Nk, w.Hkv, w.Dv), td)}
+        dev, at, td = q.device, self.device, q.dtype
+        B, Nq, H = w.B, w.Nq, w.H
+        o = (B, Nq, H, w.Dv)
+        for t, shape, dt in ((out, o, td), (d_out, o, td), (lse, (B, H, Nq), torch.float32)):
+            if t.shape != shape or t.dtype != dt or t.get_device() != at or not t.is_contiguous():
+                raise ValueError(f"out, d_out, lse: need contiguous tensors {o} and {(B, H, Nq)} (float32) on {dev}")
         if grads is None:
-            grads = {key: q.new_empty(s) for key, (s, _) in shapes.items()}
+            dq, dk, dv = q.new_empty((B, Nq, H, w.D)), k.new_empty((B, w.Nk, w.Hkv, w.D)), v.new_empty((B, w.Nk, w.Hkv, w.Dv))
+            grads = {"q": dq, "k": dk, "v": dv}
         else:
-            self._check_buffers(grads, shapes, dev, ("q", "k", "v"))
+            self._check_buffers(grads, {"q": ((B, Nq, H, w.D), td), "k": ((B, w.Nk, w.Hkv, w.D), td),
+                                        "v": ((B, w.Nk, w.Hkv, w.Dv), td)}, dev, ("q", "k", "v"))
+            dq, dk, dv = grads["q"], grads["k"], grads["v"]
         if workspace is None:
             workspace = q.new_empty(self._window_workspace(w), dtype=torch.uint8)
-        elif workspace.device != dev or not workspace.is_contiguous():
+        elif workspace.get_device() != at or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        self._check(self.lib.fipa_window_attention_backward(
+        st = self.lib.fipa_window_attention_backward(
             self.handle, hd[0], hd[1], hd[2], _addr(mask), _addr(q_start), w, out.data_ptr(), lse.data_ptr(),
-            d_out.data_ptr(), grads["q"].data_ptr(), grads["k"].data_ptr(), grads["v"].data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _raw_stream(stream, self.device)))
+            d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _raw_stream(stream, at))
+        if st != FIPA_OK:
+            self._check(st)
         return grads
 
     def _window_workspace(self, w) -> int:
@@ -621,12 +628,6 @@ def _need(name, t, shape, dtypes, dev):
         raise ValueError(f"{name}: need a contiguous tensor {tuple(shape)} of {dtypes} on {dev}")
 
 
-
-
-def _code(t: torch.Tensor) -> int:
-    return F32 if t.dtype == torch.float32 else BF16
-
-
 def _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype):
     """Checks the inputs of the junction; returns its dims, inputs, branch type and parameters."""
     dev, shape, ts = s.device, s.shape, s.dtype
@@ -636,23 +637,23 @@ def _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtyp
     tb = u.dtype if u is not None else (branch_dtype or ts)
     if ts not in _FLOATS or tb not in _FLOATS:
         raise ValueError("s, u, branch_dtype: float32 or bfloat16")
-    at = s.get_device()
-    for name, t, dt in (("s", s, ts), ("u", u, tb), ("gate", gate, tb)):
-        if t is not None and (t.dtype != dt or t.shape != shape or not t.is_contiguous() or t.get_device() != at):
-            raise ValueError(f"{name}: need a contiguous {dt} tensor {tuple(shape)} on {dev}")
+    at, f32 = s.get_device(), torch.float32
+    if not s.is_contiguous() or (u is not None and (u.shape != shape or not u.is_contiguous() or u.get_device() != at)) or (
+            gate is not None and (gate.dtype != tb or gate.shape != shape or not gate.is_contiguous()
+                                  or gate.get_device() != at)):
+        raise ValueError(f"s, u, gate: need contiguous tensors {tuple(shape)} on {dev}, gate of the branch's type {tb}")
     if mask is not None:
         _need("mask", mask, shape[:-1], _BYTES, dev)
     post_w, post_b = post or (None, None)
     pre_w, pre_b = pre or (None, None)
-    par = {"res_scale": res_scale, "post_w": post_w, "post_b": post_b, "pre_w": pre_w, "pre_b": pre_b}
-    for name, t in par.items():
-        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.numel() != C or not t.is_contiguous()
-                              or t.get_device() != at):
-            raise ValueError(f"{name}: need a contiguous float32 tensor ({C},) on {dev}")
-    if norm not in ("layer", "rms"):
+    par, line = (res_scale, post_w, post_b, pre_w, pre_b), shape[-1:]
+    for t in par:
+        if t is not None and (t.dtype != f32 or t.shape != line or not t.is_contiguous() or t.get_device() != at):
+            raise ValueError(f"{', '.join(NORM_PARAMS)}: need contiguous float32 tensors ({C},) on {dev}")
+    if norm != "layer" and norm != "rms":
         raise ValueError('norm: "layer" or "rms"')
-    d = FipaNormDims(s.numel() // C if C else 0, C, F32 if ts == torch.float32 else BF16,
-                     F32 if tb == torch.float32 else BF16, 0 if norm == "layer" else 1, eps)
+    d = FipaNormDims(s.numel() // C if C else 0, C, F32 if ts == f32 else BF16, F32 if tb == f32 else BF16,
+                     0 if norm == "layer" else 1, eps)
     i = FipaNormInputs(s.data_ptr(), _addr(u), _addr(gate), _addr(mask), _addr(res_scale), _addr(post_w), _addr(post_b),
                        _addr(pre_w), _addr(pre_b))
     return d, i, tb, par
@@ -675,29 +676,29 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
     parameters [C] float32, mask [...] bool/uint8 (0: padding, r = s and x = 0).
     Returns {"r" (with u), "x" (with pre)} and, with want_stats, "stats" [rows, 4] for the
     backward.  Without u, x = Norm(s, pre) in branch_dtype (default: that of s)."""
-    lib = load_library()
+    lib = _lib or load_library()
     d, i, tb, _ = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
-    dev = s.device
-    with _OnDevice(dev.index):
+    at = s.get_device()
+    r = x = stats = None
+    with _OnDevice(at):
         if out is None:
             out = {}
             if u is not None:
-                out["r"] = torch.empty_like(s)
+                out["r"] = r = torch.empty_like(s)
             if pre is not None:
-                out["x"] = torch.empty_like(s, dtype=tb) if u is None else torch.empty_like(u)
+                out["x"] = x = torch.empty_like(s, dtype=tb) if u is None else torch.empty_like(u)
             if want_stats:
-                out["stats"] = s.new_empty((d.rows, 4), dtype=torch.float32)
+                out["stats"] = stats = s.new_empty((d.rows, 4), dtype=torch.float32)
         else:
             want = {"stats": ((d.rows, 4), torch.float32, False), "r": (s.shape, s.dtype, u is not None),
                     "x": (s.shape, tb, pre is not None)}
             for k, (sh, dt, needed) in want.items():
                 if k in out:
-                    _need(k, out[k], sh, (dt,), dev)
+                    _need(k, out[k], sh, (dt,), s.device)
                 elif needed:
                     raise ValueError(f"{k}: buffer missing")
-        st = _raw_stream(stream, dev.index)
-        _ok(lib.fipa_norm_residual(d, i, _addr(out.get("r")), _addr(out.get("x")),
-                                   _addr(out.get("stats")), st), "fipa_norm_residual")
+            r, x, stats = out.get("r"), out.get("x"), out.get("stats")
+        _ok(lib.fipa_norm_residual(d, i, _addr(r), _addr(x), _addr(stats), _raw_stream(stream, at)), "fipa_norm_residual")
     return out
 
 
@@ -712,19 +713,23 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
     every input that was given, keyed "s", "u", "gate", "res_scale", "post_w", "post_b",
     "pre_w", "pre_b" (None where there was no input).  `grads`, if given, holds the buffers
     of the gradients that are wanted."""
-    lib = load_library()
+    lib = _lib or load_library()
     d, i, tb, par = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
-    dev = s.device
+    dev, at = s.device, s.get_device()
     _need("stats", stats, (d.rows, 4), (torch.float32,), dev)
     if d_r is not None:
         _need("d_r", d_r, s.shape, (s.dtype,), dev)
     if d_x is not None:
         _need("d_x", d_x, s.shape, (tb,), dev)
-    have = {"s": s, "u": u, "gate": gate, **par}
-    with _OnDevice(dev.index):
+    with _OnDevice(at):
         if grads is None:
-            grads = {k: None if t is None else torch.empty_like(t) for k, t in have.items()}
+            grads = {"s": torch.empty_like(s), "u": None if u is None else torch.empty_like(u),
+                     "gate": None if gate is None else torch.empty_like(gate)}
+            lines = s.new_empty((5, d.C), dtype=torch.float32).unbind(0)       # the parameters' gradients side by side
+            for k, t, line in zip(NORM_PARAMS, par, lines):
+                grads[k] = None if t is None else line
         else:
+            have = {"s": s, "u": u, "gate": gate, **dict(zip(NORM_PARAMS, par))}
             for k, t in grads.items():
                 if t is not None:
                     if have.get(k) is None:
@@ -732,16 +737,13 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
                     _need(k, t, have[k].shape, (have[k].dtype,), dev)
         if workspace is None:
             n = ctypes.c_size_t()
-            _ok(lib.fipa_norm_residual_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)),
-                "fipa_norm_residual_backward_workspace_size")
-            workspace = s.new_empty(int(n.value), dtype=torch.uint8)
+            _ok(lib.fipa_norm_residual_backward_workspace_size(d, n), "fipa_norm_residual_backward_workspace_size")
+            workspace = s.new_empty(n.value, dtype=torch.uint8)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        g = FipaNormGrads(*[None if grads.get(f) is None else grads[f].data_ptr() for f, _ in FipaNormGrads._fields_])
-        st = _raw_stream(stream, dev.index)
-        _ok(lib.fipa_norm_residual_backward(
-            d, i, _addr(stats), _addr(d_r), _addr(d_x), g, _addr(workspace),
-            workspace.numel() * workspace.element_size(), st),
+        g = FipaNormGrads(*[_addr(grads.get(f)) for f in NORM_GRADS])
+        _ok(lib.fipa_norm_residual_backward(d, i, stats.data_ptr(), _addr(d_r), _addr(d_x), g, workspace.data_ptr(),
+                                            workspace.numel() * workspace.element_size(), _raw_stream(stream, at)),
             "fipa_norm_residual_backward")
     return grads
 
@@ -782,27 +784,30 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
                        workspace: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
                        stream: Optional[torch.cuda.Stream] = None) -> dict:
     """fipa_embedding_backward: {"table": [V, C] float32}, the gradient of <d_out, out>."""
-    lib = load_library()
-    dev = d_out.device
-    if dev.type != "cuda" or d_out.dim() < 1:
-        raise ValueError("d_out: need a CUDA tensor [..., C]")
-    C = d_out.shape[-1]
-    _need("d_out", d_out, d_out.shape, _FLOATS, dev)
-    _need("idx", idx, d_out.shape[:-1], (torch.int32,), dev)
-    with _OnDevice(dev.index):
+    lib, at, td = _lib or load_library(), d_out.get_device(), d_out.dtype
+    if not d_out.is_cuda or not d_out.dim() or td not in _FLOATS or not d_out.is_contiguous():
+        raise ValueError("d_out: need a contiguous float32 or bfloat16 CUDA tensor [..., C]")
+    if idx.dtype != torch.int32 or idx.get_device() != at or not idx.is_contiguous() or idx.shape != d_out.shape[:-1]:
+        raise ValueError(f"idx: need a contiguous int32 tensor {tuple(d_out.shape[:-1])} on cuda:{at}")
+    C, T = d_out.shape[-1], idx.numel()
+    with _OnDevice(at):
         if grads is None:
-            grads = {"table": d_out.new_empty((V, C), dtype=torch.float32)}
+            g = d_out.new_empty((V, C), dtype=torch.float32)
+            grads = {"table": g}
         else:
-            _need("table", grads["table"], (V, C), (torch.float32,), dev)
+            g = grads["table"]
+            _need("table", g, (V, C), (torch.float32,), d_out.device)
         if workspace is None:
-            workspace = d_out.new_empty(embedding_backward_workspace_size(idx.numel(), V, C), dtype=torch.uint8)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        st = _raw_stream(stream, dev.index)
-        _ok(lib.fipa_embedding_backward(
-            _code(d_out), _addr(idx), _addr(d_out), idx.numel(), V, C, float(scale), _addr(grads["table"]), _addr(workspace),
-            workspace.numel() * workspace.element_size(), st),
-            "fipa_embedding_backward")
+            n = ctypes.c_size_t()
+            _ok(lib.fipa_embedding_backward_workspace_size(T, V, C, n), "fipa_embedding_backward_workspace_size")
+            workspace = d_out.new_empty(n.value, dtype=torch.uint8)
+        elif workspace.get_device() != at or not workspace.is_contiguous():
+            raise ValueError(f"workspace: need a contiguous tensor on cuda:{at}")
+        st = lib.fipa_embedding_backward(F32 if td == torch.float32 else BF16, idx.data_ptr(), d_out.data_ptr(), T, V, C,
+                                         scale, g.data_ptr(), workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _raw_stream(stream, at))
+    if st != FIPA_OK:
+        _ok(st, "fipa_embedding_backward")
     return grads
 
 
