@@ -845,7 +845,7 @@ fipa_status window_inputs(fipa_handle* h, const fipa_heads* q, const fipa_heads*
 // Workspace of the backward: delta [B,H,Nq], then the sinks' partial sums, for
 // the key tile of whichever kernels take the call.
 size_t window_bwd_bytes(const fipa::WinArgs& a) {
-  const size_t x = fipa::win_sink_plan(a, fipa::kWinSimtTile).part_floats, y = fipa::win_sink_plan(a, fipa::kWinTcRows).part_floats;
+  const size_t x = fipa::win_sink_plan(a, fipa::kWinTile).part_floats, y = fipa::win_sink_plan(a, fipa::kWinTcRows).part_floats;
   const size_t delta = ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256;
   return delta + (x > y ? x : y) * sizeof(float);
 }
@@ -868,7 +868,7 @@ FIPA_API fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, 
   a.lse = lse;
   DeviceGuard g(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_fwd_simt(a, s) : fipa::launch_win_fwd(a, s);
+  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_f32(a, false, s) : fipa::launch_win_fwd(a, s);
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention launch", e);
 }
 
@@ -916,6 +916,6 @@ FIPA_API fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_h
                                     ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256);
   DeviceGuard g(h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_bwd_simt(a, s) : fipa::launch_win_bwd(a, s);
+  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_f32(a, true, s) : fipa::launch_win_bwd(a, s);
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention backward launch", e);
 }

@@ -130,8 +130,7 @@ __device__ __forceinline__ bool win_alive(const WinArgs& a, int b, int p) {
 }
 #endif
 
-cudaError_t launch_win_fwd_simt(const WinArgs& a, cudaStream_t s);       // float32 tensors
-cudaError_t launch_win_bwd_simt(const WinArgs& a, cudaStream_t s);
+cudaError_t launch_win_f32(const WinArgs& a, bool backward, cudaStream_t s);     // float32 tensors
 cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s);            // bfloat16 tensors: one of the following
 cudaError_t launch_win_bwd(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_step(const WinArgs& a, cudaStream_t s);           // few rows
@@ -141,6 +140,6 @@ cudaError_t launch_win_bwd_q_tc(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_bwd_k_tc(const WinArgs& a, cudaStream_t s);
 cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s);
 
-constexpr int kWinSimtTile = 64;       // rows and keys of a tile
+constexpr int kWinTile = 64;           // rows and keys of a tile of the warp-level kernels
 
 }  // namespace fipa

@@ -2,7 +2,15 @@
 // backward, with warp-level matrix instructions (m16n8k16, float32 sums).
 //
 // The mathematics, the row and column numbering and the visibility rule are
-// those of window_simt.cu and window.h.  A warp owns 16 rows (forward, dq) or
+// those of window.h:
+//   forward   m the running row maximum, l the running sum of exp(s - m), O that of
+//             exp(s - m) v, both scaled by exp(m_old - m_new) when m grows;
+//             out = O / l, lse = m + ln l
+//   backward  p = exp(s - lse), ds = p (dO.v - delta) with delta = dO.out;
+//             dq = scale sum ds k (row side), dv = sum p dO, dk = scale sum ds q (key
+//             side).  Each side recomputes p, so that every sum has one owner and a
+//             fixed order.
+//  A warp owns 16 rows (forward, dq) or
 // 16 keys (dk, dv) and keeps its scores, probabilities and sums in registers:
 // the accumulator layout of one product is the operand layout of the next, so
 // nothing of the softmax touches shared memory.  Because a warp covers only 16
@@ -23,7 +31,7 @@
 namespace fipa {
 namespace {
 
-constexpr int T = kWinSimtTile;            // rows and columns of a tile
+constexpr int T = kWinTile;            // rows and columns of a tile
 constexpr int kThreads = 128;              // 4 warps x 16 rows
 template <int DP>
 constexpr int kElems = T * Tile<DP>::ld;
@@ -624,6 +632,30 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
   store_rows<DP>(dv, a.Dv, a.d_v, 1.f, lane, [&](int i, bool& keep) { return at(a.d_v, a.Dv, i, keep); });
 }
 
+__device__ __forceinline__ void stf(float* p, float x) { *p = x; }
+__device__ __forceinline__ void stf(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
+// dk, dv of the sinks: the partial sums in chunk order, in 32 neighbouring stretches that are added in order.
+template <typename E>
+__global__ void __launch_bounds__(1024) win_sink_reduce_kernel(const WinArgs a) {
+  __shared__ float red[32][32];
+  const int w = a.D + a.Dv, bh = blockIdx.x / a.sinks, j = blockIdx.x - bh * a.sinks, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, d = blockIdx.y * 32 + lane, per = (a.nchunk + 32) / 32;
+  float x = 0.f;
+  if (d < w) {
+    const float* p = a.part + ((long long)bh * (a.nchunk + 1) * a.sinks + j) * w + d;
+    const int hi = min((part + 1) * per, a.nchunk + 1);
+#pragma unroll 8
+    for (int ch = part * per; ch < hi; ++ch) x += p[(long long)ch * a.sinks * w];
+  }
+  red[part][lane] = x;
+  __syncthreads();
+  if (part != 0 || d >= w) return;
+  for (int k = 1; k < 32; ++k) x += red[k][lane];
+  const long long r = ((long long)b * a.Nk + j) * a.Hkv + hkv;
+  if (d < a.D) stf(static_cast<E*>(a.d_k) + r * a.D + d, x * a.scale);
+  else stf(static_cast<E*>(a.d_v) + r * a.Dv + (d - a.D), x);
+}
+
 template <int DP, bool VEC>
 cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
   const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
@@ -694,6 +726,12 @@ bool use_short(const WinArgs& a, bool backward) {
 
 }  // namespace
 
+cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s) {
+  const dim3 grid((unsigned)((long long)a.B * a.Hkv * a.sinks), (unsigned)((a.D + a.Dv + 31) / 32));
+  if (f32) win_sink_reduce_kernel<float><<<grid, 1024, 0, s>>>(a);
+  else win_sink_reduce_kernel<bf16><<<grid, 1024, 0, s>>>(a);
+  return cudaGetLastError();
+}
 cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s) {
   if ((long long)a.Nq * a.G <= kWinStepRows) return launch_win_step(a, s);
   if (use_short(a, false)) return launch_win_short(a, false, s);

@@ -2,7 +2,7 @@
 // backward, on the fifth-generation tensor cores (tcgen05, tensor memory).
 //
 // The mathematics, the row and column numbering and the visibility rule are
-// those of window.h and window_simt.cu.  Three kernels of one shape: a CTA keeps
+// those of window.h and window_mma.cu.  Three kernels of one shape: a CTA keeps
 // 128 rows of one side in shared memory and streams the other side past them,
 // 64 columns a tile; every accumulator has the CTA's 128 rows as tensor-memory
 // lanes, so that one thread finishes one row of the scores:
