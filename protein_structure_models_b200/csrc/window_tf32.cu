@@ -23,7 +23,7 @@ namespace fipa {
 namespace {
 
 constexpr int T = kWinTile;                // rows and columns of a tile
-constexpr int kThreads = 128;              // 4 warps x 16 rows
+constexpr int kThreads = 256;              // 4 x 16 rows, by two warps each: one takes the even groups of columns, one the odd
 
 template <int DP>
 struct Ft {
@@ -46,11 +46,22 @@ __device__ __forceinline__ void mma1(float (&c)[4], const uint32_t (&a)[4], cons
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-__device__ __forceinline__ void mma3(float (&c)[4], const A4& a, const B2& b) {
-  mma1(c, a.lo, b.hi);
-  mma1(c, a.hi, b.lo);
-  mma1(c, a.hi, b.hi);
-}
+// Three sums side by side: one after the other they would wait for each other.
+struct C3 {
+  float x[3][4];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[k][e] = 0.f;
+  }
+  __device__ __forceinline__ void add(const A4& a, const B2& b) {
+    mma1(x[0], a.lo, b.hi);
+    mma1(x[1], a.hi, b.lo);
+    mma1(x[2], a.hi, b.hi);
+  }
+  __device__ __forceinline__ float sum(int e) const { return (x[0][e] + x[1][e]) + x[2][e]; }
+};
 // 16 rows from r0, depth k0 .. k0+7 of a tile; 16 columns from n0 (two operands of 8).
 template <int DP>
 __device__ __forceinline__ void load_a(A4& a, uint32_t base, int r0, int k0, int lane) {
@@ -87,24 +98,24 @@ __device__ __forceinline__ void add_product(float (&sum)[DP / 8][4], const A4 (&
 #pragma unroll
   for (int n = 0; n < DP / 8; ++n) {
     if (8 * n >= width) break;
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    C3 c;
+    c.zero();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       B2 b;
       load_bt<DP>(b, tile, k0 + 8 * k, 8 * n, lane);
-      mma3(c, a[k], b);
+      c.add(a[k], b);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[n][e] += c[e];
+    for (int e = 0; e < 4; ++e) sum[n][e] += c.sum(e);
   }
 }
 // s (16 x 16) = rows r0 .. of tile A times rows n0 .. of tile B
 template <int DP>
 __device__ __forceinline__ void scores(float (&s)[2][4], uint32_t A, int r0, uint32_t B, int n0, int width, int lane) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[h][e] = 0.f;
+  C3 c[2];
+  c[0].zero();
+  c[1].zero();
 #pragma unroll
   for (int k = 0; k < DP / 8; ++k) {
     if (8 * k >= width) break;
@@ -112,9 +123,13 @@ __device__ __forceinline__ void scores(float (&s)[2][4], uint32_t A, int r0, uin
     B2 b[2];
     load_a<DP>(a, A, r0, 8 * k, lane);
     load_b<DP>(b, B, n0, 8 * k, lane);
-    mma3(s[0], a, b[0]);
-    mma3(s[1], a, b[1]);
+    c[0].add(a, b[0]);
+    c[1].add(a, b[1]);
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[h][e] = c[h].sum(e);
 }
 
 struct Fsrc {
@@ -176,7 +191,8 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
   float* Ks = Qs + (BWD ? 2 : 1) * EL;                     // two stages each
   float* Vs = Ks + 2 * EL;
   __shared__ uint32_t bits[2][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
+  __shared__ float2 odd[T];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7, col2 = (lane & 3) * 2;
   const int F = a.Nq * a.G, tiles = (F + T - 1) / T;
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
   const int f0 = tile * T, f1 = min(F, f0 + T), q0 = win_q0(a, b);
@@ -202,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
       }
       del[i] += __shfl_xor_sync(0xffffffffu, del[i], 1);
       del[i] += __shfl_xor_sync(0xffffffffu, del[i], 2);
-      if (f < f1 && (lane & 3) == 0) a.delta[((long long)b * a.H + h) * a.Nq + qi] = del[i];
+      if (f < f1 && (lane & 3) == 0 && half == 0) a.delta[((long long)b * a.H + h) * a.Nq + qi] = del[i];
     }
   }
   const int ntile = __syncthreads_or(alive[0] || alive[1]) ? (c.n + T - 1) / T : 0;
@@ -248,8 +264,8 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
     __syncthreads();
     const float *Kt = Ks + st * EL, *Vt = Vs + st * EL;
     const uint32_t w[2] = {bits[st][0], bits[st][1]};
-#pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
+#pragma unroll(DP <= 32 ? 2 : 1)
+    for (int g = half; g < 4; g += 2) {
       const uint32_t wg = (w[g >> 1] >> ((g & 1) * 16)) & 0xffffu;
       if (wg == 0u || !rc.any(u0 + 16 * g)) continue;
       float s[2][4];
@@ -314,6 +330,33 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
     }
     __syncthreads();
   }
+  // the odd groups' sums join the even ones'
+  float* red = sm + (16 * warp + (lane >> 2)) * Ft<DP>::ld + col2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    if (half == 0) continue;
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) *reinterpret_cast<float2*>(red + 8 * i * Ft<DP>::ld + 8 * n) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+    if ((lane & 3) == 0) odd[16 * warp + (lane >> 2) + 8 * i] = make_float2(m[i], l[i]);
+  }
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 o = odd[16 * warp + (lane >> 2) + 8 * i];
+    const float mn = fmaxf(m[i], o.x);
+    const float x = BWD ? 1.f : (m[i] == -INFINITY ? 0.f : exp2f((m[i] - mn) * sc)), y = BWD ? 1.f : (o.x == -INFINITY ? 0.f : exp2f((o.x - mn) * sc));
+    m[i] = mn;
+    l[i] = l[i] * x + o.y * y;
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) {
+      const float2 z = *reinterpret_cast<const float2*>(red + 8 * i * Ft<DP>::ld + 8 * n);
+      acc[n][2 * i] = acc[n][2 * i] * x + z.x * y;
+      acc[n][2 * i + 1] = acc[n][2 * i + 1] * x + z.y * y;
+    }
+  }
   if (BWD) {
     store_f<DP>(acc, a.D, a.scale, lane, [&](int i, bool& keep) -> float* {
       const int f = f0 + 16 * warp + (lane >> 2) + 8 * i, qi = f / a.G;
@@ -323,8 +366,6 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       const float inv = alive[i] && l[i] != 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
       for (int n = 0; n < DP / 8; ++n) {
@@ -353,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a
   float* Os = Qs + 2 * EL;
   __shared__ float slse[2][T], sdel[2][T];
   __shared__ int spos[2][T];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col2 = (lane & 3) * 2;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7, col2 = (lane & 3) * 2;
   const int per = SINK ? (a.sinks + 15) / 16 * a.nchunk : (a.Nk + T - 1) / T;
   const int job = blockIdx.x % per, bh = blockIdx.x / per, b = bh / a.Hkv, hkv = bh - b * a.Hkv;
   const int chunk = SINK ? job % a.nchunk : -1, q0 = win_q0(a, b);
@@ -438,10 +479,9 @@ __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a
     }
     __syncthreads();
     const float *Qt = Qs + st * EL, *Ot = Os + st * EL;
-#pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
-      if (fl + t * T + 16 * g >= fh) break;
-      if (SINK && g != warp) continue;
+#pragma unroll(DP <= 32 ? 2 : 1)
+    for (int g = SINK ? warp : half; g < 4; g += SINK ? 4 : 2) {
+      if (fl + t * T + 16 * g >= fh || (SINK && (t & 1) != half)) break;
       const int pa = spos[st][16 * g], pb = spos[st][16 * g + 15];
       if (kb < ka || pb < ka - a.right || (pa > kb + a.left && ka >= a.sinks)) continue;
       uint32_t ob[2] = {0xffffffffu, 0xffffffffu};
@@ -474,8 +514,8 @@ __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a
   }
   if (SINK) {
     constexpr int OL = 2 * DP + 4;
-    for (int w = 0; w < 4; ++w) {
-      if (warp == w) {
+    for (int w = 0; w < 8; ++w) {
+      if (warp + 4 * half == w) {
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
@@ -496,6 +536,30 @@ __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a
     }
     return;
   }
+  float* red = sm + (16 * warp + (lane >> 2)) * (2 * Ft<DP>::ld) + col2;
+  if (half == 1) {
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float* o = red + 8 * i * (2 * Ft<DP>::ld) + 8 * n;
+        *reinterpret_cast<float2*>(o) = make_float2(dk[n][2 * i], dk[n][2 * i + 1]);
+        *reinterpret_cast<float2*>(o + Ft<DP>::ld) = make_float2(dv[n][2 * i], dv[n][2 * i + 1]);
+      }
+  }
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* o = red + 8 * i * (2 * Ft<DP>::ld) + 8 * n;
+      const float2 x = *reinterpret_cast<const float2*>(o), y = *reinterpret_cast<const float2*>(o + Ft<DP>::ld);
+      dk[n][2 * i] += x.x;
+      dk[n][2 * i + 1] += x.y;
+      dv[n][2 * i] += y.x;
+      dv[n][2 * i + 1] += y.y;
+    }
   if (part) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
