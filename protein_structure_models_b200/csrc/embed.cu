@@ -64,28 +64,44 @@ __device__ __forceinline__ float cvt(__nv_bfloat16 x) { return __bfloat162float(
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// One piece (16 bytes, or one element) of an output row per thread.
+// 2^lg threads a token, each with every 2^lg-th piece (16 bytes, or one element)
+// of its row, four tokens at a time: the tokens' indices, then their pieces, are in
+// flight together.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(const int* __restrict__ idx, const T* __restrict__ table, T* __restrict__ out,
-                                                        long long rows, int V, int C, int pieces, float scale) {
-  const long long n = rows * pieces, step = (long long)gridDim.x * blockDim.x;
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += step) {
-    const long long t = n < (1ll << 31) ? (long long)((unsigned)e / (unsigned)pieces) : e / pieces;
-    const int p = (int)(e - t * pieces), v = __ldg(idx + t);
-    const bool on = v >= 0 && v < V;
-    if (VEC) {
-      constexpr int N = Vec<T>::n;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (on) {
-        float x[N];
-        unpack<T>(__ldg(reinterpret_cast<const uint4*>(table + (long long)v * C) + p), x);
+                                                        long long rows, int V, int C, int pieces, int lg, float scale) {
+  constexpr int N = VEC ? Vec<T>::n : 1, U = 4;
+  const int me = threadIdx.x & ((1 << lg) - 1), groups = 256 >> lg;
+  const long long step = (long long)gridDim.x * groups * U;
+  for (long long t = ((long long)blockIdx.x * groups + (threadIdx.x >> lg)) * U; t < rows; t += step) {
+    int v[U];
 #pragma unroll
-        for (int k = 0; k < N; ++k) x[k] *= scale;
-        w = pack<T>(x);
+    for (int k = 0; k < U; ++k) v[k] = t + k < rows ? __ldg(idx + t + k) : -1;
+    for (int p = me; p < pieces; p += 1 << lg) {
+      uint4 w[U];
+      T one[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const bool on = v[k] >= 0 && v[k] < V;
+        const T* src = table + (long long)(on ? v[k] : 0) * C + p * N;
+        if (VEC) w[k] = on ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+        else one[k] = on ? *src : T(0.f);
       }
-      reinterpret_cast<uint4*>(out + t * C)[p] = w;
-    } else {
-      put(out + t * C + p, on ? cvt(table[(long long)v * C + p]) * scale : 0.f);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (t + k >= rows) break;
+        T* dst = out + (t + k) * C + p * N;
+        const bool on = v[k] >= 0 && v[k] < V;                // a skipped row is 0 whatever the scale
+        if (VEC) {
+          float x[N];
+          unpack<T>(w[k], x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) x[e] = on ? x[e] * scale : 0.f;
+          *reinterpret_cast<uint4*>(dst) = pack<T>(x);
+        } else {
+          put(dst, on ? cvt(one[k]) * scale : 0.f);
+        }
+      }
     }
   }
 }
@@ -93,7 +109,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const int* __restrict__ 
 // ---------------------------------------------------------------- stable sort
 // Digit counts of every block of 2048 elements: hist[digit][block].
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __restrict__ key, int n, int V, int first, int shift,
-                                                                  int mask, int* __restrict__ hist, uint8_t* __restrict__ mark) {
+                                                                  int mask, int* __restrict__ hist) {
   __shared__ int cnt[kDigits];
   cnt[threadIdx.x] = 0;
   __syncthreads();
@@ -107,7 +123,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int* __r
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     if (v[k] < 0) continue;
-    if (first && v[k] < V) mark[v[k]] = 1;                    // every writer writes the same
     atomicAdd(&cnt[(v[k] >> shift) & mask], 1);
   }
   __syncthreads();
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int* __r
 // part[chunk][0]: the run that came from the chunk before; [1]: the run that
 // starts here and goes on.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const int* __restrict__ key, const int* __restrict__ tok, const T* __restrict__ dout,
+__global__ void __launch_bounds__(256, 4) embed_sum_kernel(const int* __restrict__ key, const int* __restrict__ tok, const T* __restrict__ dout,
                                                         int n, int V, int C, int L, int tpc, int slabs, float scale,
                                                         float* __restrict__ dtable, float* __restrict__ part, int nchunk) {
   constexpr int N = VEC ? Vec<T>::n : 1, U = 8;
@@ -376,30 +391,35 @@ __device__ __forceinline__ void add_pieces(float (&x)[N], const float* part, int
 }
 // CTAs [0, ncross): a warp looks at one chunk.  If a run starts in it and goes
 // on, its pieces are added: up to 16 by the warp, more by all 16 warps of the
-// CTA, in 16 neighbouring stretches whose sums are added in order.  CTAs beyond:
-// rows without a token are zero (marked by the sort's first pass, or searched
-// for in a short list).  blockIdx.y: slab of 32 N columns.
+// CTA, in 16 neighbouring stretches whose sums are added in order.  CTAs beyond: a
+// warp searches the list for 32 rows at once, one a lane, and writes zeros to those
+// without a token.  blockIdx.y: slab of 32 N columns of the sums.
 template <int N>
 __global__ void __launch_bounds__(512) embed_join_kernel(const int* __restrict__ key, int n, int V, int C, int L, int nchunk,
                                                          int ncross, float scale, const float* __restrict__ part,
-                                                         const uint8_t* __restrict__ mark, float* __restrict__ dtable) {
+                                                         float* __restrict__ dtable) {
   __shared__ float red[16][32 * N];
   __shared__ int long_last[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.y * 32 * N, c = c0 + lane * N;
   if ((int)blockIdx.x >= ncross) {
-    const long long step = (long long)(gridDim.x - ncross) * 16;
-    for (long long v = (long long)(blockIdx.x - ncross) * 16 + warp; v < V; v += step) {
-      bool used;
-      if (mark != nullptr) {
-        used = mark[v] != 0;
-      } else {
+    if (blockIdx.y > 0) return;
+    const long long step = (long long)(gridDim.x - ncross) * 16 * 32;
+    for (long long v0 = ((long long)(blockIdx.x - ncross) * 16 + warp) * 32; v0 < V; v0 += step) {
+      const long long v = v0 + lane;
+      bool none = false;
+      if (v < V) {
         const int b = lower_bound(key, n, (int)v);
-        used = b < n && key[b] == (int)v;
+        none = b >= n || key[b] != (int)v;
       }
-      if (used) continue;
-      if (c < C) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) dtable[v * C + c + k] = 0.f;
+      for (unsigned left = __ballot_sync(0xffffffffu, none); left != 0u; left &= left - 1u) {
+        float* o = dtable + (v0 + __ffs(left) - 1) * C;
+        for (int k = lane * N; k < C; k += 32 * N) {
+          if (N == 4) {
+            *reinterpret_cast<float4*>(o + k) = make_float4(0.f, 0.f, 0.f, 0.f);
+          } else {
+            o[k] = 0.f;
+          }
+        }
       }
     }
     return;
@@ -409,19 +429,16 @@ __global__ void __launch_bounds__(512) embed_join_kernel(const int* __restrict__
   if (q + 1 < nchunk) {
     const int cur = key[e];
     if (cur < V && key[e - 1] == cur && !(q > 0 && key[q * L - 1] == cur)) {
-      // last chunk that begins inside the run
-      const bool in = q + 1 + lane < nchunk && key[(q + 1 + lane) * L] == cur;
-      const unsigned all = __ballot_sync(0xffffffffu, in);
-      int last = q + __ffs(~all) - 1;
-      if (all == 0xffffffffu) {
-        int lo = q + 32, hi = nchunk;                       // key at lo L is cur, at hi L it is not (or the list ends)
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (key[(size_t)mid * L] == cur) lo = mid;
-          else hi = mid;
-        }
-        last = lo;
+      // last chunk that begins inside the run: 32 places of the rest at a time
+      int lo = q + 1, hi = nchunk;                            // lo begins inside, hi does not (or the list ends)
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned in = __ballot_sync(0xffffffffu, at < hi && key[(size_t)at * L] == cur);
+        const int k = in == 0xffffffffu ? 31 : __ffs(~in) - 2;   // the last place inside
+        if (lo + (k + 1) * step < hi) hi = lo + (k + 1) * step;
+        lo += k * step;
       }
+      const int last = lo;
       if (last - q < 16) {
         if (c < C) {
           float x[N] = {0.f};
@@ -459,7 +476,7 @@ bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 // Workspace of the gradient: two copies of (key, token), digit counts, pieces.
 struct EmbedPlan {
   int nblk, passes, bits, L, nchunk;
-  size_t off_key[2], off_tok[2], off_hist, off_total, off_mark, off_part, total;
+  size_t off_key[2], off_tok[2], off_hist, off_total, off_part, total;
 };
 EmbedPlan embed_plan(long long T, int V, int C) {
   EmbedPlan p;
@@ -485,7 +502,6 @@ EmbedPlan embed_plan(long long T, int V, int C) {
   }
   p.off_hist = take((size_t)p.nblk * kDigits * 4);
   p.off_total = take(kDigits * 4);
-  p.off_mark = take((size_t)V);
   p.off_part = take((size_t)p.nchunk * 2 * C * 4);
   p.total = o;
   return p;
@@ -495,12 +511,14 @@ template <typename T>
 cudaError_t embed_fwd(const int* idx, const void* table, void* out, long long rows, int V, int C, float scale, cudaStream_t s) {
   const bool vec = C % Vec<T>::n == 0 && is_aligned(table, 16) && is_aligned(out, 16);
   const int pieces = vec ? C / Vec<T>::n : C;
-  const long long need = (rows * pieces + 255) / 256, most = 148 * 64;
+  int lg = 0;
+  while ((1 << lg) < pieces && lg < 8) ++lg;
+  const long long need = (rows + 4 * (256 >> lg) - 1) / (4 * (256 >> lg)), most = 148 * 32;
   const unsigned grid = (unsigned)(need < most ? need : most);
   if (vec)
-    embed_fwd_kernel<T, true><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, scale);
+    embed_fwd_kernel<T, true><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, lg, scale);
   else
-    embed_fwd_kernel<T, false><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, scale);
+    embed_fwd_kernel<T, false><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, lg, scale);
   return cudaGetLastError();
 }
 
@@ -577,7 +595,6 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
   const int* key = idx;
   const int* tok = nullptr;
   int at = 0;
-  const uint8_t* mark = nullptr;
   if (n > 0 && n <= kSortBlock) {
     int* okey = reinterpret_cast<int*>(ws + p.off_key[0]);
     int* otok = reinterpret_cast<int*>(ws + p.off_tok[0]);
@@ -585,14 +602,11 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
     key = okey;
   } else if (n > 0) {
     const int mask = (1 << p.bits) - 1;
-    uint8_t* mk = ws + p.off_mark;
-    if (cudaMemsetAsync(mk, 0, (size_t)V, s) != cudaSuccess) return FIPA_ERR_CUDA;
-    mark = mk;
     for (int k = 0; k < p.passes; ++k) {
       at = k & 1;
       int* okey = reinterpret_cast<int*>(ws + p.off_key[at]);
       int* otok = reinterpret_cast<int*>(ws + p.off_tok[at]);
-      sort_count_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, n, V, k == 0, k * p.bits, mask, hist, mk);
+      sort_count_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, n, V, k == 0, k * p.bits, mask, hist);
       sort_scan_kernel<<<mask + 1, 256, 0, s>>>(hist, total, p.nblk);
       sort_move_kernel<<<p.nblk, kSortThreads, 0, s>>>(key, tok, n, V, k == 0, k * p.bits, mask, hist, total, p.nblk, okey, otok);
       key = okey;
@@ -605,12 +619,12 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
     if (e != cudaSuccess) return FIPA_ERR_CUDA;
   }
   const int ncross = p.nchunk > 1 ? (p.nchunk - 1 + 15) / 16 : 0;
-  const long long fill = ((long long)V + 15) / 16;
-  const unsigned gx = (unsigned)(ncross + (fill < 148 * 8 ? fill : 148 * 8));
+  const long long fill = ((long long)V + 511) / 512;
+  const unsigned gx = (unsigned)(ncross + (fill < 148 * 4 ? fill : 148 * 4));
   const float* part = reinterpret_cast<const float*>(ws + p.off_part);
   if (C % 4 == 0 && is_aligned(d_table, 16))
-    embed_join_kernel<4><<<dim3(gx, (unsigned)((C + 127) / 128)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, mark, d_table);
+    embed_join_kernel<4><<<dim3(gx, (unsigned)((C + 127) / 128)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, d_table);
   else
-    embed_join_kernel<1><<<dim3(gx, (unsigned)((C + 31) / 32)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, mark, d_table);
+    embed_join_kernel<1><<<dim3(gx, (unsigned)((C + 31) / 32)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, d_table);
   return cudaGetLastError() == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
 }
