@@ -17,6 +17,7 @@
 
 #include "fipa.h"
 #include "kernels.h"
+#include "sm100.cuh"
 
 #define FIPA_API extern "C" __attribute__((visibility("default")))
 
@@ -45,34 +46,6 @@ __device__ __forceinline__ float cvt(__nv_bfloat16 x) { return __bfloat162float(
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Two float32 operations an instruction: a row's arithmetic is what bounds these
-// kernels beside the memory.
-__device__ __forceinline__ unsigned long long bits2(float2 a) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-  return r;
-}
-__device__ __forceinline__ float2 pair2(unsigned long long a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 constexpr int H = E / 2;                   // pairs of a row per thread
 
 // The thread's elements of a row: 8 neighbours by 16-byte accesses (VEC), or

@@ -60,8 +60,10 @@ inline WinSinkPlan win_sink_plan(const WinArgs& a, int key_tile) {
   s.sink_pos = (int)(end < a.Nk ? end : a.Nk) + a.left;
   if (a.sinks <= 0 || s.sink_pos >= a.Nk) return s;          // the window reaches every position
   const long long tiles = ((long long)a.Nq * a.G + 63) / 64;
-  s.chunk_tiles = 2;
-  while ((tiles + s.chunk_tiles - 1) / s.chunk_tiles > 256) s.chunk_tiles *= 2;
+  // chunks of at least two tiles, and no more of them than are resident at once (three CTAs an SM)
+  const long long jobs = (long long)a.B * a.Hkv * ((a.sinks + 15) / 16), most = 444 / jobs < 1 ? 1 : 444 / jobs;
+  s.chunk_tiles = (int)((tiles + most - 1) / most);
+  if (s.chunk_tiles < 2) s.chunk_tiles = 2;
   s.nchunk = (int)((tiles + s.chunk_tiles - 1) / s.chunk_tiles);
   s.part_floats = (size_t)a.B * a.Hkv * (s.nchunk + 1) * a.sinks * (a.D + a.Dv);
   return s;

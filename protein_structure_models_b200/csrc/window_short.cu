@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
       if (!alive[i]) pos[i] = kNowhere;
     }
     const bool any = __any_sync(0xffffffffu, alive[0] || alive[1]);
-    float acc[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2];
+    float2 l2[2] = {both(0.f), both(0.f)};
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
         for (int i = 0; i < 2; ++i) {
           const float mn = fmaxf(m[i], mx[i]), f = ex2_approx(mn == -INFINITY ? -INFINITY : (m[i] - mn) * sc);
           m[i] = mn;
-          l[i] *= f;
+          l2[i] = mul2(l2[i], both(f));
 #pragma unroll
           for (int n = 0; n < DP / 8; ++n) {
             acc[n][2 * i] *= f;
@@ -183,15 +184,16 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         if (!go[g]) continue;
-        float p[2][4];
+        uint32_t pf[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[h][e] = ex2_approx(fmaf(sc_[2 * g + h][e], sc, -mb[e >> 1]));
-            l[e >> 1] += p[h][e];
+          for (int i = 0; i < 2; ++i) {
+            float2 p = fma2(make_float2(sc_[2 * g + h][2 * i], sc_[2 * g + h][2 * i + 1]), both(sc), both(-mb[i]));
+            p = make_float2(ex2_approx(p.x), ex2_approx(p.y));
+            l2[i] = add2(l2[i], p);
+            pf[2 * h + i] = pack(p.x, p.y);
           }
-        const uint32_t pf[4] = {pack(p[0][0], p[0][1]), pack(p[0][2], p[0][3]), pack(p[1][0], p[1][1]), pack(p[1][2], p[1][3])};
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
           if (n >= kv) break;
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(128) win_short_fwd_kernel(const WinArgs a) {
     float inv[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      l[i] = l2[i].x + l2[i].y;
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       inv[i] = alive[i] && l[i] != 0.f ? 1.f / l[i] : 0.f;
@@ -270,7 +273,8 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
   for (int f0 = 16 * warp; f0 < s.F; f0 += 64) {
     const int f1 = min(s.F, f0 + 16);
     const Units un = units_of(a, win_cols(a, s.q0, f0, f1));
-    float lse2[2], del[2], eps[2] = {0.f, 0.f}, acc[DP / 8][4], avg[DP / 8][4];
+    float lse2[2], del[2], eps[2], acc[DP / 8][4], avg[DP / 8][4];
+    float2 e2[2] = {both(0.f), both(0.f)};
     int pos[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -316,17 +320,18 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
             mma(dp[1], gf[kk], bf[2], bf[3]);
           }
         }
+        uint32_t pf[4], df[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = ex2_approx(fmaf(x[h][e], sc, -lse2[e >> 1]));
-            x[h][e] = ob[e >> 1] & (1u << (16 * g + 8 * h + (e & 1))) ? y : 0.f;
-            dp[h][e] = x[h][e] * (dp[h][e] - del[e >> 1]);
-            eps[e >> 1] += dp[h][e];
+          for (int i = 0; i < 2; ++i) {
+            const float2 y = fma2(make_float2(x[h][2 * i], x[h][2 * i + 1]), both(sc), both(-lse2[i]));
+            const float2 p = make_float2(ob[i] & (1u << (16 * g + 8 * h)) ? ex2_approx(y.x) : 0.f, ob[i] & (2u << (16 * g + 8 * h)) ? ex2_approx(y.y) : 0.f);
+            const float2 d = mul2(p, add2(make_float2(dp[h][2 * i], dp[h][2 * i + 1]), both(-del[i])));
+            e2[i] = add2(e2[i], d);
+            pf[2 * h + i] = pack(p.x, p.y);
+            df[2 * h + i] = pack(d.x, d.y);
           }
-        const uint32_t pf[4] = {pack(x[0][0], x[0][1]), pack(x[0][2], x[0][3]), pack(x[1][0], x[1][1]), pack(x[1][2], x[1][3])};
-        const uint32_t df[4] = {pack(dp[0][0], dp[0][1]), pack(dp[0][2], dp[0][3]), pack(dp[1][0], dp[1][1]), pack(dp[1][2], dp[1][3])};
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
           if (n >= kd) break;
@@ -339,6 +344,8 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
         }
       }
     }
+    eps[0] = e2[0].x + e2[0].y;
+    eps[1] = e2[1].x + e2[1].y;
     take_back<DP>(acc, avg, eps);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -399,18 +406,19 @@ __global__ void __launch_bounds__(128) win_short_bwd_kernel(const WinArgs a) {
           mma(dp[1], vf[kk], bf[2], bf[3]);
         }
       }
+      uint32_t pf[4], df[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float2 ls = *reinterpret_cast<const float2*>(slse + f0 + 8 * h + col2), de = *reinterpret_cast<const float2*>(sdel + f0 + 8 * h + col2);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = ex2_approx(fmaf(x[h][e], sc, -(e & 1 ? ls.y : ls.x)));
-          x[h][e] = ob[e >> 1] & (1u << (8 * h + (e & 1))) ? y : 0.f;
-          dp[h][e] = x[h][e] * (dp[h][e] - (e & 1 ? de.y : de.x));
+        for (int i = 0; i < 2; ++i) {
+          const float2 y = fma2(make_float2(x[h][2 * i], x[h][2 * i + 1]), both(sc), make_float2(-ls.x, -ls.y));
+          const float2 p = make_float2(ob[i] & (1u << (8 * h)) ? ex2_approx(y.x) : 0.f, ob[i] & (2u << (8 * h)) ? ex2_approx(y.y) : 0.f);
+          const float2 d = mul2(p, add2(make_float2(dp[h][2 * i], dp[h][2 * i + 1]), make_float2(-de.x, -de.y)));
+          pf[2 * h + i] = pack(p.x, p.y);
+          df[2 * h + i] = pack(d.x, d.y);
         }
       }
-      const uint32_t pf[4] = {pack(x[0][0], x[0][1]), pack(x[0][2], x[0][3]), pack(x[1][0], x[1][1]), pack(x[1][2], x[1][3])};
-      const uint32_t df[4] = {pack(dp[0][0], dp[0][1]), pack(dp[0][2], dp[0][3]), pack(dp[1][0], dp[1][1]), pack(dp[1][2], dp[1][3])};
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
         uint32_t bf[4];

@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
   const uint32_t tmem = *slot;
   const WaitCtx wc{abort_flag, a.status, a.timeout_ns};
   const float sc = a.scale * kLog2e;
-  float m = -INFINITY, l = 0.f, lse2 = INFINITY, del = 0.f, eps = 0.f;
+  float m = -INFINITY, l = 0.f, lse2 = INFINITY, del = 0.f;
+  float2 eps = both(0.f);
 
   if (warp >= 5) {
     // ------------------------------------------------------------- copies
@@ -376,23 +377,24 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       if (MODE == kFwd) {
         const uint32_t w[2] = {reinterpret_cast<const uint32_t*>(inf)[0], reinterpret_cast<const uint32_t*>(inf)[1]};
         const bool edge = (w[0] & w[1]) != 0xffffffffu || !rc.all(u0, kCols);
-        uint32_t s[2][32];
-        tmem_ld32(trow + L::s_of(t), s[0]);
-        tmem_ld32(trow + L::s_of(t) + 32, s[1]);
-        tmem_ld_wait();
-        if (edge) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        // 32 scores at a time, read twice: 64 at once do not fit the registers
+        auto scores = [&](int h, uint32_t (&s)[32]) {
+          tmem_ld32(trow + L::s_of(t) + 32 * h, s);
+          tmem_ld_wait();
+          if (edge) {
             const uint32_t on = w[h] & row.sees(u0 + 32 * h);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[h][e] = (on >> e) & 1u ? s[h][e] : __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e) s[e] = (on >> e) & 1u ? s[e] : __float_as_uint(-INFINITY);
           }
-        }
+        };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[32];
+          scores(h, s);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[h][e]));
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+        }
         mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         // m follows the true maximum only when it would be left behind by 2^8
         if (__any_sync(0xffffffffu, (mx[0] - m) * sc > kWinLag)) {
@@ -413,20 +415,21 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           }
         }
         const float mb = m == -INFINITY ? 0.f : m * sc;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t p[16];
+          uint32_t s[32], p[16];
+          scores(h, s);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float x = ex2_approx(fmaf(__uint_as_float(s[h][e]), sc, -mb)), y = ex2_approx(fmaf(__uint_as_float(s[h][e + 1]), sc, -mb));
-            sum[e & 2] += x;
-            sum[(e & 2) + 1] += y;
-            p[e / 2] = pack(x, y);
+          for (int e = 0; e < 16; ++e) {
+            float2 x = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), both(sc), both(-mb));
+            x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sum[e & 1] = add2(sum[e & 1], x);
+            p[e] = pack(x.x, x.y);
           }
           tmem_st16(trow + L::p_of(t) + 16 * h, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       } else if (MODE == kRowSide) {
         const uint32_t w[2] = {reinterpret_cast<const uint32_t*>(inf)[0], reinterpret_cast<const uint32_t*>(inf)[1]};
         const bool edge = (w[0] & w[1]) != 0xffffffffu || !rc.all(u0, kCols);
@@ -438,8 +441,13 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           tmem_ld32(trow + L::dP + 32 * h, d);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            s[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(s[e]), sc, -lse2)) * (__uint_as_float(d[e]) - del));
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), both(sc), both(-lse2));
+            const float2 y = mul2(make_float2(ex2_approx(x.x), ex2_approx(x.y)),
+                                  add2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), both(-del)));
+            s[e] = __float_as_uint(y.x);
+            s[e + 1] = __float_as_uint(y.y);
+          }
           if (edge) {
             const uint32_t on = w[h] & row.sees(u0 + 32 * h);
 #pragma unroll
@@ -448,10 +456,11 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
           // dS as two bfloat16 numbers: with one, its rounding would weigh as much as that of d_q itself
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x = __uint_as_float(s[2 * e]), y = __uint_as_float(s[2 * e + 1]);
-            eps += x + y;
-            p[e] = pack(x, y);
-            o[e] = pack(x - __uint_as_float(p[e] << 16), y - __uint_as_float(p[e] & 0xffff0000u));
+            const float2 x = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+            eps = add2(eps, x);
+            p[e] = pack(x.x, x.y);
+            const float2 y = add2(x, make_float2(-__uint_as_float(p[e] << 16), -__uint_as_float(p[e] & 0xffff0000u)));
+            o[e] = pack(y.x, y.y);
           }
           if (!free) {
             free = __all_sync(0xffffffffu, mbar_wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, wc, 89));
@@ -477,12 +486,17 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 x = *reinterpret_cast<const float4*>(sl + 32 * h + e), y = *reinterpret_cast<const float4*>(sl + 64 + 32 * h + e);
-            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            const float2 xs[2] = {make_float2(-x.x, -x.y), make_float2(-x.z, -x.w)}, ys[2] = {make_float2(-y.x, -y.y), make_float2(-y.z, -y.w)};
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const float ex = ex2_approx(fmaf(__uint_as_float(s[e + z]), sc, -xs[z])), pr = (on >> (e + z)) & 1u ? ex : 0.f;
-              s[e + z] = __float_as_uint(pr);
-              d[e + z] = __float_as_uint(pr * (__uint_as_float(d[e + z]) - ys[z]));
+            for (int z = 0; z < 2; ++z) {
+              const int i = e + 2 * z;
+              const float2 u = fma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), both(sc), xs[z]);
+              const float2 pr = make_float2((on >> i) & 1u ? ex2_approx(u.x) : 0.f, (on >> (i + 1)) & 1u ? ex2_approx(u.y) : 0.f);
+              const float2 ds = mul2(pr, add2(make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), ys[z]));
+              s[i] = __float_as_uint(pr.x);
+              s[i + 1] = __float_as_uint(pr.y);
+              d[i] = __float_as_uint(ds.x);
+              d[i + 1] = __float_as_uint(ds.y);
             }
           }
 #pragma unroll
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
         if (a.lse != nullptr && in) a.lse[((long long)b * a.H + h) * a.Nq + i] = some ? fmaf(m, a.scale, logf(l)) : -INFINITY;
       } else {
         // delta from the rounded out is off by the sum of dS, which is 0 for the right one: for the key side
-        if (in) a.delta[((long long)b * a.H + h) * a.Nq + i] = del + eps;
+        if (in) a.delta[((long long)b * a.H + h) * a.Nq + i] = del + (eps.x + eps.y);
         write_row(trow, L::acc0, a.D, a.scale, done, done && alive && lse2 != INFINITY, in ? static_cast<bf16*>(a.d_q) + o * a.D : nullptr);
       }
     } else if (split && first < a.sinks) {
