@@ -166,13 +166,17 @@ struct RowSum {
   int turn;
   __device__ __forceinline__ float operator()(float v, int tpr) {
     const int w = tpr < 32 ? tpr : 32;
-    for (int o = w >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < w) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (tpr > 32) v = across(make_float2(v, 0.f), tpr).x;
     return v;
   }
   __device__ __forceinline__ float2 operator()(float2 v, int tpr) {
     const int w = tpr < 32 ? tpr : 32;
-    for (int o = w >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= w) continue;
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
       v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
@@ -210,11 +214,11 @@ __device__ __forceinline__ float2 there(int e, int n) {
 
 // mean and rstd of the row; z becomes z - mean
 template <bool VEC>
-__device__ __forceinline__ float2 moments(float2 (&z)[H], int n, const NormArgs& a, float inv, RowSum& sum) {
+__device__ __forceinline__ float2 moments(float2 (&z)[H], int n, const NormArgs& a, int tpr, float inv, RowSum& sum) {
   float mean = 0.f;
   if (!a.rms) {
     const float2 v = add2(add2(z[0], z[1]), add2(z[2], z[3]));
-    mean = sum(v.x + v.y, a.tpr) * inv;
+    mean = sum(v.x + v.y, tpr) * inv;
   }
   float2 v = both(0.f);
 #pragma unroll
@@ -224,7 +228,7 @@ __device__ __forceinline__ float2 moments(float2 (&z)[H], int n, const NormArgs&
     v = fma2(z[e], z[e], v);
   }
   const float q = VEC && n == 0 ? 0.f : v.x + v.y;
-  return make_float2(mean, rsqrtf(sum(q, a.tpr) * inv + a.eps));
+  return make_float2(mean, rsqrtf(sum(q, tpr) * inv + a.eps));
 }
 
 // 1 / (1 + 2^(-x log2 e)); the rounding of x log2 e, which 2^() would pass on
@@ -241,28 +245,31 @@ __device__ __forceinline__ float2 sigmoid(float2 x) {
   return p;
 }
 
-template <typename TS, typename TB, bool VEC, int BLOCK>
-__global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const NormArgs a) {
+// CTAs of the forward on an SM: 1024 threads, or 768 where element-wise accesses take more registers.
+constexpr int fwd_ctas(int block, bool vec) { return block > 512 ? 1 : (vec ? 1024 : 768) / block < 1 ? 1 : (vec ? 1024 : 768) / block; }
+
+template <typename TS, typename TB, bool VEC, int BLOCK, int TPR>
+__global__ void __launch_bounds__(BLOCK, fwd_ctas(BLOCK, VEC)) norm_fwd_kernel(const NormArgs a) {
   typedef Slot<TS, VEC, BLOCK> SS;
   typedef Slot<TB, VEC, BLOCK> SB;
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kStage = SS::kBytes + 2 * SB::kBytes;
   __shared__ float2 red[2][32];
   RowSum sum{red, 0};
-  const int t = threadIdx.x & (a.tpr - 1), rpb = BLOCK / a.tpr;
+  const int tpr = TPR > 0 ? TPR : a.tpr, t = threadIdx.x & (tpr - 1), rpb = BLOCK / tpr;
   const bool branch = a.u != nullptr, gated = a.gate != nullptr;
-  const int n = mine<VEC>(t, a.tpr, a.C);
+  const int n = mine<VEC>(t, tpr, a.C);
   const float inv = 1.f / (float)a.C;
   const long long step = (long long)gridDim.x * rpb;
-  const long long first = (long long)blockIdx.x * rpb + threadIdx.x / a.tpr;     // this thread's rows: first, first + step, ...
+  const long long first = (long long)blockIdx.x * rpb + threadIdx.x / tpr;     // this thread's rows: first, first + step, ...
   bool soon;                                                                     // whether the row to be fetched next is valid
   auto look = [&](long long row) { return row < a.rows && (a.mask == nullptr || a.mask[row] != 0); };
   auto fetch = [&](int k, long long row, bool live) {
     uint8_t* slot = ring + (k & 1) * kStage;
     const long long o = (row < a.rows ? row : 0) * a.C;
-    SS::fetch(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, row < a.rows);
-    if (branch) SB::fetch(slot + SS::kBytes, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live);
-    if (gated) SB::fetch(slot + SS::kBytes + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live);
+    SS::fetch(slot, static_cast<const TS*>(a.s) + o, t, tpr, a.C, row < a.rows);
+    if (branch) SB::fetch(slot + SS::kBytes, static_cast<const TB*>(a.u) + o, t, tpr, a.C, live);
+    if (gated) SB::fetch(slot + SS::kBytes + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, tpr, a.C, live);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   bool live0 = look(first), live1 = look(first + step);
@@ -276,40 +283,40 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
     const uint8_t* slot = ring + (k & 1) * kStage;
     float2 s[H], u[H], g[H];
     asm volatile("cp.async.wait_group 1;" ::: "memory");
-    SS::get(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, in, s);
-    if (branch) SB::get(slot + SS::kBytes, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
-    if (gated) SB::get(slot + SS::kBytes + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
+    SS::get(slot, static_cast<const TS*>(a.s) + o, t, tpr, a.C, in, s);
+    if (branch) SB::get(slot + SS::kBytes, static_cast<const TB*>(a.u) + o, t, tpr, a.C, live, u);
+    if (gated) SB::get(slot + SS::kBytes + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, tpr, a.C, live, g);
     float2 mu = make_float2(0.f, 0.f), mr = mu;
     if (branch) {
       if (a.post_w != nullptr) {
         float2 w[H], b[H];
-        mu = moments<VEC>(u, n, a, inv, sum);
-        get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
-        get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, b);
+        mu = moments<VEC>(u, n, a, tpr, inv, sum);
+        get_param<VEC>(a.post_w, 1.f, t, tpr, a.C, w);
+        get_param<VEC>(a.post_b, 0.f, t, tpr, a.C, b);
 #pragma unroll
         for (int e = 0; e < H; ++e) u[e] = fma2(mul2(u[e], both(mu.y)), w[e], b[e]);
       }
       float2 ga[H];
-      get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
+      get_param<VEC>(a.res_scale, 1.f, t, tpr, a.C, ga);
 #pragma unroll
       for (int e = 0; e < H; ++e) {
         if (gated) u[e] = mul2(u[e], sigmoid(g[e]));
         const float2 r = fma2(ga[e], u[e], s[e]);
         s[e] = live ? r : s[e];
       }
-      if (in) put_row<VEC>(static_cast<TS*>(a.r) + o, t, a.tpr, a.C, s);
+      if (in) put_row<VEC>(static_cast<TS*>(a.r) + o, t, tpr, a.C, s);
     }
     if (a.pre_w != nullptr) {
       float2 w[H], b[H];
-      mr = moments<VEC>(s, n, a, inv, sum);
-      get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, w);
-      get_param<VEC>(a.pre_b, 0.f, t, a.tpr, a.C, b);
+      mr = moments<VEC>(s, n, a, tpr, inv, sum);
+      get_param<VEC>(a.pre_w, 1.f, t, tpr, a.C, w);
+      get_param<VEC>(a.pre_b, 0.f, t, tpr, a.C, b);
 #pragma unroll
       for (int e = 0; e < H; ++e) {
         const float2 x = fma2(mul2(s[e], both(mr.y)), w[e], b[e]);
         s[e] = live ? x : both(0.f);
       }
-      if (in) put_row<VEC>(static_cast<TB*>(a.x) + o, t, a.tpr, a.C, s);
+      if (in) put_row<VEC>(static_cast<TB*>(a.x) + o, t, tpr, a.C, s);
     }
     if (a.stats != nullptr && in && t == 0)
       *reinterpret_cast<float4*>(a.stats + 4 * row) = live ? make_float4(mu.x, mu.y, mr.x, mr.y) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) norm_fwd_kernel(const Nor
 // Rows ahead in the backward: two, or one where 1024 threads' five tensors fill the shared memory.
 constexpr int bwd_slots(int block) { return block > 512 ? 1 : 2; }
 
-template <typename TS, typename TB, bool VEC, int BLOCK>
+template <typename TS, typename TB, bool VEC, int BLOCK, int TPR>
 __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd_kernel(const NormArgs a) {
   typedef Slot<TS, VEC, BLOCK> SS;
   typedef Slot<TB, VEC, BLOCK> SB;
@@ -332,26 +339,26 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
   float* acc_s = reinterpret_cast<float*>(ring);          // [rows of the CTA][5][C] when several share it
   __shared__ float2 red[2][32];
   RowSum sums{red, 0};
-  const int t = threadIdx.x & (a.tpr - 1), rpb = BLOCK / a.tpr;
+  const int tpr = TPR > 0 ? TPR : a.tpr, t = threadIdx.x & (tpr - 1), rpb = BLOCK / tpr;
   const float inv = 1.f / (float)a.C;
   const bool branch = a.u != nullptr, gated = a.gate != nullptr, pre = a.d_x != nullptr, thru = a.d_r != nullptr;
-  const int n = mine<VEC>(t, a.tpr, a.C);
+  const int n = mine<VEC>(t, tpr, a.C);
   float2 dga[H], dpw[H], dpb[H], dqw[H], dqb[H];
 #pragma unroll
   for (int e = 0; e < H; ++e) dga[e] = dpw[e] = dpb[e] = dqw[e] = dqb[e] = both(0.f);
   const long long step = (long long)gridDim.x * rpb;
-  const long long first = (long long)blockIdx.x * rpb + threadIdx.x / a.tpr;     // this thread's rows: first, first + step, ...
+  const long long first = (long long)blockIdx.x * rpb + threadIdx.x / tpr;     // this thread's rows: first, first + step, ...
   bool soon;                                                                     // whether the row to be fetched next is valid
   auto look = [&](long long row) { return row < a.rows && (a.mask == nullptr || a.mask[row] != 0); };
   auto fetch = [&](int k, long long row, bool live) {
     uint8_t* slot = ring + (k % NS) * kStage;
     const long long o = (row < a.rows ? row : 0) * a.C;
-    SS::fetch(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, live);
-    if (thru) SS::fetch(slot + SS::kBytes, static_cast<const TS*>(a.d_r) + o, t, a.tpr, a.C, row < a.rows);
+    SS::fetch(slot, static_cast<const TS*>(a.s) + o, t, tpr, a.C, live);
+    if (thru) SS::fetch(slot + SS::kBytes, static_cast<const TS*>(a.d_r) + o, t, tpr, a.C, row < a.rows);
     slot += 2 * SS::kBytes;
-    if (branch) SB::fetch(slot, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live);
-    if (gated) SB::fetch(slot + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live);
-    if (pre) SB::fetch(slot + 2 * SB::kBytes, static_cast<const TB*>(a.d_x) + o, t, a.tpr, a.C, live);
+    if (branch) SB::fetch(slot, static_cast<const TB*>(a.u) + o, t, tpr, a.C, live);
+    if (gated) SB::fetch(slot + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, tpr, a.C, live);
+    if (pre) SB::fetch(slot + 2 * SB::kBytes, static_cast<const TB*>(a.d_x) + o, t, tpr, a.C, live);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   bool live0 = look(first), live1 = look(first + step);
@@ -366,17 +373,17 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
     const uint8_t* slot = ring + (k % NS) * kStage;
     float2 s[H], u[H], g[H], dr[H], dx[H];
     asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
-    SS::get(slot, static_cast<const TS*>(a.s) + o, t, a.tpr, a.C, live, s);
+    SS::get(slot, static_cast<const TS*>(a.s) + o, t, tpr, a.C, live, s);
     if (thru) {
-      SS::get(slot + SS::kBytes, static_cast<const TS*>(a.d_r) + o, t, a.tpr, a.C, in, dr);
+      SS::get(slot + SS::kBytes, static_cast<const TS*>(a.d_r) + o, t, tpr, a.C, in, dr);
     } else {
 #pragma unroll
       for (int e = 0; e < H; ++e) dr[e] = both(0.f);
     }
     slot += 2 * SS::kBytes;
-    if (branch) SB::get(slot, static_cast<const TB*>(a.u) + o, t, a.tpr, a.C, live, u);
-    if (gated) SB::get(slot + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, a.tpr, a.C, live, g);
-    if (pre) SB::get(slot + 2 * SB::kBytes, static_cast<const TB*>(a.d_x) + o, t, a.tpr, a.C, live, dx);
+    if (branch) SB::get(slot, static_cast<const TB*>(a.u) + o, t, tpr, a.C, live, u);
+    if (gated) SB::get(slot + SB::kBytes, static_cast<const TB*>(a.gate) + o, t, tpr, a.C, live, g);
+    if (pre) SB::get(slot + 2 * SB::kBytes, static_cast<const TB*>(a.d_x) + o, t, tpr, a.C, live, dx);
     const float4 st = nst;
     if (live1) nst = *reinterpret_cast<const float4*>(a.stats + 4 * (row + step));
     else nst = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -384,9 +391,9 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
     // u -> uhat; y in w; s -> r; gate -> sigmoid
     if (branch) {
       float2 pb[H], ga[H];
-      get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, w);
-      get_param<VEC>(a.post_b, 0.f, t, a.tpr, a.C, pb);
-      get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
+      get_param<VEC>(a.post_w, 1.f, t, tpr, a.C, w);
+      get_param<VEC>(a.post_b, 0.f, t, tpr, a.C, pb);
+      get_param<VEC>(a.res_scale, 1.f, t, tpr, a.C, ga);
 #pragma unroll
       for (int e = 0; e < H; ++e) {
         if (a.post_w != nullptr) {
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
     }
     if (pre) {
       float2 qw[H], mx = both(0.f), my = both(0.f);
-      get_param<VEC>(a.pre_w, 1.f, t, a.tpr, a.C, qw);
+      get_param<VEC>(a.pre_w, 1.f, t, tpr, a.C, qw);
 #pragma unroll
       for (int e = 0; e < H; ++e) {
         s[e] = mul2(add2(s[e], both(-st.z)), both(st.w));         // rhat
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
         mx = add2(mx, dx[e]);
         my = fma2(dx[e], s[e], my);
       }
-      const float2 m = sums(make_float2(mx.x + mx.y, my.x + my.y), a.tpr);
+      const float2 m = sums(make_float2(mx.x + mx.y, my.x + my.y), tpr);
       const float c1 = a.rms || (VEC && n == 0) ? 0.f : m.x * inv, c2 = VEC && n == 0 ? 0.f : m.y * inv;
 #pragma unroll
       for (int e = 0; e < H; ++e) {                               // a masked row has st.w = 0
@@ -420,11 +427,11 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
         dr[e] = fma2(both(st.w), d, dr[e]);
       }
     }
-    if (a.d_s != nullptr && in) put_row<VEC>(static_cast<TS*>(a.d_s) + o, t, a.tpr, a.C, dr);
+    if (a.d_s != nullptr && in) put_row<VEC>(static_cast<TS*>(a.d_s) + o, t, tpr, a.C, dr);
     if (branch) {
       float2 ga[H], pw[H], mx = both(0.f), my = both(0.f);
-      get_param<VEC>(a.res_scale, 1.f, t, a.tpr, a.C, ga);
-      get_param<VEC>(a.post_w, 1.f, t, a.tpr, a.C, pw);
+      get_param<VEC>(a.res_scale, 1.f, t, tpr, a.C, ga);
+      get_param<VEC>(a.post_w, 1.f, t, tpr, a.C, pw);
 #pragma unroll
       for (int e = 0; e < H; ++e) {
         const float2 d = live ? dr[e] : both(0.f), gy = mul2(g[e], w[e]);
@@ -437,14 +444,14 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
         mx = add2(mx, w[e]);
         my = fma2(w[e], u[e], my);
       }
-      if (a.d_gate != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_gate) + o, t, a.tpr, a.C, g);
+      if (a.d_gate != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_gate) + o, t, tpr, a.C, g);
       if (a.post_w != nullptr) {
-        const float2 m = sums(make_float2(mx.x + mx.y, my.x + my.y), a.tpr);
+        const float2 m = sums(make_float2(mx.x + mx.y, my.x + my.y), tpr);
         const float e1 = a.rms ? 0.f : m.x * inv, e2 = m.y * inv;
 #pragma unroll
         for (int e = 0; e < H; ++e) w[e] = mul2(both(st.y), fma2(u[e], both(-e2), add2(w[e], both(-e1))));
       }
-      if (a.d_u != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_u) + o, t, a.tpr, a.C, w);
+      if (a.d_u != nullptr && in) put_row<VEC>(static_cast<TB*>(a.d_u) + o, t, tpr, a.C, w);
     }
     live0 = live1;
     live1 = soon;
@@ -462,18 +469,18 @@ __global__ void __launch_bounds__(BLOCK, BLOCK > 512 ? 1 : 512 / BLOCK) norm_bwd
     for (int k = 0; k < 5; ++k)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int c = col<VEC>(t, a.tpr, e);
+        const int c = col<VEC>(t, tpr, e);
         if (c < a.C) out[k * a.C + c] = e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x;
       }
     return;
   }
   // every row's sums side by side, then one thread a column adds them in row order
-  const int q = threadIdx.x / a.tpr, line = 5 * a.C;
+  const int q = threadIdx.x / tpr, line = 5 * a.C;
 #pragma unroll
   for (int k = 0; k < 5; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int c = col<VEC>(t, a.tpr, e);
+      const int c = col<VEC>(t, tpr, e);
       if (c < a.C) acc_s[q * line + k * a.C + c] = e & 1 ? sum[k][e / 2].y : sum[k][e / 2].x;
     }
   __syncthreads();
@@ -526,28 +533,34 @@ int norm_bwd_grid(long long rows, int C) {
   return (int)(need < most ? need : most);
 }
 
-template <typename TS, typename TB, bool VEC, int BLOCK>
+template <typename TS, typename TB, bool VEC, int BLOCK, int TPR>
 cudaError_t norm_launch(const NormArgs& a, bool bwd, int grid, cudaStream_t st) {
   const int ks = Slot<TS, VEC, BLOCK>::kBytes, kb = Slot<TB, VEC, BLOCK>::kBytes;
   size_t smem = bwd ? (size_t)bwd_slots(BLOCK) * (2 * ks + 3 * kb) : 2 * (size_t)(ks + 2 * kb);
   const size_t sums = bwd && BLOCK > a.tpr ? (size_t)(BLOCK / a.tpr) * 5 * a.C * sizeof(float) : 0;
   if (smem < sums) smem = sums;
-  const cudaError_t e = allow_max_smem(bwd ? reinterpret_cast<const void*>(&norm_bwd_kernel<TS, TB, VEC, BLOCK>)
-                                           : reinterpret_cast<const void*>(&norm_fwd_kernel<TS, TB, VEC, BLOCK>));
+  const cudaError_t e = allow_max_smem(bwd ? reinterpret_cast<const void*>(&norm_bwd_kernel<TS, TB, VEC, BLOCK, TPR>)
+                                           : reinterpret_cast<const void*>(&norm_fwd_kernel<TS, TB, VEC, BLOCK, TPR>));
   if (e != cudaSuccess) return e;
-  if (bwd) norm_bwd_kernel<TS, TB, VEC, BLOCK><<<grid, BLOCK, smem, st>>>(a);
-  else norm_fwd_kernel<TS, TB, VEC, BLOCK><<<grid, BLOCK, smem, st>>>(a);
+  if (bwd) norm_bwd_kernel<TS, TB, VEC, BLOCK, TPR><<<grid, BLOCK, smem, st>>>(a);
+  else norm_fwd_kernel<TS, TB, VEC, BLOCK, TPR><<<grid, BLOCK, smem, st>>>(a);
   return cudaGetLastError();
 }
-template <typename TS, typename TB, int BLOCK>
-cudaError_t norm_launch(const NormArgs& a, bool vec, bool bwd, int grid, cudaStream_t st) {
-  return vec ? norm_launch<TS, TB, true, BLOCK>(a, bwd, grid, st) : norm_launch<TS, TB, false, BLOCK>(a, bwd, grid, st);
+// Threads a row known at compile time where a row is a warp's (C up to 256) or the
+// CTA's (C beyond 1024): columns become constant offsets, sums unroll.
+template <typename TS, typename TB, bool VEC>
+cudaError_t norm_launch(const NormArgs& a, bool bwd, int grid, cudaStream_t st) {
+  switch (a.tpr) {
+    case 1024: return norm_launch<TS, TB, VEC, 1024, 1024>(a, bwd, grid, st);
+    case 512: return norm_launch<TS, TB, VEC, 512, 512>(a, bwd, grid, st);
+    case 256: return norm_launch<TS, TB, VEC, 256, 256>(a, bwd, grid, st);
+    case 32: return norm_launch<TS, TB, VEC, 256, 32>(a, bwd, grid, st);
+    default: return norm_launch<TS, TB, VEC, 256, 0>(a, bwd, grid, st);
+  }
 }
 template <typename TS, typename TB>
 cudaError_t norm_launch(const NormArgs& a, bool vec, bool bwd, int grid, cudaStream_t st) {
-  const int block = norm_block(a.tpr);
-  return block == 256 ? norm_launch<TS, TB, 256>(a, vec, bwd, grid, st)
-                      : (block == 512 ? norm_launch<TS, TB, 512>(a, vec, bwd, grid, st) : norm_launch<TS, TB, 1024>(a, vec, bwd, grid, st));
+  return vec ? norm_launch<TS, TB, true>(a, bwd, grid, st) : norm_launch<TS, TB, false>(a, bwd, grid, st);
 }
 
 fipa_status norm_args(const fipa_norm_dims* d, const fipa_norm_inputs* in, NormArgs* a) {
@@ -605,7 +618,7 @@ FIPA_API fipa_status fipa_norm_residual(const fipa_norm_dims* d, const fipa_norm
   const bool vec = a.C % E == 0 && params_aligned(a) && is_aligned(a.s, 16) && is_aligned(a.u, 16) && is_aligned(a.gate, 16) &&
                    is_aligned(r, 16) && is_aligned(x, 16);
   const int rpb = norm_block(a.tpr) / a.tpr;
-  const long long need = (a.rows + rpb - 1) / rpb, most = 148 * (1024 / norm_block(a.tpr));
+  const long long need = (a.rows + rpb - 1) / rpb, most = 148 * fwd_ctas(norm_block(a.tpr), vec);
   return norm_dispatch(d, a, vec, false, (int)(need < most ? need : most), static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FIPA_OK
              : FIPA_ERR_CUDA;
