@@ -382,14 +382,15 @@ typedef struct {
  *   q_start  [B] int32 or NULL
  *   out      [B,Nq,H,Dv] contiguous, every row written
  *   lse      [B,H,Nq] or NULL: natural-log logsumexp of the visible scores
- * FIPA_ERR_UNSUPPORTED for D or Dv > 128 or sinks > 128.  Allocates nothing;
- * runs on `stream`. */
+ * out and lse must not overlap the inputs.  FIPA_ERR_UNSUPPORTED for D or Dv > 128
+ * or sinks > 128.  Allocates nothing; runs on `stream`. */
 fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
                                   const fipa_heads* v, const uint8_t* mask, const int32_t* q_start,
                                   const fipa_window* win, void* out, float* lse, void* stream);
 
 /* Gradients of <d_out, out>: d_q [B,Nq,H,D], d_k [B,Nk,Hkv,D] (summed over the
- * heads of a group), d_v [B,Nk,Hkv,Dv], contiguous, every element written.
+ * heads of a group), d_v [B,Nk,Hkv,Dv], contiguous, every element written, none of
+ * them overlapping the inputs.
  * out and lse are those of the forward call; workspace >=
  * fipa_window_attention_backward_workspace_size() bytes, 256-byte aligned.
  * Deterministic: every sum is taken in a fixed order. */

@@ -733,7 +733,8 @@ cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s) {
   return cudaGetLastError();
 }
 cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s) {
-  if ((long long)a.Nq * a.G <= kWinStepRows) return launch_win_step(a, s);
+  const long long F = (long long)a.Nq * a.G;
+  if (F <= kWinStepRows || (F <= 4 * kWinStepRows && (long long)a.B * a.Hkv < 74)) return launch_win_step(a, s);
   if (use_short(a, false)) return launch_win_short(a, false, s);
   if (use_tc(a, false)) return launch_win_fwd_tc(a, s);
   const int w = a.D > a.Dv ? a.D : a.Dv;

@@ -186,6 +186,14 @@ def _raw_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
+def _used_on(stream: Optional[torch.cuda.Stream], *tensors):
+    """Tells the allocator that tensors made here are used on `stream`, not on the current one."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 class _OnDevice:
     """torch.cuda.device(dev), at no cost when dev is current already."""
     __slots__ = ("guard",)
@@ -459,6 +467,7 @@ class Fipa:
             out = {"out": o}
             if want_lse:
                 out["lse"] = lse = q.new_empty((B, H, Nq), dtype=torch.float32)
+            _used_on(stream, o, lse)
         else:
             self._check_buffers(out, {"out": ((B, Nq, H, w.Dv), q.dtype), "lse": ((B, H, Nq), torch.float32)}, q.device,
                                 ("out",))
@@ -496,12 +505,14 @@ class Fipa:
         if grads is None:
             dq, dk, dv = q.new_empty((B, Nq, H, w.D)), k.new_empty((B, w.Nk, w.Hkv, w.D)), v.new_empty((B, w.Nk, w.Hkv, w.Dv))
             grads = {"q": dq, "k": dk, "v": dv}
+            _used_on(stream, dq, dk, dv)
         else:
             self._check_buffers(grads, {"q": ((B, Nq, H, w.D), td), "k": ((B, w.Nk, w.Hkv, w.D), td),
                                         "v": ((B, w.Nk, w.Hkv, w.Dv), td)}, dev, ("q", "k", "v"))
             dq, dk, dv = grads["q"], grads["k"], grads["v"]
         if workspace is None:
             workspace = q.new_empty(self._window_workspace(w), dtype=torch.uint8)
+            _used_on(stream, workspace)
         elif workspace.get_device() != at or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
         st = self.lib.fipa_window_attention_backward(
@@ -689,6 +700,7 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
                 out["x"] = x = torch.empty_like(s, dtype=tb) if u is None else torch.empty_like(u)
             if want_stats:
                 out["stats"] = stats = s.new_empty((d.rows, 4), dtype=torch.float32)
+            _used_on(stream, r, x, stats)
         else:
             want = {"stats": ((d.rows, 4), torch.float32, False), "r": (s.shape, s.dtype, u is not None),
                     "x": (s.shape, tb, pre is not None)}
@@ -728,6 +740,7 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
             lines = s.new_empty((5, d.C), dtype=torch.float32).unbind(0)       # the parameters' gradients side by side
             for k, t, line in zip(NORM_PARAMS, par, lines):
                 grads[k] = None if t is None else line
+            _used_on(stream, grads["s"], grads["u"], grads["gate"], lines[0])
         else:
             have = {"s": s, "u": u, "gate": gate, **dict(zip(NORM_PARAMS, par))}
             for k, t in grads.items():
@@ -739,6 +752,7 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
             n = ctypes.c_size_t()
             _ok(lib.fipa_norm_residual_backward_workspace_size(d, n), "fipa_norm_residual_backward_workspace_size")
             workspace = s.new_empty(n.value, dtype=torch.uint8)
+            _used_on(stream, workspace)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on {dev}")
         g = FipaNormGrads(*[_addr(grads.get(f)) for f in NORM_GRADS])
@@ -762,6 +776,7 @@ def embedding(idx: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: O
         if out is None:
             o = table.new_empty((*idx.shape, C))
             out = {"out": o}
+            _used_on(stream, o)
         else:
             o = out["out"]
             _need("out", o, (*idx.shape, C), (td,), table.device)
@@ -794,6 +809,7 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
         if grads is None:
             g = d_out.new_empty((V, C), dtype=torch.float32)
             grads = {"table": g}
+            _used_on(stream, g)
         else:
             g = grads["table"]
             _need("table", g, (V, C), (torch.float32,), d_out.device)
@@ -801,6 +817,7 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
             n = ctypes.c_size_t()
             _ok(lib.fipa_embedding_backward_workspace_size(T, V, C, n), "fipa_embedding_backward_workspace_size")
             workspace = d_out.new_empty(n.value, dtype=torch.uint8)
+            _used_on(stream, workspace)
         elif workspace.get_device() != at or not workspace.is_contiguous():
             raise ValueError(f"workspace: need a contiguous tensor on cuda:{at}")
         st = lib.fipa_embedding_backward(F32 if td == torch.float32 else BF16, idx.data_ptr(), d_out.data_ptr(), T, V, C,

@@ -287,3 +287,22 @@ def test_refusals(handles):
                                     workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 3
     h.sync_status()
+
+
+def test_on_another_stream_with_its_own_allocations(handles):
+    """A call on a side stream whose temporaries and results the allocator hands out on the current one."""
+    h = handles["bf16"]
+    q, k, v = make("bf16", 2, 512, 512, 8, 2, 64, 64, 61)
+    d = rnd((2, 512, 8, 64), torch.bfloat16, 64)
+    kw = dict(window=(200, 0), sinks=4)
+    o = h.window_attention(q, k, v, want_lse=True, **kw)
+    want = [x.clone() for x in h.window_attention_backward(q, k, v, o["out"], o["lse"], d, **kw).values()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        s = h.window_attention(q, k, v, want_lse=True, stream=side, **kw)
+        g = list(h.window_attention_backward(q, k, v, s["out"], s["lse"], d, stream=side, **kw).values())
+        junk = [torch.full((1 << 20,), 3.0, device="cuda") for _ in range(8)]     # would land in freed temporaries
+        del junk, s
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(g, want))
