@@ -1,4 +1,5 @@
-"""Build libfipa.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libfipa.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_native.so (the compiled calls of the sequence operators from Python) with g++.
 
 Usage: python -m protein_structure_models_b200.build
 """
@@ -8,17 +9,21 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfipa.so")
+NATIVE = os.path.join(PKG, "_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+    "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "--expt-relaxed-constexpr",
 ]
 
@@ -27,29 +32,57 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _stale(target, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
+def _headers():
+    return glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _stale(LIB, sources() + _headers())
+
+
+def _run(cmd) -> str:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    return res.stdout + res.stderr
+
+
+def build_native(force: bool = False) -> str:
+    """Compile the Python calls against the headers of Python and PyTorch; returns the module's path."""
+    import sysconfig
+
+    import torch
+    if not force and not _stale(NATIVE, [NATIVE_SOURCE, os.path.join(INCLUDE, "fipa.h")]):
+        return NATIVE
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc], NATIVE_SOURCE,
+          "-o", NATIVE + ".tmp", "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(NATIVE + ".tmp", NATIVE)
+    return NATIVE
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source into one shared library; returns its path."""
-    if not force and not needs_build():
-        return LIB
-    nvcc = os.environ.get("NVCC", "nvcc")
-    cmd = [nvcc, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, *sources(), "-o", LIB + ".tmp"]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if verbose:
-        sys.stderr.write(res.stdout + res.stderr)
-    os.replace(LIB + ".tmp", LIB)
+    """Compile every CUDA source into one shared library (the sources side by side),
+    and the Python calls; returns the library's path."""
+    if force or needs_build():
+        nvcc = os.environ.get("NVCC", "nvcc")
+        flags = [*NVCC_FLAGS, *(["-Xptxas=-v"] if verbose else []), "-I", INCLUDE, "-I", CSRC]
+        with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(max(1, os.cpu_count() or 1)) as pool:
+            objects = [os.path.join(tmp, os.path.basename(s)[:-3] + ".o") for s in sources()]
+            for log in pool.map(lambda so: _run([nvcc, *flags, "-c", so[0], "-o", so[1]]), zip(sources(), objects)):
+                if verbose:
+                    sys.stderr.write(log)
+            _run([nvcc, *NVCC_FLAGS[:2], "-shared", "-Xcompiler", "-fPIC", *objects, "-o", LIB + ".tmp"])
+        os.replace(LIB + ".tmp", LIB)
+    build_native(force)
     return LIB
 
 

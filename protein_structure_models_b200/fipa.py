@@ -1,4 +1,5 @@
-"""ctypes binding of libfipa.so (include/fipa.h).  Argument marshalling only.
+"""Binding of libfipa.so (include/fipa.h).  Argument marshalling only: ctypes, and
+for the sequence operators the compiled calls of csrc/binding.cpp.
 
 Every step of the forward runs in the CUDA library; this module checks
 shapes/dtypes of torch tensors, allocates outputs and the workspace with torch,
@@ -71,6 +72,10 @@ class FipaError(RuntimeError):
 
 
 _lib = None
+_native = None         # the compiled calls of the sequence operators (csrc/binding.cpp)
+NATIVE_CALLS = ("fipa_window_attention", "fipa_window_attention_backward_workspace_size", "fipa_window_attention_backward",
+                "fipa_norm_residual", "fipa_norm_residual_backward_workspace_size", "fipa_norm_residual_backward",
+                "fipa_embedding", "fipa_embedding_backward_workspace_size", "fipa_embedding_backward")
 
 
 def library_path() -> str:
@@ -161,12 +166,17 @@ def load_library():
     lib.fipa_embedding_backward.restype = c_int
     lib.fipa_destroy.argtypes = [vp]
     lib.fipa_destroy.restype = c_int
+    global _native
+    try:
+        from . import _native
+    except ImportError as e:
+        raise RuntimeError(f"{e}; build it with `python -m protein_structure_models_b200.build`") from e
+    _native.bind({name: ctypes.cast(getattr(lib, name), vp).value for name in NATIVE_CALLS})
     _lib = lib
     return lib
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
-_BYTES = (torch.bool, torch.uint8)
 
 
 def make_dims(**kw) -> FipaDims:
@@ -177,13 +187,8 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
-    """Address of `stream`, or of the device's current stream, without building a Stream object."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+def _stream_address(stream: Optional[torch.cuda.Stream]):
+    return None if stream is None else stream.cuda_stream
 
 
 def _used_on(stream: Optional[torch.cuda.Stream], *tensors):
@@ -192,22 +197,6 @@ def _used_on(stream: Optional[torch.cuda.Stream], *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-
-
-class _OnDevice:
-    """torch.cuda.device(dev), at no cost when dev is current already."""
-    __slots__ = ("guard",)
-
-    def __init__(self, index):
-        self.guard = None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
 
 
 INPUT_KEYS = ("q", "k", "v", "q_points", "k_points", "v_points", "rotation", "translation",
@@ -221,6 +210,7 @@ class Fipa:
         self.lib = load_library()
         self.dtype = dtype
         self.torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self._code = BF16 if dtype == "bf16" else F32
         self.device = device
         h = ctypes.c_void_p()
         md = make_dims(**max_dims) if max_dims else None
@@ -421,33 +411,6 @@ class Fipa:
             ctypes.c_size_t(workspace.numel()), ctypes.c_void_p(st.cuda_stream)))
         return out
 
-    def _window_problem(self, q, k, v, window, sinks, mask, q_start, scale):
-        """Checks the tensors of a window attention call; returns its sizes and head views."""
-        at, td = self.device, self.torch_dtype
-        B, Nq, H, D = q.shape if q.dim() == 4 else (-1,) * 4
-        Bk, Nk, Hkv, Dk = k.shape if k.dim() == 4 else (-1,) * 4
-        Bv, Nv, Hv, Dv = v.shape if v.dim() == 4 else (-1,) * 4
-        heads = []
-        for t, width in ((q, D), (k, Dk), (v, Dv)):
-            if width < 0 or t.dtype != td or t.get_device() != at or not t.is_cuda:
-                raise ValueError(f"q, k, v: need {td} tensors [B, N, heads, width] on cuda:{at}")
-            st = t.stride()
-            if st[3] != 1 and width > 1:
-                raise ValueError("q, k, v: need a contiguous width")
-            heads.append(FipaHeads(t.data_ptr(), st[0], st[1], st[2]))
-        if Bk != B or Bv != B or Nv != Nk or Hv != Hkv or Dk != D:
-            raise ValueError("q [B,Nq,H,D], k [B,Nk,Hkv,D], v [B,Nk,Hkv,Dv] do not fit together")
-        if mask is not None and (mask.dtype not in _BYTES or mask.get_device() != at
-                                 or mask.shape != (B, Nk) or not mask.is_contiguous()):
-            raise ValueError(f"mask: need a contiguous bool/uint8 tensor [B, Nk] on cuda:{at}")
-        if q_start is not None and (q_start.dtype != torch.int32 or q_start.get_device() != at
-                                    or q_start.shape != (B,) or not q_start.is_contiguous()):
-            raise ValueError(f"q_start: need a contiguous int32 tensor [B] on cuda:{at}")
-        left, right = window
-        return FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, -1 if left is None else min(int(left), 0x7fffffff),
-                          -1 if right is None else min(int(right), 0x7fffffff), sinks,
-                          D ** -0.5 if scale is None and D > 0 else float(scale or 0.0)), heads
-
     def window_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: tuple, sinks: int = 0,
                          mask: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
                          scale: Optional[float] = None, want_lse: bool = False, out: Optional[dict] = None,
@@ -459,34 +422,21 @@ class Fipa:
         last Nq positions); a single token of a cached sequence is Nq = 1 with
         window = (left, 0) and its position in q_start.  Returns {"out": [B,Nq,H,Dv]}
         (+ "lse" [B,H,Nq] float32, which the backward needs)."""
-        w, hd = self._window_problem(q, k, v, window, sinks, mask, q_start, scale)
-        B, Nq, H = w.B, w.Nq, w.H
-        lse = None
+        left, right = window
+        o = lse = None
+        if out is not None:
+            o, lse = out.get("out"), out.get("lse")
+            if o is None:
+                raise ValueError("out: buffer missing")
+        r = _native.window(self.handle.value, self._code, self.device, q, k, v, -1 if left is None else left,
+                           -1 if right is None else right, sinks, mask, q_start, scale, want_lse, o, lse,
+                           _stream_address(stream))
+        if type(r) is int:
+            self._check(r)
         if out is None:
-            o = q.new_empty((B, Nq, H, w.Dv))
-            out = {"out": o}
-            if want_lse:
-                out["lse"] = lse = q.new_empty((B, H, Nq), dtype=torch.float32)
-            _used_on(stream, o, lse)
-        else:
-            self._check_buffers(out, {"out": ((B, Nq, H, w.Dv), q.dtype), "lse": ((B, H, Nq), torch.float32)}, q.device,
-                                ("out",))
-            o, lse = out["out"], out.get("lse")
-        st = self.lib.fipa_window_attention(self.handle, hd[0], hd[1], hd[2], _addr(mask), _addr(q_start), w,
-                                            o.data_ptr(), _addr(lse), _raw_stream(stream, self.device))
-        if st != FIPA_OK:
-            self._check(st)
+            out = {"out": r[0], "lse": r[1]} if want_lse else {"out": r[0]}
+            _used_on(stream, *r)
         return out
-
-    @staticmethod
-    def _check_buffers(bufs, want, dev, needed):
-        for name, (shape, dt) in want.items():
-            t = bufs.get(name)
-            if t is None:
-                if name in needed:
-                    raise ValueError(f"{name}: buffer missing")
-            elif t.shape != shape or t.dtype != dt or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{name}: need a contiguous {dt} tensor {tuple(shape)} on {dev}")
 
     def window_attention_backward(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
                                   lse: torch.Tensor, d_out: torch.Tensor, window: tuple, sinks: int = 0,
@@ -495,44 +445,33 @@ class Fipa:
                                   grads: Optional[dict] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
         """fipa_window_attention_backward: gradients "q", "k", "v" (handle's dtype) of
         <d_out, out>, from the forward's out and lse."""
-        w, hd = self._window_problem(q, k, v, window, sinks, mask, q_start, scale)
-        dev, at, td = q.device, self.device, q.dtype
-        B, Nq, H = w.B, w.Nq, w.H
-        o = (B, Nq, H, w.Dv)
-        for t, shape, dt in ((out, o, td), (d_out, o, td), (lse, (B, H, Nq), torch.float32)):
-            if t.shape != shape or t.dtype != dt or t.get_device() != at or not t.is_contiguous():
-                raise ValueError(f"out, d_out, lse: need contiguous tensors {o} and {(B, H, Nq)} (float32) on {dev}")
-        if grads is None:
-            dq, dk, dv = q.new_empty((B, Nq, H, w.D)), k.new_empty((B, w.Nk, w.Hkv, w.D)), v.new_empty((B, w.Nk, w.Hkv, w.Dv))
-            grads = {"q": dq, "k": dk, "v": dv}
-            _used_on(stream, dq, dk, dv)
-        else:
-            self._check_buffers(grads, {"q": ((B, Nq, H, w.D), td), "k": ((B, w.Nk, w.Hkv, w.D), td),
-                                        "v": ((B, w.Nk, w.Hkv, w.Dv), td)}, dev, ("q", "k", "v"))
-            dq, dk, dv = grads["q"], grads["k"], grads["v"]
-        if workspace is None:
-            workspace = q.new_empty(self._window_workspace(w), dtype=torch.uint8)
+        left, right = window
+        dq = dk = dv = None
+        if grads is not None:
+            dq, dk, dv = grads.get("q"), grads.get("k"), grads.get("v")
+            if dq is None or dk is None or dv is None:
+                raise ValueError("grads: need buffers q, k and v")
+        if workspace is None and stream is not None:
+            workspace = q.new_empty(self.window_attention_backward_workspace_size(q, k, v, window, sinks), dtype=torch.uint8)
             _used_on(stream, workspace)
-        elif workspace.get_device() != at or not workspace.is_contiguous():
-            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        st = self.lib.fipa_window_attention_backward(
-            self.handle, hd[0], hd[1], hd[2], _addr(mask), _addr(q_start), w, out.data_ptr(), lse.data_ptr(),
-            d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _raw_stream(stream, at))
-        if st != FIPA_OK:
-            self._check(st)
+        r = _native.window_backward(self.handle.value, self._code, self.device, q, k, v, -1 if left is None else left,
+                                    -1 if right is None else right, sinks, mask, q_start, scale, out, lse, d_out, dq, dk, dv,
+                                    workspace, _stream_address(stream))
+        if type(r) is int:
+            self._check(r)
+        if grads is None:
+            grads = {"q": r[0], "k": r[1], "v": r[2]}
+            _used_on(stream, *r)
         return grads
-
-    def _window_workspace(self, w) -> int:
-        n = ctypes.c_size_t()
-        self._check(self.lib.fipa_window_attention_backward_workspace_size(self.handle, ctypes.byref(w),
-                                                                           ctypes.byref(n)))
-        return int(n.value)
 
     def window_attention_backward_workspace_size(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                                  window: tuple, sinks: int = 0) -> int:
         """Bytes of workspace window_attention_backward needs for these tensors."""
-        return self._window_workspace(self._window_problem(q, k, v, window, sinks, None, None, None)[0])
+        (B, Nq, H, D), (_, Nk, Hkv, Dv) = q.shape, v.shape
+        left, right = (-1 if x is None else min(int(x), 0x7fffffff) for x in window)
+        w, n = FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, left, right, int(sinks), 1.0), ctypes.c_size_t()
+        self._check(self.lib.fipa_window_attention_backward_workspace_size(self.handle, w, n))
+        return int(n.value)
 
     BWD_STAGES = ("recompute", "prep", "q_side", "k_side", "chain")
 
@@ -634,45 +573,25 @@ def knn_distogram(translation: torch.Tensor, mask: torch.Tensor, k: int, edges: 
     return out
 
 
-def _need(name, t, shape, dtypes, dev):
-    if t.shape != shape or t.dtype not in dtypes or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous tensor {tuple(shape)} of {dtypes} on {dev}")
-
-
-def _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype):
-    """Checks the inputs of the junction; returns its dims, inputs, branch type and parameters."""
-    dev, shape, ts = s.device, s.shape, s.dtype
-    if dev.type != "cuda" or not shape:
-        raise ValueError("s: need a CUDA tensor [..., C]")
-    C = shape[-1]
-    tb = u.dtype if u is not None else (branch_dtype or ts)
-    if ts not in _FLOATS or tb not in _FLOATS:
-        raise ValueError("s, u, branch_dtype: float32 or bfloat16")
-    at, f32 = s.get_device(), torch.float32
-    if not s.is_contiguous() or (u is not None and (u.shape != shape or not u.is_contiguous() or u.get_device() != at)) or (
-            gate is not None and (gate.dtype != tb or gate.shape != shape or not gate.is_contiguous()
-                                  or gate.get_device() != at)):
-        raise ValueError(f"s, u, gate: need contiguous tensors {tuple(shape)} on {dev}, gate of the branch's type {tb}")
-    if mask is not None:
-        _need("mask", mask, shape[:-1], _BYTES, dev)
-    post_w, post_b = post or (None, None)
-    pre_w, pre_b = pre or (None, None)
-    par, line = (res_scale, post_w, post_b, pre_w, pre_b), shape[-1:]
-    for t in par:
-        if t is not None and (t.dtype != f32 or t.shape != line or not t.is_contiguous() or t.get_device() != at):
-            raise ValueError(f"{', '.join(NORM_PARAMS)}: need contiguous float32 tensors ({C},) on {dev}")
-    if norm != "layer" and norm != "rms":
-        raise ValueError('norm: "layer" or "rms"')
-    d = FipaNormDims(s.numel() // C if C else 0, C, F32 if ts == f32 else BF16, F32 if tb == f32 else BF16,
-                     0 if norm == "layer" else 1, eps)
-    i = FipaNormInputs(s.data_ptr(), _addr(u), _addr(gate), _addr(mask), _addr(res_scale), _addr(post_w), _addr(post_b),
-                       _addr(pre_w), _addr(pre_b))
-    return d, i, tb, par
-
-
 def _ok(st, what):
     if st != FIPA_OK:
         raise FipaError(st, what + " failed")
+
+
+def _norm_arguments(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype):
+    """The arguments of the compiled junction calls that both of them share."""
+    if norm not in _NORMS:
+        raise ValueError('norm: "layer" or "rms"')
+    if branch_dtype is not None and branch_dtype not in _FLOATS:
+        raise ValueError("branch_dtype: float32 or bfloat16")
+    post_w, post_b = post or _NONE
+    pre_w, pre_b = pre or _NONE
+    return (s, u, gate, res_scale, post_w, post_b, pre_w, pre_b, mask, _NORMS[norm], eps,
+            -1 if branch_dtype is None else F32 if branch_dtype == torch.float32 else BF16)
+
+
+_NORMS = {"layer": 0, "rms": 1}
+_NONE = (None, None)
 
 
 def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
@@ -687,30 +606,26 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
     parameters [C] float32, mask [...] bool/uint8 (0: padding, r = s and x = 0).
     Returns {"r" (with u), "x" (with pre)} and, with want_stats, "stats" [rows, 4] for the
     backward.  Without u, x = Norm(s, pre) in branch_dtype (default: that of s)."""
-    lib = _lib or load_library()
-    d, i, tb, _ = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
-    at = s.get_device()
+    if _native is None:
+        load_library()
+    a = _norm_arguments(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
     r = x = stats = None
-    with _OnDevice(at):
-        if out is None:
-            out = {}
-            if u is not None:
-                out["r"] = r = torch.empty_like(s)
-            if pre is not None:
-                out["x"] = x = torch.empty_like(s, dtype=tb) if u is None else torch.empty_like(u)
-            if want_stats:
-                out["stats"] = stats = s.new_empty((d.rows, 4), dtype=torch.float32)
-            _used_on(stream, r, x, stats)
-        else:
-            want = {"stats": ((d.rows, 4), torch.float32, False), "r": (s.shape, s.dtype, u is not None),
-                    "x": (s.shape, tb, pre is not None)}
-            for k, (sh, dt, needed) in want.items():
-                if k in out:
-                    _need(k, out[k], sh, (dt,), s.device)
-                elif needed:
-                    raise ValueError(f"{k}: buffer missing")
-            r, x, stats = out.get("r"), out.get("x"), out.get("stats")
-        _ok(lib.fipa_norm_residual(d, i, _addr(r), _addr(x), _addr(stats), _raw_stream(stream, at)), "fipa_norm_residual")
+    if out is not None:
+        r, x, stats = out.get("r"), out.get("x"), out.get("stats")
+        if (u is not None and r is None) or (pre is not None and x is None):
+            raise ValueError("out: buffer r or x missing")
+    res = _native.norm(*a, want_stats, out is not None, r, x, stats, _stream_address(stream))
+    if type(res) is int:
+        _ok(res, "fipa_norm_residual")
+    if out is None:
+        out = {}
+        if u is not None:
+            out["r"] = res[0]
+        if pre is not None:
+            out["x"] = res[1]
+        if want_stats:
+            out["stats"] = res[2]
+        _used_on(stream, *res)
     return out
 
 
@@ -725,65 +640,38 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
     every input that was given, keyed "s", "u", "gate", "res_scale", "post_w", "post_b",
     "pre_w", "pre_b" (None where there was no input).  `grads`, if given, holds the buffers
     of the gradients that are wanted."""
-    lib = _lib or load_library()
-    d, i, tb, par = _norm_problem(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
-    dev, at = s.device, s.get_device()
-    _need("stats", stats, (d.rows, 4), (torch.float32,), dev)
-    if d_r is not None:
-        _need("d_r", d_r, s.shape, (s.dtype,), dev)
-    if d_x is not None:
-        _need("d_x", d_x, s.shape, (tb,), dev)
-    with _OnDevice(at):
-        if grads is None:
-            grads = {"s": torch.empty_like(s), "u": None if u is None else torch.empty_like(u),
-                     "gate": None if gate is None else torch.empty_like(gate)}
-            lines = s.new_empty((5, d.C), dtype=torch.float32).unbind(0)       # the parameters' gradients side by side
-            for k, t, line in zip(NORM_PARAMS, par, lines):
-                grads[k] = None if t is None else line
-            _used_on(stream, grads["s"], grads["u"], grads["gate"], lines[0])
-        else:
-            have = {"s": s, "u": u, "gate": gate, **dict(zip(NORM_PARAMS, par))}
-            for k, t in grads.items():
-                if t is not None:
-                    if have.get(k) is None:
-                        raise ValueError(f"{k}: a gradient of an input that was not given")
-                    _need(k, t, have[k].shape, (have[k].dtype,), dev)
-        if workspace is None:
-            n = ctypes.c_size_t()
-            _ok(lib.fipa_norm_residual_backward_workspace_size(d, n), "fipa_norm_residual_backward_workspace_size")
-            workspace = s.new_empty(n.value, dtype=torch.uint8)
-            _used_on(stream, workspace)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        g = FipaNormGrads(*[_addr(grads.get(f)) for f in NORM_GRADS])
-        _ok(lib.fipa_norm_residual_backward(d, i, stats.data_ptr(), _addr(d_r), _addr(d_x), g, workspace.data_ptr(),
-                                            workspace.numel() * workspace.element_size(), _raw_stream(stream, at)),
-            "fipa_norm_residual_backward")
+    lib = load_library()
+    a = _norm_arguments(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
+    if workspace is None and stream is not None:
+        d, n = FipaNormDims(s.numel() // max(1, s.shape[-1]), s.shape[-1], F32, F32, 0, 1.0), ctypes.c_size_t()
+        _ok(lib.fipa_norm_residual_backward_workspace_size(d, n), "fipa_norm_residual_backward_workspace_size")
+        workspace = s.new_empty(n.value, dtype=torch.uint8)
+        _used_on(stream, workspace)
+    given = _NO_GRADS if grads is None else [grads.get(f) for f in NORM_GRADS]
+    res = _native.norm_backward(*a, stats, d_r, d_x, grads is not None, *given, workspace, _stream_address(stream))
+    if type(res) is int:
+        _ok(res, "fipa_norm_residual_backward")
+    if grads is None:
+        grads = dict(zip(NORM_GRADS, res))
+        _used_on(stream, *res)
     return grads
+
+
+_NO_GRADS = (None,) * 8
 
 
 def embedding(idx: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: Optional[dict] = None,
               stream: Optional[torch.cuda.Stream] = None) -> dict:
     """fipa_embedding: {"out": scale * table[idx]} for idx [...] int32 and table [V, C]
     float32/bfloat16; an index outside [0, V) gives a zero row."""
-    lib, at, td = _lib or load_library(), table.get_device(), table.dtype
-    if not table.is_cuda or table.dim() != 2 or td not in _FLOATS or not table.is_contiguous():
-        raise ValueError("table: need a contiguous float32 or bfloat16 CUDA tensor [V, C]")
-    if idx.dtype != torch.int32 or idx.get_device() != at or not idx.is_contiguous():
-        raise ValueError(f"idx: need a contiguous int32 tensor on cuda:{at}")
-    V, C = table.shape
-    with _OnDevice(at):
-        if out is None:
-            o = table.new_empty((*idx.shape, C))
-            out = {"out": o}
-            _used_on(stream, o)
-        else:
-            o = out["out"]
-            _need("out", o, (*idx.shape, C), (td,), table.device)
-        st = lib.fipa_embedding(F32 if td == torch.float32 else BF16, idx.data_ptr(), table.data_ptr(), idx.numel(), V, C,
-                                scale, o.data_ptr(), _raw_stream(stream, at))
-    if st != FIPA_OK:
-        _ok(st, "fipa_embedding")
+    if _native is None:
+        load_library()
+    r = _native.embedding(idx, table, scale, None if out is None else out["out"], _stream_address(stream))
+    if type(r) is int:
+        _ok(r, "fipa_embedding")
+    if out is None:
+        out = {"out": r[0]}
+        _used_on(stream, r[0])
     return out
 
 
@@ -799,32 +687,18 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
                        workspace: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
                        stream: Optional[torch.cuda.Stream] = None) -> dict:
     """fipa_embedding_backward: {"table": [V, C] float32}, the gradient of <d_out, out>."""
-    lib, at, td = _lib or load_library(), d_out.get_device(), d_out.dtype
-    if not d_out.is_cuda or not d_out.dim() or td not in _FLOATS or not d_out.is_contiguous():
-        raise ValueError("d_out: need a contiguous float32 or bfloat16 CUDA tensor [..., C]")
-    if idx.dtype != torch.int32 or idx.get_device() != at or not idx.is_contiguous() or idx.shape != d_out.shape[:-1]:
-        raise ValueError(f"idx: need a contiguous int32 tensor {tuple(d_out.shape[:-1])} on cuda:{at}")
-    C, T = d_out.shape[-1], idx.numel()
-    with _OnDevice(at):
-        if grads is None:
-            g = d_out.new_empty((V, C), dtype=torch.float32)
-            grads = {"table": g}
-            _used_on(stream, g)
-        else:
-            g = grads["table"]
-            _need("table", g, (V, C), (torch.float32,), d_out.device)
-        if workspace is None:
-            n = ctypes.c_size_t()
-            _ok(lib.fipa_embedding_backward_workspace_size(T, V, C, n), "fipa_embedding_backward_workspace_size")
-            workspace = d_out.new_empty(n.value, dtype=torch.uint8)
-            _used_on(stream, workspace)
-        elif workspace.get_device() != at or not workspace.is_contiguous():
-            raise ValueError(f"workspace: need a contiguous tensor on cuda:{at}")
-        st = lib.fipa_embedding_backward(F32 if td == torch.float32 else BF16, idx.data_ptr(), d_out.data_ptr(), T, V, C,
-                                         scale, g.data_ptr(), workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), _raw_stream(stream, at))
-    if st != FIPA_OK:
-        _ok(st, "fipa_embedding_backward")
+    if _native is None:
+        load_library()
+    if workspace is None and stream is not None:
+        workspace = d_out.new_empty(embedding_backward_workspace_size(idx.numel(), V, d_out.shape[-1]), dtype=torch.uint8)
+        _used_on(stream, workspace)
+    r = _native.embedding_backward(idx, d_out, V, scale, None if grads is None else grads["table"], workspace,
+                                   _stream_address(stream))
+    if type(r) is int:
+        _ok(r, "fipa_embedding_backward")
+    if grads is None:
+        grads = {"table": r[0]}
+        _used_on(stream, r[0])
     return grads
 
 
