@@ -383,19 +383,29 @@ typedef struct {
  *   out      [B,Nq,H,Dv] contiguous, every row written
  *   lse      [B,H,Nq] or NULL: natural-log logsumexp of the visible scores
  * out and lse must not overlap the inputs.  FIPA_ERR_UNSUPPORTED for D or Dv > 128
- * or sinks > 128.  Allocates nothing; runs on `stream`. */
+ * or sinks > 128.  Allocates nothing; runs on `stream`.  workspace >=
+ * fipa_window_attention_workspace_size() bytes, 256-byte aligned: room for copies
+ * of tensors whose addresses, strides or widths are not multiples of 16 bytes;
+ * 0 bytes (workspace may be NULL) where they are, and for bfloat16 calls of few
+ * queries, which read them as they are. */
+fipa_status fipa_window_attention_workspace_size(const fipa_handle* h, const fipa_heads* q,
+                                                 const fipa_heads* k, const fipa_heads* v,
+                                                 const fipa_window* win, size_t* bytes);
 fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
                                   const fipa_heads* v, const uint8_t* mask, const int32_t* q_start,
-                                  const fipa_window* win, void* out, float* lse, void* stream);
+                                  const fipa_window* win, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /* Gradients of <d_out, out>: d_q [B,Nq,H,D], d_k [B,Nk,Hkv,D] (summed over the
  * heads of a group), d_v [B,Nk,Hkv,Dv], contiguous, every element written, none of
  * them overlapping the inputs.
- * out and lse are those of the forward call; workspace >=
+ * out and lse are those of the forward call.  d_out must be 16-byte aligned where
+ * its rows are multiples of 16 bytes.  workspace >=
  * fipa_window_attention_backward_workspace_size() bytes, 256-byte aligned.
  * Deterministic: every sum is taken in a fixed order. */
-fipa_status fipa_window_attention_backward_workspace_size(const fipa_handle* h, const fipa_window* win,
-                                                          size_t* bytes);
+fipa_status fipa_window_attention_backward_workspace_size(const fipa_handle* h, const fipa_heads* q,
+                                                          const fipa_heads* k, const fipa_heads* v,
+                                                          const fipa_window* win, size_t* bytes);
 fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
                                            const fipa_heads* v, const uint8_t* mask,
                                            const int32_t* q_start, const fipa_window* win,

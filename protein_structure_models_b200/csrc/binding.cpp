@@ -22,8 +22,9 @@ namespace {
 
 struct Entry {
   decltype(&fipa_window_attention) window;
-  decltype(&fipa_window_attention_backward_workspace_size) window_size;
+  decltype(&fipa_window_attention_workspace_size) window_size;
   decltype(&fipa_window_attention_backward) window_backward;
+  decltype(&fipa_window_attention_backward_workspace_size) window_backward_size;
   decltype(&fipa_norm_residual) norm;
   decltype(&fipa_norm_residual_backward_workspace_size) norm_size;
   decltype(&fipa_norm_residual_backward) norm_backward;
@@ -183,7 +184,7 @@ Window window_args(Args& a) {
   p.w.scale = a.none() ? (D > 0 ? 1.0 / std::sqrt((double)D) : 0.0) : a.real();
   return p;
 }
-// ..., want_lse, out, lse, stream -> out, lse
+// ..., want_lse, out, lse, workspace, stream -> out, lse
 PyObject* window(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Args a{argv, n};
@@ -198,8 +199,15 @@ PyObject* window(PyObject*, PyObject* const* argv, Py_ssize_t n) {
       out = make(p.q, {w.B, w.Nq, w.H, w.Dv}, p.type);
       if (want) lse = make(p.q, {w.B, w.H, w.Nq}, at::kFloat);
     }
+    Tensor ws = a.optional();
+    size_t size = 0;
+    if (!ws.defined()) {
+      const fipa_status st = entry.window_size(p.h, &p.hq, &p.hk, &p.hv, &w, &size);
+      if (st != FIPA_OK) return PyLong_FromLong(st);
+    }
+    if (ws.defined() || size > 0) ws = room(ws, p.q, size, p.dev);
     return answer(entry.window(p.h, &p.hq, &p.hk, &p.hv, static_cast<const uint8_t*>(at_of(p.mask)), static_cast<const int32_t*>(at_of(p.start)),
-                               &w, out.data_ptr(), static_cast<float*>(at_of(lse)), a.stream(p.dev)),
+                               &w, out.data_ptr(), static_cast<float*>(at_of(lse)), at_of(ws), ws.defined() ? ws.nbytes() : 0, a.stream(p.dev)),
                   out, lse);
   });
 }
@@ -223,7 +231,7 @@ PyObject* window_backward(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     Tensor ws = a.optional();
     size_t size = 0;
     if (!ws.defined()) {
-      const fipa_status st = entry.window_size(p.h, &w, &size);
+      const fipa_status st = entry.window_backward_size(p.h, &p.hq, &p.hk, &p.hv, &w, &size);
       if (st != FIPA_OK) return PyLong_FromLong(st);
     }
     ws = room(ws, p.q, size, p.dev);
@@ -383,8 +391,9 @@ PyObject* bind(PyObject*, PyObject* dict) {
 #define FIPA_BIND(field, name)                                          \
   if ((entry.field = reinterpret_cast<decltype(entry.field)>(get(#name))) == nullptr) return nullptr;
   FIPA_BIND(window, fipa_window_attention)
-  FIPA_BIND(window_size, fipa_window_attention_backward_workspace_size)
+  FIPA_BIND(window_size, fipa_window_attention_workspace_size)
   FIPA_BIND(window_backward, fipa_window_attention_backward)
+  FIPA_BIND(window_backward_size, fipa_window_attention_backward_workspace_size)
   FIPA_BIND(norm, fipa_norm_residual)
   FIPA_BIND(norm_size, fipa_norm_residual_backward_workspace_size)
   FIPA_BIND(norm_backward, fipa_norm_residual_backward)

@@ -842,19 +842,63 @@ fipa_status window_inputs(fipa_handle* h, const fipa_heads* q, const fipa_heads*
   return FIPA_OK;
 }
 
-// Workspace of the backward: delta [B,H,Nq], then the sinks' partial sums, for
-// the key tile of whichever kernels take the call.
-size_t window_bwd_bytes(const fipa::WinArgs& a) {
-  const size_t x = fipa::win_sink_plan(a, fipa::kWinTile).part_floats, y = fipa::win_sink_plan(a, fipa::kWinTcRows).part_floats;
-  const size_t delta = ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256;
-  return delta + (x > y ? x : y) * sizeof(float);
+// Workspace of a call.  Backward: delta [B,H,Nq], then the sinks' partial sums,
+// for the key tile of whichever kernels take the call and widths rounded up; last,
+// forward as well, the copies with such widths.
+struct WindowRoom {
+  size_t part, pad, all;                  // offsets, bytes
+};
+fipa_status window_room(fipa_handle* h, const fipa::WinArgs& a, bool backward, WindowRoom* r) {
+  const int es = h->dtype == FIPA_F32 ? 4 : 2;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  *r = WindowRoom{0, 0, 0};
+  if (backward) {
+    fipa::WinArgs p = a;
+    p.D = (a.D + 7) / 8 * 8;
+    p.Dv = (a.Dv + 7) / 8 * 8;
+    const size_t x = fipa::win_sink_plan(p, fipa::kWinTile).part_floats, y = fipa::win_sink_plan(p, fipa::kWinTcRows).part_floats;
+    r->part = up((size_t)a.B * a.H * a.Nq * sizeof(float));
+    r->pad = r->part + up((x > y ? x : y) * sizeof(float));
+  }
+  const size_t pad = fipa::win_pad_bytes(a, es, backward);
+  if (pad > 0 && ((int64_t)a.B * a.Nq * a.H > 0x7fffffff || (int64_t)a.B * a.Nk * a.Hkv > 0x7fffffff))
+    return fail(h, FIPA_ERR_UNSUPPORTED, "too many rows off 16-byte boundaries");
+  r->all = r->pad + pad;
+  return FIPA_OK;
+}
+fipa_status window_size(const fipa_handle* hc, const fipa_heads* q, const fipa_heads* k, const fipa_heads* v, const fipa_window* win,
+                        bool backward, size_t* bytes) {
+  fipa_handle* h = const_cast<fipa_handle*>(hc);
+  if (h == nullptr || bytes == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, "null argument");
+  fipa::WinArgs a;
+  WindowRoom r;
+  fipa_status st;
+  if ((st = window_args(h, win, &a)) != FIPA_OK) return st;
+  if ((st = window_inputs(h, q, k, v, nullptr, nullptr, &a)) != FIPA_OK) return st;
+  if ((st = window_room(h, a, backward, &r)) != FIPA_OK) return st;
+  *bytes = r.all;
+  return FIPA_OK;
+}
+fipa_status window_workspace(fipa_handle* h, fipa::WinArgs* a, bool backward, void* workspace, size_t bytes) {
+  WindowRoom r;
+  const fipa_status st = window_room(h, *a, backward, &r);
+  if (st != FIPA_OK) return st;
+  if (r.all > 0 && (workspace == nullptr || bytes < r.all))
+    return fail(h, FIPA_ERR_WORKSPACE, "workspace needs " + std::to_string(r.all) + " bytes");
+  if (!aligned(workspace, 256)) return fail(h, FIPA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a->delta = reinterpret_cast<float*>(w);
+  a->part = reinterpret_cast<float*>(w + r.part);
+  a->pad = w + r.pad;
+  return FIPA_OK;
 }
 
 }  // namespace
 
 FIPA_API fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
                                            const fipa_heads* v, const uint8_t* mask, const int32_t* q_start,
-                                           const fipa_window* win, void* out, float* lse, void* stream) {
+                                           const fipa_window* win, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
   if (h == nullptr) return FIPA_ERR_INVALID_ARG;
   h->last_error.clear();
   fipa::WinArgs a;
@@ -866,23 +910,21 @@ FIPA_API fipa_status fipa_window_attention(fipa_handle* h, const fipa_heads* q, 
     return fail(h, FIPA_ERR_INVALID_ARG, "output pointer misaligned");
   a.out = out;
   a.lse = lse;
+  if ((st = window_workspace(h, &a, false, workspace, workspace_bytes)) != FIPA_OK) return st;
   DeviceGuard g(h->device);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_f32(a, false, s) : fipa::launch_win_fwd(a, s);
+  const cudaError_t e = fipa::launch_win(a, h->dtype == FIPA_F32 ? 4 : 2, false, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention launch", e);
 }
 
-FIPA_API fipa_status fipa_window_attention_backward_workspace_size(const fipa_handle* hc, const fipa_window* win,
-                                                                   size_t* bytes) {
-  fipa_handle* h = const_cast<fipa_handle*>(hc);
-  if (h == nullptr || bytes == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, "null argument");
-  fipa::WinArgs a;
-  const fipa_status st = window_args(h, win, &a);
-  if (st != FIPA_OK) return st;
-  *bytes = window_bwd_bytes(a);
-  return FIPA_OK;
+FIPA_API fipa_status fipa_window_attention_workspace_size(const fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
+                                                          const fipa_heads* v, const fipa_window* win, size_t* bytes) {
+  return window_size(h, q, k, v, win, false, bytes);
 }
-
+FIPA_API fipa_status fipa_window_attention_backward_workspace_size(const fipa_handle* h, const fipa_heads* q,
+                                                                   const fipa_heads* k, const fipa_heads* v,
+                                                                   const fipa_window* win, size_t* bytes) {
+  return window_size(h, q, k, v, win, true, bytes);
+}
 FIPA_API fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_heads* q, const fipa_heads* k,
                                                     const fipa_heads* v, const uint8_t* mask, const int32_t* q_start,
                                                     const fipa_window* win, const void* out, const float* lse,
@@ -901,21 +943,15 @@ FIPA_API fipa_status fipa_window_attention_backward(fipa_handle* h, const fipa_h
     if (req[i] == nullptr) return fail(h, FIPA_ERR_INVALID_ARG, std::string(names[i]) + " is NULL");
     if (!aligned(req[i], i == 1 ? 4 : es)) return fail(h, FIPA_ERR_INVALID_ARG, std::string(names[i]) + " is misaligned");
   }
-  const size_t need = window_bwd_bytes(a);
-  if (workspace == nullptr || workspace_bytes < need)
-    return fail(h, FIPA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
-  if (!aligned(workspace, 256)) return fail(h, FIPA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (a.Dv * es % 16 == 0 && !aligned(d_out, 16)) return fail(h, FIPA_ERR_INVALID_ARG, "d_out must be 16-byte aligned where its rows are multiples of 16 bytes");
+  if ((st = window_workspace(h, &a, true, workspace, workspace_bytes)) != FIPA_OK) return st;
   a.out = const_cast<void*>(out);
   a.lse = const_cast<float*>(lse);
   a.d_out = d_out;
   a.d_q = d_q;
   a.d_k = d_k;
   a.d_v = d_v;
-  a.delta = static_cast<float*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                    ((size_t)a.B * a.H * a.Nq * sizeof(float) + 255) / 256 * 256);
   DeviceGuard g(h->device);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = h->dtype == FIPA_F32 ? fipa::launch_win_f32(a, true, s) : fipa::launch_win_bwd(a, s);
+  const cudaError_t e = fipa::launch_win(a, (int)es, true, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FIPA_OK : cuda_fail(h, "window attention backward launch", e);
 }

@@ -39,11 +39,11 @@ struct WinArgs {
   int sink_pos;                      // first position that belongs to them
   int* status;
   unsigned long long timeout_ns;
+  void* pad;                         // workspace of window_pad.cu
 };
 
 constexpr int kWinMaxD = 128;
 constexpr int kWinMaxSinks = 128;
-constexpr int kWinStepRows = 32;       // up to here columns are split instead of rows (window_step.cu)
 
 // The gradient of a sink key sums over every later query, which one CTA would
 // walk alone: the queries beyond the window of the key tiles that hold sinks
@@ -77,11 +77,37 @@ inline size_t win_short_smem(const WinArgs& a, int dp, bool backward) {
   const size_t F = ((size_t)a.Nq * a.G + 15) / 16 * 16, K = ((size_t)a.Nk + 31) / 32 * 32;
   return (2 * K + (backward ? 2 : 1) * F) * (dp + 8) * 2;
 }
-
-// Whether q, k and v can be read 16 bytes at a time.
+// Whether a CTA takes a whole sequence: two of them fit an SM, and there are that many.
+//   64 x 128 x 8 heads of 16, window 63: 11.7 / 21 us against 14.0 / 38; 8 x 256 x 8: 14.5 / 27 against 8.9 / 24
+inline bool win_short_takes(const WinArgs& a, bool backward) {
+  const int w = a.D > a.Dv ? a.D : a.Dv;
+  if (w > 64 || a.Nk > kWinShortRows || (long long)a.Nq * a.G > kWinShortRows || (long long)a.B * a.Hkv < 296) return false;
+  return win_short_smem(a, w <= 16 ? 16 : (w <= 32 ? 32 : 64), backward) <= 100 * 1024;
+}
+// Whether bfloat16 q, k and v can be read 16 bytes at a time.
 inline bool win_vec(const WinArgs& a) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
   return ((p & 15) | ((a.qb | a.qn | a.qh | a.kb | a.kn | a.kh | a.vb | a.vn | a.vh | a.D | a.Dv) & 7)) == 0;
+}
+// Whether the columns of a forward call are split over warps and CTAs instead of
+// its rows (window_step.cu).  That pays for a unit of 16 rows with many columns,
+// while there are few units, or few rows in each; us, split against row tiles:
+//   units  rows each  columns   width 32     64          128
+//       8          1      256   6.7 / 10.1   6.4 / 13.4  7.1 / 18.9
+//       8         16      128   9.9 / 6.8    10.5 / 8.9  10.9 / 12.3
+//      60         16      200   9.6 / 9.8    10.3 / 12.8 13.0 / 17.7
+//     400          1      190   7.6 / 8.3    9.1 / 11.1  16.4 / 30.5
+//     400         16      384   20 / 13      26 / 21     44 / 56
+//     600         16     1015   54 / 66      84 / 92     116 / 197
+//     800         16      256   36 / 10      43 / 15     59 / 40
+// Tensors off 16-byte boundaries are read as they are where the copies that row
+// tiles need would cost more (10 rows of 110 channels, 31 of 3582 keys: 18 against 42).
+inline bool win_step_takes(const WinArgs& a) {
+  const long long F = (long long)a.Nq * a.G, units = (long long)a.B * a.Hkv * ((F + 15) / 16);
+  if (!win_vec(a) && (F <= 4 || (F <= 16 && (a.Nk > 256 || units <= 148)))) return true;
+  const long long cols = (long long)a.left + a.Nq + a.right + a.sinks, n = cols < a.Nk ? cols : a.Nk;
+  if (units <= 148 && F <= 128) return n >= (F <= 4 ? 128 : 160);
+  return (F <= 4 && n >= 128) || (F <= 16 && n >= (a.D > 64 || a.Dv > 64 ? 256 : 768)) || (F <= 32 && n >= 1536);
 }
 
 #ifdef __CUDACC__
@@ -132,6 +158,8 @@ __device__ __forceinline__ bool win_alive(const WinArgs& a, int b, int p) {
 }
 #endif
 
+size_t win_pad_bytes(const WinArgs& a, int es, bool backward);           // workspace of launch_win at a.pad; es: bytes of an element
+cudaError_t launch_win(const WinArgs& a, int es, bool backward, cudaStream_t s);  // any widths and strides, by the following:
 cudaError_t launch_win_f32(const WinArgs& a, bool backward, cudaStream_t s);     // float32 tensors
 cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s);            // bfloat16 tensors: one of the following
 cudaError_t launch_win_bwd(const WinArgs& a, cudaStream_t s);

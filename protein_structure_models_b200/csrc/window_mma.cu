@@ -47,47 +47,25 @@ __device__ __forceinline__ void column_bits(uint32_t* bits, const WinArgs& a, in
 }
 
 // Rows f0 .. f0+63 (those below fh) of the queries and of dO, and columns u0 .. u0+63 of keys and values.
-template <int DP, bool VEC>
+template <int DP>
 __device__ __forceinline__ void load_queries(bf16* Qs, bf16* Os, const WinArgs& a, int b, int q0, const Src& q, const Src& g, int f0, int fh) {
-  if (VEC) {
-    constexpr int step = kThreads / (DP / 8);
-    const int first = threadIdx.x / (DP / 8);
-    copy_padded<DP>(Qs, Os, a.D, a.Dv, walk_queries(a, q, g, min(f0 + first, fh - 1), step), first, step, T, fh - f0,
-                    [&](int i) { return win_alive(a, b, q0 + i); });
-  } else {
-    auto rows = [&](const Src& s) {
-      return [&](int r) -> const bf16* {
-        const int f = f0 + r, i = f / a.G;
-        return f < fh && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
-      };
-    };
-    load_tile<DP, VEC>(Qs, q, T, threadIdx.x, kThreads, rows(q));
-    load_tile<DP, VEC>(Os, g, T, threadIdx.x, kThreads, rows(g));
-  }
+  constexpr int step = kThreads / (DP / 8);
+  const int first = threadIdx.x / (DP / 8);
+  copy_padded<DP>(Qs, Os, a.D, a.Dv, walk_queries(a, q, g, min(f0 + first, fh - 1), step), first, step, T, fh - f0,
+                  [&](int i) { return win_alive(a, b, q0 + i); });
 }
-template <int DP, bool VEC>
+template <int DP>
 __device__ __forceinline__ void load_keys(bf16* Ks, bf16* Vs, const WinArgs& a, int b, const Src& k, const Src& v, const WinCols& c, int u0) {
   auto valid = [&](int j) { return a.mask == nullptr || a.mask[(long long)b * a.Nk + j] != 0; };
-  if (VEC) {
-    constexpr int step = kThreads / (DP / 8);
-    int first = threadIdx.x / (DP / 8);
-    const int ns = min(max(c.s - u0, 0), T);                  // sinks first, then the window; a tile may hold the seam
-    if (ns > 0) copy_padded<DP>(Ks, Vs, a.D, a.Dv, walk_keys(k, v, min(u0 + first, a.Nk - 1), step), first, step, ns, ns, valid);
-    while (first < ns) first += step;
-    if (first < T) copy_padded<DP>(Ks, Vs, a.D, a.Dv, walk_keys(k, v, min(c.key(u0 + first), a.Nk - 1), step), first, step, T, c.n - u0, valid);
-  } else {
-    auto keyed = [&](const Src& s) {
-      return [&](int r) -> const bf16* {
-        const int u = u0 + r;
-        return u < c.n && valid(c.key(u)) ? s.p + c.key(u) * s.sn : nullptr;
-      };
-    };
-    load_tile<DP, VEC>(Ks, k, T, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP, VEC>(Vs, v, T, threadIdx.x, kThreads, keyed(v));
-  }
+  constexpr int step = kThreads / (DP / 8);
+  int first = threadIdx.x / (DP / 8);
+  const int ns = min(max(c.s - u0, 0), T);                  // sinks first, then the window; a tile may hold the seam
+  if (ns > 0) copy_padded<DP>(Ks, Vs, a.D, a.Dv, walk_keys(k, v, min(u0 + first, a.Nk - 1), step), first, step, ns, ns, valid);
+  while (first < ns) first += step;
+  if (first < T) copy_padded<DP>(Ks, Vs, a.D, a.Dv, walk_keys(k, v, min(c.key(u0 + first), a.Nk - 1), step), first, step, T, c.n - u0, valid);
 }
 
-template <int DP, bool VEC>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Qs = reinterpret_cast<bf16*>(smem);
@@ -113,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
   const Reach rc = reach(a, c, q0, f0 + 16 * warp, f1);
   auto load = [&](int t) {
     const int st = t & 1, u0 = t * T;
-    load_keys<DP, VEC>(Ks + st * kElems<DP>, Vs + st * kElems<DP>, a, b, k, v, c, u0);
+    load_keys<DP>(Ks + st * kElems<DP>, Vs + st * kElems<DP>, a, b, k, v, c, u0);
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -126,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
   uint32_t qf[DP / 16][4];
   const float sc = a.scale * kLog2e;
   if (ntile > 0) {
-    load_tile<DP, VEC>(Qs, q, T, threadIdx.x, kThreads, [&](int r) -> const bf16* {
+    load_tile<DP>(Qs, q, T, threadIdx.x, kThreads, [&](int r) -> const bf16* {
       const int f = f0 + r, i = f / a.G;
       return f < f1 && win_alive(a, b, q0 + i) ? q.p + i * q.sn + (f - i * a.G) * q.sh : nullptr;
     });
@@ -288,7 +266,7 @@ __device__ __forceinline__ void row_delta(float* sdelta, const bf16* dOs, const 
   }
 }
 
-template <int DP, bool VEC>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* Qs = reinterpret_cast<bf16*>(smem);
@@ -317,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
   const Reach rc = reach(a, c, q0, f0 + 16 * warp, f1);
   auto load = [&](int t) {
     const int st = t & 1, u0 = t * T;
-    load_keys<DP, VEC>(Ks + st * kElems<DP>, Vs + st * kElems<DP>, a, b, k, v, c, u0);
+    load_keys<DP>(Ks + st * kElems<DP>, Vs + st * kElems<DP>, a, b, k, v, c, u0);
     column_bits(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -329,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
     for (int e = 0; e < 4; ++e) acc[n][e] = avg[n][e] = 0.f;
   const float sc = a.scale * kLog2e;
   if (ntile > 0) {
-    load_queries<DP, VEC>(Qs, Os, a, b, q0, q, g_, f0, f1);
+    load_queries<DP>(Qs, Os, a, b, q0, q, g_, f0, f1);
     load(0);
     cp_wait<0>();
     __syncthreads();
@@ -430,7 +408,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
 // dk and dv.  SINK false: of one key tile over the rows of its window, a warp 16
 // keys.  SINK true: of 16 keys that hold sinks, over one chunk of the rows beyond
 // the window; the warps take every fourth 16 rows and are added in order.
-template <int DP, bool VEC, bool SINK>
+template <int DP, bool SINK>
 __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a) {
   constexpr int KR = SINK ? 16 : T;                     // keys of the CTA
   extern __shared__ __align__(16) uint8_t smem[];
@@ -472,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
   int rp = 0;
   auto load = [&](int t) {
     const int st = t & 1, f0 = fl + t * T;
-    load_queries<DP, VEC>(Qs + st * kElems<DP>, Os + st * kElems<DP>, a, b, q0, q, g_, f0, fh);
+    load_queries<DP>(Qs + st * kElems<DP>, Os + st * kElems<DP>, a, b, q0, q, g_, f0, fh);
     cp_async_commit();
     // a row's lse, delta and position wait in registers until the tile before is done
     if (threadIdx.x < T) {
@@ -505,8 +483,8 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
     auto keyed = [&](const Src& s) {
       return [&](int r) -> const bf16* { return j0 + r <= j1 && win_alive(a, b, j0 + r) ? s.p + (j0 + r) * s.sn : nullptr; };
     };
-    load_tile<DP, VEC>(Ks, k, KR, threadIdx.x, kThreads, keyed(k));
-    load_tile<DP, VEC>(Vs, v, KR, threadIdx.x, kThreads, keyed(v));
+    load_tile<DP>(Ks, k, KR, threadIdx.x, kThreads, keyed(k));
+    load_tile<DP>(Vs, v, KR, threadIdx.x, kThreads, keyed(v));
     load(0);
     put(0);
   }
@@ -656,54 +634,45 @@ __global__ void __launch_bounds__(1024) win_sink_reduce_kernel(const WinArgs a) 
   else stf(static_cast<E*>(a.d_v) + r * a.Dv + (d - a.D), x);
 }
 
-template <int DP, bool VEC>
+template <int DP>
 cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
   const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
-  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_fwd_mma_kernel<DP, VEC>));
+  cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_fwd_mma_kernel<DP>));
   if (e != cudaSuccess) return e;
-  win_fwd_mma_kernel<DP, VEC><<<(unsigned)grid, kThreads, 5 * kElems<DP> * sizeof(bf16), s>>>(a);
+  win_fwd_mma_kernel<DP><<<(unsigned)grid, kThreads, 5 * kElems<DP> * sizeof(bf16), s>>>(a);
   return cudaGetLastError();
 }
 
-template <int DP, bool VEC>
+template <int DP>
 cudaError_t bwd_q(const WinArgs& a, cudaStream_t s) {
-  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP, VEC>));
+  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_q_mma_kernel<DP>));
   if (e != cudaSuccess) return e;
   const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
-  win_bwd_q_mma_kernel<DP, VEC><<<(unsigned)grid, kThreads, 6 * kElems<DP> * sizeof(bf16), s>>>(a);
+  win_bwd_q_mma_kernel<DP><<<(unsigned)grid, kThreads, 6 * kElems<DP> * sizeof(bf16), s>>>(a);
   return cudaGetLastError();
 }
-template <int DP, bool VEC, bool SINK>
+template <int DP, bool SINK>
 cudaError_t bwd_k(const WinArgs& a, cudaStream_t s) {
-  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP, VEC, SINK>));
+  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_bwd_k_mma_kernel<DP, SINK>));
   if (e != cudaSuccess) return e;
   const long long grid = (long long)a.B * a.Hkv * (SINK ? (long long)(a.sinks + 15) / 16 * a.nchunk : (a.Nk + T - 1) / T);
   const size_t smem = (size_t)(2 * (SINK ? 16 : T) + 4 * T) * Tile<DP>::ld * sizeof(bf16);
-  win_bwd_k_mma_kernel<DP, VEC, SINK><<<(unsigned)grid, kThreads, smem, s>>>(a);
+  win_bwd_k_mma_kernel<DP, SINK><<<(unsigned)grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
-template <int DP, bool VEC>
+template <int DP>
 cudaError_t bwd(const WinArgs& a, bool tc, cudaStream_t s) {
-  cudaError_t e = tc ? launch_win_bwd_q_tc(a, s) : bwd_q<DP, VEC>(a, s);
-  if (e == cudaSuccess) e = tc ? launch_win_bwd_k_tc(a, s) : bwd_k<DP, VEC, false>(a, s);
-  if (e == cudaSuccess && a.nchunk > 0) e = bwd_k<DP, VEC, true>(a, s);
+  cudaError_t e = tc ? launch_win_bwd_q_tc(a, s) : bwd_q<DP>(a, s);
+  if (e == cudaSuccess) e = tc ? launch_win_bwd_k_tc(a, s) : bwd_k<DP, false>(a, s);
+  if (e == cudaSuccess && a.nchunk > 0) e = bwd_k<DP, true>(a, s);
   if (e == cudaSuccess && a.nchunk > 0) e = launch_win_sink_reduce(a, 0, s);
   return e;
 }
-template <int DP>
-cudaError_t fwd(const WinArgs& a, cudaStream_t s) {
-  return win_vec(a) ? fwd<DP, true>(a, s) : fwd<DP, false>(a, s);
-}
-template <int DP>
-cudaError_t bwd(const WinArgs& a, bool tc, cudaStream_t s) {
-  return win_vec(a) && (reinterpret_cast<uintptr_t>(a.d_out) & 15) == 0 ? bwd<DP, true>(a, tc, s) : bwd<DP, false>(a, false, s);
-}
-
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Whether every tensor of a call is on 16-byte boundaries.
+// Whether the outputs, which may be anywhere, are on 16-byte boundaries like the inputs.
 bool vectors(const WinArgs& a, bool backward) {
-  return win_vec(a) && on16(a.out) && (!backward || (on16(a.d_out) && on16(a.d_q) && on16(a.d_k) && on16(a.d_v)));
+  return on16(a.out) && (!backward || (on16(a.d_q) && on16(a.d_k) && on16(a.d_v)));
 }
 // Whether the tcgen05 kernels take a call: their tile of 128 rows and 64 columns
 // pays when the window is wide and the rows long, and when there are rows to fill
@@ -716,14 +685,6 @@ bool use_tc(const WinArgs& a, bool backward) {
   const long long w = a.D > a.Dv ? a.D : a.Dv, all = (long long)a.left + a.right + 1, win = all < a.Nk ? all : a.Nk;
   return win * w * w >= 200000 && (long long)a.Nq * a.G >= 64 && a.Nk >= 64 && vectors(a, backward);
 }
-// Whether a CTA takes a whole sequence: two of them fit an SM, and there are that many.
-//   64 x 128 x 8 heads of 16, window 63: 11.7 / 21 us against 14.0 / 38; 8 x 256 x 8: 14.5 / 27 against 8.9 / 24
-bool use_short(const WinArgs& a, bool backward) {
-  const int w = a.D > a.Dv ? a.D : a.Dv;
-  if (w > 64 || a.Nk > kWinShortRows || (long long)a.Nq * a.G > kWinShortRows || (long long)a.B * a.Hkv < 296) return false;
-  return win_short_smem(a, w <= 16 ? 16 : (w <= 32 ? 32 : 64), backward) <= 100 * 1024 && vectors(a, backward);
-}
-
 }  // namespace
 
 cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s) {
@@ -733,16 +694,15 @@ cudaError_t launch_win_sink_reduce(const WinArgs& a, int f32, cudaStream_t s) {
   return cudaGetLastError();
 }
 cudaError_t launch_win_fwd(const WinArgs& a, cudaStream_t s) {
-  const long long F = (long long)a.Nq * a.G;
-  if (F <= kWinStepRows || (F <= 4 * kWinStepRows && (long long)a.B * a.Hkv < 74)) return launch_win_step(a, s);
-  if (use_short(a, false)) return launch_win_short(a, false, s);
+  if (win_step_takes(a)) return launch_win_step(a, s);
+  if (win_short_takes(a, false) && vectors(a, false)) return launch_win_short(a, false, s);
   if (use_tc(a, false)) return launch_win_fwd_tc(a, s);
   const int w = a.D > a.Dv ? a.D : a.Dv;
   return w <= 16 ? fwd<16>(a, s) : (w <= 32 ? fwd<32>(a, s) : (w <= 64 ? fwd<64>(a, s) : fwd<128>(a, s)));
 }
 cudaError_t launch_win_bwd(const WinArgs& in, cudaStream_t s) {
   WinArgs a = in;
-  if (use_short(a, true)) return launch_win_short(a, true, s);
+  if (win_short_takes(a, true) && vectors(a, true)) return launch_win_short(a, true, s);
   const bool tc = use_tc(a, true);
   const WinSinkPlan sp = win_sink_plan(a, tc ? kWinTcRows : T);
   a.nchunk = sp.nchunk;

@@ -48,11 +48,8 @@ struct Src {                               // one of the inputs, for one (b, hkv
   long long sn, sh;
   int width;
 };
-// VEC: every load is on a 16-byte boundary.  The slow loads are instantiations
-// of their own: beside the fast ones they would fill the instruction cache.
-//
 // A tile of rows x width elements, by `threads` threads of which this is `me`; at(r) gives row r's elements, or null for a row of zeros.
-template <int DP, bool VEC, typename At>
+template <int DP, typename At>
 __device__ __forceinline__ void load_tile(bf16* dst, const Src& s, int rows, int me, int threads, At at) {
   constexpr int CH = DP / 8;
   for (int e = me; e < rows * CH; e += threads) {
@@ -60,15 +57,7 @@ __device__ __forceinline__ void load_tile(bf16* dst, const Src& s, int rows, int
     const bf16* p = at(r);
     bf16* d = dst + r * Tile<DP>::ld + c * 8;
     const bool on = p != nullptr && c * 8 < s.width;
-    if (VEC) {
-      cp16_zfill(smem_u32(d), on ? p + c * 8 : s.p, on);
-    } else {
-      uint16_t w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = on && c * 8 + k < s.width ? reinterpret_cast<const uint16_t*>(p)[c * 8 + k] : (uint16_t)0;
-      *reinterpret_cast<uint4*>(d) = make_uint4(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16,
-                                                w[4] | (uint32_t)w[5] << 16, w[6] | (uint32_t)w[7] << 16);
-    }
+    cp16_zfill(smem_u32(d), on ? p + c * 8 : s.p, on);
   }
 }
 __device__ __forceinline__ Src source(const void* base, long long sb, long long sn, long long sh, int width, int b, int h0) {

@@ -140,21 +140,17 @@ struct Fsrc {
 __device__ __forceinline__ Fsrc fsource(const void* base, long long sb, long long sn, long long sh, int width, int b, int h0) {
   return Fsrc{static_cast<const float*>(base) + b * sb + h0 * sh, sn, sh, width};
 }
-__device__ __forceinline__ void cp4_zfill(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
-}
 // A tile of rows; at(r) gives row r's elements, or null for a row of zeros.
-template <int DP, bool VEC, typename At>
+template <int DP, typename At>
 __device__ __forceinline__ void load_f(float* dst, const Fsrc& s, int rows, At at) {
-  constexpr int N = VEC ? 4 : 1, CH = DP / N;
+  constexpr int N = 4, CH = DP / N;
   const int c = threadIdx.x % CH * N;
   const uint32_t d = smem_u32(dst) + c * 4;
 #pragma unroll 4
   for (int r = threadIdx.x / CH; r < rows; r += kThreads / CH) {
     const float* p = at(r);
     const bool on = p != nullptr && c < s.width;
-    if (VEC) cp16_zfill(d + r * Ft<DP>::ld * 4, on ? p + c : s.p, on);
-    else cp4_zfill(d + r * Ft<DP>::ld * 4, on ? p + c : s.p, on);
+    cp16_zfill(d + r * Ft<DP>::ld * 4, on ? p + c : s.p, on);
   }
 }
 __device__ __forceinline__ void column_words(uint32_t* bits, const WinArgs& a, int b, const WinCols& c, int u0) {
@@ -182,7 +178,7 @@ __device__ __forceinline__ void store_f(const float (&acc)[DP / 8][4], int width
 }
 
 // Forward (BWD false) and row side of the backward (BWD true: delta, dq).
-template <int DP, bool VEC, bool BWD>
+template <int DP, bool BWD>
 __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int EL = Ft<DP>::elems;
@@ -231,8 +227,8 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
         return u < c.n && (a.mask == nullptr || a.mask[(long long)b * a.Nk + c.key(u)] != 0) ? s.p + c.key(u) * s.sn : nullptr;
       };
     };
-    load_f<DP, VEC>(Ks + st * EL, k, T, keyed(k));
-    load_f<DP, VEC>(Vs + st * EL, v, T, keyed(v));
+    load_f<DP>(Ks + st * EL, k, T, keyed(k));
+    load_f<DP>(Vs + st * EL, v, T, keyed(v));
     column_words(bits[st], a, b, c, u0);
     cp_async_commit();
   };
@@ -249,8 +245,8 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
         return f < f1 && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
       };
     };
-    load_f<DP, VEC>(Qs, q, T, rows(q));
-    if (BWD) load_f<DP, VEC>(Os, g_, T, rows(g_));
+    load_f<DP>(Qs, q, T, rows(q));
+    if (BWD) load_f<DP>(Os, g_, T, rows(g_));
     load(0);
   }
   for (int t = 0; t < ntile; ++t) {
@@ -384,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) win_rows_tf32_kernel(const WinArgs a
 }
 
 // dk and dv, as win_bwd_k_mma_kernel (SINK: 16 keys that hold sinks over one chunk of the rows beyond the window).
-template <int DP, bool VEC, bool SINK>
+template <int DP, bool SINK>
 __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a) {
   constexpr int KR = SINK ? 16 : T, EL = Ft<DP>::elems;
   extern __shared__ __align__(16) float sm[];
@@ -432,8 +428,8 @@ __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a
         return f < fh && win_alive(a, b, q0 + i) ? s.p + i * s.sn + (f - i * a.G) * s.sh : nullptr;
       };
     };
-    load_f<DP, VEC>(Qs + st * EL, q, T, rows(q));
-    load_f<DP, VEC>(Os + st * EL, g_, T, rows(g_));
+    load_f<DP>(Qs + st * EL, q, T, rows(q));
+    load_f<DP>(Os + st * EL, g_, T, rows(g_));
     cp_async_commit();
     if (threadIdx.x < T) {
       const int f = f0 + threadIdx.x, i = f / a.G;
@@ -464,8 +460,8 @@ __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a
     auto keyed = [&](const Fsrc& s) {
       return [&](int r) -> const float* { return j0 + r <= j1 && win_alive(a, b, j0 + r) ? s.p + (j0 + r) * s.sn : nullptr; };
     };
-    load_f<DP, VEC>(Ks, k, KR, keyed(k));
-    load_f<DP, VEC>(Vs, v, KR, keyed(v));
+    load_f<DP>(Ks, k, KR, keyed(k));
+    load_f<DP>(Vs, v, KR, keyed(v));
     load(0);
     put(0);
   }
@@ -585,39 +581,33 @@ __global__ void __launch_bounds__(kThreads) win_keys_tf32_kernel(const WinArgs a
   store_f<DP>(dv, a.Dv, 1.f, lane, [&](int i, bool& keep) { return at(a.d_v, a.Dv, i, keep); });
 }
 
-template <int DP, bool VEC, bool BWD>
+template <int DP, bool BWD>
 cudaError_t rows(const WinArgs& a, cudaStream_t s) {
-  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_rows_tf32_kernel<DP, VEC, BWD>));
+  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_rows_tf32_kernel<DP, BWD>));
   if (e != cudaSuccess) return e;
   const long long grid = (long long)a.B * a.Hkv * (((long long)a.Nq * a.G + T - 1) / T);
-  win_rows_tf32_kernel<DP, VEC, BWD><<<(unsigned)grid, kThreads, (BWD ? 6 : 5) * Ft<DP>::elems * sizeof(float), s>>>(a);
+  win_rows_tf32_kernel<DP, BWD><<<(unsigned)grid, kThreads, (BWD ? 6 : 5) * Ft<DP>::elems * sizeof(float), s>>>(a);
   return cudaGetLastError();
 }
-template <int DP, bool VEC, bool SINK>
+template <int DP, bool SINK>
 cudaError_t keys(const WinArgs& a, cudaStream_t s) {
-  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_keys_tf32_kernel<DP, VEC, SINK>));
+  const cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(&win_keys_tf32_kernel<DP, SINK>));
   if (e != cudaSuccess) return e;
   const long long grid = (long long)a.B * a.Hkv * (SINK ? (long long)(a.sinks + 15) / 16 * a.nchunk : (a.Nk + T - 1) / T);
-  win_keys_tf32_kernel<DP, VEC, SINK><<<(unsigned)grid, kThreads, (size_t)(2 * (SINK ? 16 : T) + 4 * T) * Ft<DP>::ld * sizeof(float), s>>>(a);
+  win_keys_tf32_kernel<DP, SINK><<<(unsigned)grid, kThreads, (size_t)(2 * (SINK ? 16 : T) + 4 * T) * Ft<DP>::ld * sizeof(float), s>>>(a);
   return cudaGetLastError();
 }
-template <int DP, bool VEC>
+template <int DP>
 cudaError_t bwd(const WinArgs& a, cudaStream_t s) {
-  cudaError_t e = rows<DP, VEC, true>(a, s);
-  if (e == cudaSuccess) e = keys<DP, VEC, false>(a, s);
-  if (e == cudaSuccess && a.nchunk > 0) e = keys<DP, VEC, true>(a, s);
+  cudaError_t e = rows<DP, true>(a, s);
+  if (e == cudaSuccess) e = keys<DP, false>(a, s);
+  if (e == cudaSuccess && a.nchunk > 0) e = keys<DP, true>(a, s);
   if (e == cudaSuccess && a.nchunk > 0) e = launch_win_sink_reduce(a, 1, s);
   return e;
 }
-bool vectors(const WinArgs& a) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
-                      reinterpret_cast<uintptr_t>(a.d_out);
-  return ((p & 15) | ((a.qb | a.qn | a.qh | a.kb | a.kn | a.kh | a.vb | a.vn | a.vh | a.D | a.Dv) & 3)) == 0;
-}
 template <int DP>
 cudaError_t run(const WinArgs& a, bool backward, cudaStream_t s) {
-  if (backward) return vectors(a) ? bwd<DP, true>(a, s) : bwd<DP, false>(a, s);
-  return vectors(a) ? rows<DP, true, false>(a, s) : rows<DP, false, false>(a, s);
+  return backward ? bwd<DP>(a, s) : rows<DP, false>(a, s);
 }
 
 }  // namespace

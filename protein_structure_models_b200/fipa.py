@@ -73,7 +73,8 @@ class FipaError(RuntimeError):
 
 _lib = None
 _native = None         # the compiled calls of the sequence operators (csrc/binding.cpp)
-NATIVE_CALLS = ("fipa_window_attention", "fipa_window_attention_backward_workspace_size", "fipa_window_attention_backward",
+NATIVE_CALLS = ("fipa_window_attention", "fipa_window_attention_workspace_size", "fipa_window_attention_backward",
+                "fipa_window_attention_backward_workspace_size",
                 "fipa_norm_residual", "fipa_norm_residual_backward_workspace_size", "fipa_norm_residual_backward",
                 "fipa_embedding", "fipa_embedding_backward_workspace_size", "fipa_embedding_backward")
 
@@ -144,10 +145,11 @@ def load_library():
         + [vp] * 4 + [vp, sz, vp]
     lib.fipa_ipa_layer.restype = c_int
     heads, win = ctypes.POINTER(FipaHeads), ctypes.POINTER(FipaWindow)
-    lib.fipa_window_attention.argtypes = [vp, heads, heads, heads, vp, vp, win, vp, vp, vp]
+    lib.fipa_window_attention.argtypes = [vp, heads, heads, heads, vp, vp, win, vp, vp, vp, sz, vp]
     lib.fipa_window_attention.restype = c_int
-    lib.fipa_window_attention_backward_workspace_size.argtypes = [vp, win, ctypes.POINTER(sz)]
-    lib.fipa_window_attention_backward_workspace_size.restype = c_int
+    for name in ("fipa_window_attention_workspace_size", "fipa_window_attention_backward_workspace_size"):
+        getattr(lib, name).argtypes = [vp, heads, heads, heads, win, ctypes.POINTER(sz)]
+        getattr(lib, name).restype = c_int
     lib.fipa_window_attention_backward.argtypes = [vp, heads, heads, heads, vp, vp, win] + [vp] * 7 + [sz, vp]
     lib.fipa_window_attention_backward.restype = c_int
     nd, ni = ctypes.POINTER(FipaNormDims), ctypes.POINTER(FipaNormInputs)
@@ -414,7 +416,7 @@ class Fipa:
     def window_attention(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: tuple, sinks: int = 0,
                          mask: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
                          scale: Optional[float] = None, want_lse: bool = False, out: Optional[dict] = None,
-                         stream: Optional[torch.cuda.Stream] = None) -> dict:
+                         stream: Optional[torch.cuda.Stream] = None, workspace: Optional[torch.Tensor] = None) -> dict:
         """fipa_window_attention: q [B,Nq,H,D], k [B,Nk,Hkv,D], v [B,Nk,Hkv,Dv] of the
         handle's dtype (any strides, width contiguous); window = (left, right), None or
         a negative number for no bound; the first `sinks` tokens stay visible.  q_start
@@ -428,8 +430,11 @@ class Fipa:
             o, lse = out.get("out"), out.get("lse")
             if o is None:
                 raise ValueError("out: buffer missing")
+        if workspace is None and stream is not None:
+            workspace = self._window_room("fipa_window_attention_workspace_size", q, k, v, window, sinks)
+            _used_on(stream, workspace)
         r = _native.window(self.handle.value, self._code, self.device, q, k, v, -1 if left is None else left,
-                           -1 if right is None else right, sinks, mask, q_start, scale, want_lse, o, lse,
+                           -1 if right is None else right, sinks, mask, q_start, scale, want_lse, o, lse, workspace,
                            _stream_address(stream))
         if type(r) is int:
             self._check(r)
@@ -452,7 +457,7 @@ class Fipa:
             if dq is None or dk is None or dv is None:
                 raise ValueError("grads: need buffers q, k and v")
         if workspace is None and stream is not None:
-            workspace = q.new_empty(self.window_attention_backward_workspace_size(q, k, v, window, sinks), dtype=torch.uint8)
+            workspace = self._window_room("fipa_window_attention_backward_workspace_size", q, k, v, window, sinks)
             _used_on(stream, workspace)
         r = _native.window_backward(self.handle.value, self._code, self.device, q, k, v, -1 if left is None else left,
                                     -1 if right is None else right, sinks, mask, q_start, scale, out, lse, d_out, dq, dk, dv,
@@ -464,14 +469,27 @@ class Fipa:
             _used_on(stream, *r)
         return grads
 
-    def window_attention_backward_workspace_size(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
-                                                 window: tuple, sinks: int = 0) -> int:
-        """Bytes of workspace window_attention_backward needs for these tensors."""
+    def _window_bytes(self, call, q, k, v, window, sinks):
         (B, Nq, H, D), (_, Nk, Hkv, Dv) = q.shape, v.shape
         left, right = (-1 if x is None else min(int(x), 0x7fffffff) for x in window)
         w, n = FipaWindow(B, Nq, Nk, H, Hkv, D, Dv, left, right, int(sinks), 1.0), ctypes.c_size_t()
-        self._check(self.lib.fipa_window_attention_backward_workspace_size(self.handle, w, n))
+        heads = [FipaHeads(x.data_ptr(), x.stride(0), x.stride(1), x.stride(2)) for x in (q, k, v)]
+        self._check(getattr(self.lib, call)(self.handle, *heads, w, n))
         return int(n.value)
+
+    def _window_room(self, call, q, k, v, window, sinks):
+        return q.new_empty(self._window_bytes(call, q, k, v, window, sinks), dtype=torch.uint8)
+
+    def window_attention_workspace_size(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: tuple,
+                                        sinks: int = 0) -> int:
+        """Bytes of workspace window_attention needs for these tensors: 0 where their
+        addresses, strides and widths are multiples of 16 bytes."""
+        return self._window_bytes("fipa_window_attention_workspace_size", q, k, v, window, sinks)
+
+    def window_attention_backward_workspace_size(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                                 window: tuple, sinks: int = 0) -> int:
+        """Bytes of workspace window_attention_backward needs for these tensors."""
+        return self._window_bytes("fipa_window_attention_backward_workspace_size", q, k, v, window, sinks)
 
     BWD_STAGES = ("recompute", "prep", "q_side", "k_side", "chain")
 

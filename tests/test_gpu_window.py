@@ -286,6 +286,49 @@ def test_refusals(handles):
         h.window_attention_backward(q, k, v, o["out"], o["lse"], o["out"], (1, 1),
                                     workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 3
+    odd = make("bf16", 1, 256, 256, 2, 2, 17, 16)
+    assert h.window_attention_workspace_size(q, k, v, (1, 1)) == 0 < h.window_attention_workspace_size(*odd, (1, 1))
+    with pytest.raises(FipaError) as e:
+        h.window_attention(*odd, (1, 1), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 3
+    with pytest.raises(FipaError) as e:
+        h.window_attention_backward(q, k, v, o["out"], o["lse"], rnd((129,), torch.bfloat16, 3)[1:].view(o["out"].shape), (1, 1))
+    assert e.value.status == 1
+    h.sync_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["width", "value width", "stride", "address"])
+def test_off_16_byte_boundaries_as_on_them(handles, dtype, what):
+    """Each way to be off 16-byte boundaries, with garbage beside and behind the
+    tensors, a window far from most keys, and guarded buffers and workspaces."""
+    h, td = handles[dtype], torch.bfloat16 if dtype == "bf16" else torch.float32
+    B, Nq, Nk, H, Hkv = 2, 70, 301, 4, 2
+    D, Dv = {"width": (21, 16), "value width": (16, 13)}.get(what, (16, 24))
+    q, k, v = make(dtype, B, Nq, Nk, H, Hkv, D, Dv, 71)
+
+    def moved(t):
+        if what == "stride":
+            w = torch.full((*t.shape[:3], t.shape[3] + 1), math.nan, dtype=td, device="cuda")[..., :t.shape[3]]
+        else:
+            w = torch.full((t.numel() + 2,), math.nan, dtype=td, device="cuda")[1 if what == "address" else 0:][:t.numel()].view(t.shape)
+        return w.copy_(t)
+
+    start = torch.tensor([231, 5], dtype=torch.int32, device="cuda")
+    kw = dict(window=(9, 2), sinks=3, q_start=start)
+    mq, mk, mv = moved(q), moved(k), moved(v)
+    d = rnd((B, Nq, H, Dv), td, 72)
+    o, g = check(h, mq, mk, mv, 9, 2, 3, q_start=start, d_out=d)
+    room, bufs = [], []
+    for size in (h.window_attention_workspace_size, h.window_attention_backward_workspace_size):
+        n = size(mq, mk, mv, kw["window"], 3)
+        bufs.append(torch.full((n + 512,), 0xff, dtype=torch.uint8, device="cuda"))       # NaN wherever nothing is written
+        room.append(bufs[-1][256:256 + n])
+    o2 = h.window_attention(mq, mk, mv, want_lse=True, workspace=room[0], **kw)
+    g2 = h.window_attention_backward(mq, mk, mv, o["out"], o["lse"], d, workspace=room[1], **kw)
+    assert all(torch.equal(a, b) for x, y in ((o, o2), (g, g2)) for a, b in zip(x.values(), y.values()))
+    for w in bufs:
+        assert (w[:256] == 0xff).all() and (w[-256:] == 0xff).all()
     h.sync_status()
 
 

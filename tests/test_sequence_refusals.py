@@ -76,6 +76,7 @@ def test_embedding(lib):
 def test_window_attention_without_a_handle(lib):
     from protein_structure_models_b200.fipa import FipaHeads, FipaWindow
     w, t, n = FipaWindow(1, 1, 1, 1, 1, 8, 8, 1, 1, 0, 1.0), FipaHeads(P, 8, 8, 8), ctypes.c_size_t()
-    assert lib.fipa_window_attention(None, t, t, t, None, None, w, P, None, None) == 1
+    assert lib.fipa_window_attention(None, t, t, t, None, None, w, P, None, None, 0, None) == 1
     assert lib.fipa_window_attention_backward(None, t, t, t, None, None, w, P, P, P, P, P, P, P, 1 << 20, None) == 1
-    assert lib.fipa_window_attention_backward_workspace_size(None, w, ctypes.byref(n)) == 1
+    assert lib.fipa_window_attention_workspace_size(None, t, t, t, w, ctypes.byref(n)) == 1
+    assert lib.fipa_window_attention_backward_workspace_size(None, t, t, t, w, ctypes.byref(n)) == 1
