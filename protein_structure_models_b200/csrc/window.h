@@ -40,6 +40,7 @@ struct WinArgs {
   int* status;
   unsigned long long timeout_ns;
   void* pad;                         // workspace of window_pad.cu
+  int fine;                          // bfloat16: probabilities and dS enter their products as two numbers, see win_is_fine
 };
 
 constexpr int kWinMaxD = 128;
@@ -84,6 +85,12 @@ inline bool win_short_takes(const WinArgs& a, bool backward) {
   if (w > 64 || a.Nk > kWinShortRows || (long long)a.Nq * a.G > kWinShortRows || (long long)a.B * a.Hkv < 296) return false;
   return win_short_smem(a, w <= 16 ? 16 : (w <= 32 ? 32 : 64), backward) <= 100 * 1024;
 }
+// Probabilities and dS are rounded to bfloat16 for their products.  Over many rows
+// that adds as much to a result's error as the rounding of the result (together
+// 2^-9.2 of it, against 2^-9.2 / 1.4); over few rows chance makes it more, and
+// there is time for a second product with what the rounding left.
+inline int win_is_fine(const WinArgs& a) { return (long long)a.B * a.Nq * a.H < 16384; }
+
 // Whether bfloat16 q, k and v can be read 16 bytes at a time.
 inline bool win_vec(const WinArgs& a) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);

@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) win_fwd_mma_kernel(const WinArgs a) 
           mma(acc[2 * n], pf, bf[0], bf[1]);
           mma(acc[2 * n + 1], pf, bf[2], bf[3]);
         }
+        if (a.fine) add_rest<DP>(acc, pf, s[2 * g], s[2 * g + 1], vs, 16 * g, kv, lane);
       }
       l[0] += sum[0];
       l[1] += sum[1];
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(kThreads) win_bwd_q_mma_kernel(const WinArgs a
         mma(avg[2 * n], pf, bf[0], bf[1]);
         mma(avg[2 * n + 1], pf, bf[2], bf[3]);
       }
+      if (a.fine) add_rest<DP>(acc, df, dp[0], dp[1], ks, 16 * g, kd, lane);
     }
     __syncthreads();
   }
@@ -555,6 +557,10 @@ __global__ void __launch_bounds__(kThreads) win_bwd_k_mma_kernel(const WinArgs a
           mma(dk[2 * n + 1], df, bf[2], bf[3]);
         }
       }
+      if (a.fine) {
+        add_rest<DP>(dv, pf, s[0], s[1], os, 16 * g, kv, lane);
+        add_rest<DP>(dk, df, dp[0], dp[1], qs, 16 * g, kd, lane);
+      }
     }
     if (t + 1 < ntile) put(st ^ 1);
     __syncthreads();
@@ -683,6 +689,7 @@ bool vectors(const WinArgs& a, bool backward) {
 //   512 x 40 x 8 of 128: 113 / 341 against 120 / 503
 bool use_tc(const WinArgs& a, bool backward) {
   const long long w = a.D > a.Dv ? a.D : a.Dv, all = (long long)a.left + a.right + 1, win = all < a.Nk ? all : a.Nk;
+  if ((long long)a.B * a.Nq * a.H < 256) return false;     // see win_is_fine
   return win * w * w >= 200000 && (long long)a.Nq * a.G >= 64 && a.Nk >= 64 && vectors(a, backward);
 }
 }  // namespace

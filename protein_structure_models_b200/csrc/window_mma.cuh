@@ -153,6 +153,25 @@ __device__ __forceinline__ uint32_t bt_addr(uint32_t base, int k0, int n0, int l
   return base + 2 * ((k0 + (lane & 7) + (((lane >> 3) & 1) << 3)) * Tile<DP>::ld + n0 + ((lane >> 4) << 3));
 }
 
+// What two packed bfloat16 leave of the numbers that they stand for.
+__device__ __forceinline__ uint32_t rest(uint32_t hi, float x, float y) {
+  return pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+// acc += (what the operand `hi` of 16 x 16 leaves of x0 and x1) times rows r .. r+15 of a tile, for 16 n16 columns
+template <int DP>
+__device__ __forceinline__ void add_rest(float (&acc)[DP / 8][4], const uint32_t (&hi)[4], const float (&x0)[4], const float (&x1)[4],
+                                         uint32_t tile, int r, int n16, int lane) {
+  const uint32_t lo[4] = {rest(hi[0], x0[0], x0[1]), rest(hi[1], x0[2], x0[3]), rest(hi[2], x1[0], x1[1]), rest(hi[3], x1[2], x1[3])};
+#pragma unroll
+  for (int n = 0; n < DP / 16; ++n) {
+    if (n >= n16) break;
+    uint32_t bf[4];
+    ldsm4t(bf, bt_addr<DP>(tile, r, 16 * n, lane));
+    mma(acc[2 * n], lo, bf[0], bf[1]);
+    mma(acc[2 * n + 1], lo, bf[2], bf[3]);
+  }
+}
+
 // Columns that neighbouring rows see: any of them, and all of them (n columns from u on).
 struct Reach {
   int s_any, s_all, a_any, a_all, e_any, e_all;       // sinks [0, s), window [a, e)

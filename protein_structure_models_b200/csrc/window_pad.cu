@@ -106,6 +106,7 @@ struct PadPlan {
 PadPlan plan(const WinArgs& a, int es, bool backward) {
   PadPlan p{a, {}, {}, 0};
   p.in.n = p.out.n = 0;
+  p.a.fine = win_is_fine(a);
   if (!backward && es == 2 && win_step_takes(a)) return p;          // reads what it is given
   const int V = 16 / es, D = (a.D + V - 1) / V * V, Dv = (a.Dv + V - 1) / V * V;
   p.a.D = D;
@@ -152,8 +153,7 @@ cudaError_t launch_win(const WinArgs& a, int es, bool backward, cudaStream_t s) 
   const PadPlan p = plan(a, es, backward);
   cudaError_t e = copy<false>(p.in, a, es, s);
   if (e != cudaSuccess) return e;
-  const WinArgs& w = p.bytes > 0 ? p.a : a;
-  e = es == 4 ? launch_win_f32(w, backward, s) : (backward ? launch_win_bwd(w, s) : launch_win_fwd(w, s));
+  e = es == 4 ? launch_win_f32(p.a, backward, s) : (backward ? launch_win_bwd(p.a, s) : launch_win_fwd(p.a, s));
   return e == cudaSuccess ? copy<true>(p.out, a, es, s) : e;
 }
 

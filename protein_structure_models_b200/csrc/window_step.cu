@@ -81,16 +81,17 @@ __global__ void __launch_bounds__(kWarps * 32, DP <= 16 ? 5 : (DP <= 64 ? 4 : 2)
   const int ntile = all > first ? (all - first + W - 1) / W : 0;
   constexpr int KW = DP / 8 < 4 ? DP / 8 : 4, KC = DP / (8 * KW);     // words of a key load, loads of a key
   constexpr int VW = DP / 16;                                          // words of a value load
+  bool alive[2];
   WinRow row[2];
   uint32_t qf[KC][2][KW];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int f = f0 + g + 8 * i, qi = f / a.G, p = q0 + qi;
-    const bool alive = f < f1 && win_alive(a, b, p);
-    row[i] = win_row(a, c, p, alive);
+    alive[i] = f < f1 && win_alive(a, b, p);
+    row[i] = win_row(a, c, p, alive[i]);
 #pragma unroll
     for (int x = 0; x < KC; ++x)
-      words<KW, VEC>(qf[x][i], alive ? q.p + qi * q.sn + (f - qi * a.G) * q.sh : q.p, 8 * KW * x + 2 * KW * c4, a.D, alive);
+      words<KW, VEC>(qf[x][i], alive[i] ? q.p + qi * q.sn + (f - qi * a.G) * q.sh : q.p, 8 * KW * x + 2 * KW * c4, a.D, alive[i]);
   }
   const Reach rc = reach(a, c, q0, f0, f1);
   float acc[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -211,6 +212,14 @@ __global__ void __launch_bounds__(kWarps * 32, DP <= 16 ? 5 : (DP <= 64 ? 4 : 2)
         mma(acc[2 * w], pf, __byte_perm(vw[0][w], vw[1][w], 0x5410), __byte_perm(vw[2][w], vw[3][w], 0x5410));
         mma(acc[2 * w + 1], pf, __byte_perm(vw[0][w], vw[1][w], 0x7632), __byte_perm(vw[2][w], vw[3][w], 0x7632));
       }
+      if (a.fine) {
+        const uint32_t lo[4] = {rest(pf[0], s[0][0], s[0][1]), rest(pf[1], s[0][2], s[0][3]), rest(pf[2], s[1][0], s[1][1]), rest(pf[3], s[1][2], s[1][3])};
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          mma(acc[2 * w], lo, __byte_perm(vw[0][w], vw[1][w], 0x5410), __byte_perm(vw[2][w], vw[3][w], 0x5410));
+          mma(acc[2 * w + 1], lo, __byte_perm(vw[0][w], vw[1][w], 0x7632), __byte_perm(vw[2][w], vw[3][w], 0x7632));
+        }
+      }
     }
     load_v(vw, t + AHEAD, next);
     now = next;
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, DP <= 16 ? 5 : (DP <= 64 ? 4 : 2)
     l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     if (c4 == 0) {
       wm[warp][g + 8 * i] = m[i];
-      wl[warp][g + 8 * i] = l[i];
+      wl[warp][g + 8 * i] = alive[i] ? l[i] : 0.f;       // tiles of which every column is seen are not masked row by row
     }
   }
   __syncthreads();

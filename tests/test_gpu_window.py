@@ -149,6 +149,18 @@ def test_tokens_against_a_cache(handles, dtype, Nq, Nk, H, Hkv, D):
         check(handles[dtype], q, k, v, left, 0, sinks, q_start=start, backward=Nq in (3, 200))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Nq,Nk,H,Hkv,D", [(1, 300, 8, 8, 64), (3, 290, 6, 2, 20), (22, 203, 16, 8, 32), (100, 400, 2, 2, 16), (5, 70, 4, 4, 32)])
+def test_tokens_of_a_padded_batch(handles, dtype, Nq, Nk, H, Hkv, D):
+    """The last tokens of samples of several lengths: those behind a sample's end see nothing, though all their columns may be valid."""
+    q, k, v = make(dtype, 5, Nq, Nk, H, Hkv, D, D, 21)
+    ends = torch.tensor([Nk, Nk - Nq, Nk - Nq // 2, Nk - Nq - 16, 0], device="cuda")
+    mask = torch.arange(Nk, device="cuda")[None] < ends[:, None]
+    for left, sinks in ((Nk, 0), (180, 1), (20, 4)):
+        got, _ = check(handles[dtype], q, k, v, left, 0, sinks, mask=mask)
+        assert (got["out"][~mask[:, -Nq:]] == 0).all()
+
+
 @pytest.mark.parametrize("big", [2 ** 31 - 1, -2 ** 31])
 def test_start_positions_at_the_ends_of_int32(handles, big):
     q, k, v = make("bf16", 2, 4, 50, 2, 2, 16, 16)
