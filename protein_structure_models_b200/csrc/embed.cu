@@ -6,7 +6,8 @@
 // Bound by memory: idx, dout and out once, the table's used rows, dtable once.
 // The gradient sorts (index, token) by a stable radix sort on the bits that V
 // needs, cuts the sorted list into chunks of equal length, one group of threads
-// each, and adds rows of dout while the index stays the same.  A run inside one
+// each, and adds rows of dout while the index stays the same (few tokens: see
+// embed_few_kernel).  A run inside one
 // chunk is final; the pieces of a run that crosses chunks are kept in float32
 // and added in chunk order, so no sum depends on the order of atomics and a row
 // with all the tokens costs what many rows cost.
@@ -471,6 +472,60 @@ __global__ void __launch_bounds__(512) embed_join_kernel(const int* __restrict__
   }
 }
 
+// The whole gradient of at most kFew tokens in one launch, where the sort's three
+// would cost more than the work (37 tokens, 44947 x 128, forward and backward: 8.3 us
+// against 16.3; 128 of one row of 256: 10.8 against 12.6): a warp owns a row of the
+// table and 32 pieces of columns, finds the row's tokens by comparing all of them,
+// four a lane, and adds eight rows of dout at a time, in order.
+constexpr int kFew = 128;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) embed_few_kernel(const int* __restrict__ idx, const T* __restrict__ dout, int n, int V, int C,
+                                                        int slabs, float scale, float* __restrict__ dtable) {
+  constexpr int N = VEC ? Vec<T>::n : 1, W = kFew / 32, U = 8;
+  const int lane = threadIdx.x & 31;
+  int key[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) key[j] = 32 * j + lane < n ? idx[32 * j + lane] : -1;
+  const long long units = (long long)V * slabs, step = (long long)gridDim.x * 8;
+  for (long long x = blockIdx.x * 8ll + (threadIdx.x >> 5); x < units; x += step) {
+    const int v = (int)(x / slabs), c = ((int)(x - (long long)v * slabs) * 32 + lane) * N;
+    float acc[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      unsigned mine = __ballot_sync(0xffffffffu, key[j] == v);
+      while (mine != 0) {
+        float w[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const T* p = dout + (size_t)(32 * j + __ffs(mine) - 1) * C + c;
+          const bool on = mine != 0 && c < C;
+          if (VEC) {
+            unpack<T>(on ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0), w[u]);
+          } else {
+            w[u][0] = on ? cvt(p[0]) : 0.f;
+          }
+          mine &= mine - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < N; ++k) acc[k] += w[u][k];
+      }
+    }
+    if (c >= C) continue;
+    float* o = dtable + (size_t)v * C + c;
+    if (VEC) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4)
+        *reinterpret_cast<float4*>(o + k) = make_float4(acc[k] * scale, acc[k + 1] * scale, acc[k + 2] * scale, acc[k + 3] * scale);
+    } else {
+      o[0] = acc[0] * scale;
+    }
+  }
+}
+
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Workspace of the gradient: two copies of (key, token), digit counts, pieces.
@@ -519,6 +574,17 @@ cudaError_t embed_fwd(const int* idx, const void* table, void* out, long long ro
     embed_fwd_kernel<T, true><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, lg, scale);
   else
     embed_fwd_kernel<T, false><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(table), static_cast<T*>(out), rows, V, C, pieces, lg, scale);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t embed_few(const int* idx, const void* dout, int n, int V, int C, float scale, float* dtable, cudaStream_t s) {
+  const bool vec = C % Vec<T>::n == 0 && is_aligned(dout, 16) && is_aligned(dtable, 16);
+  const int slabs = (C + 32 * (vec ? Vec<T>::n : 1) - 1) / (32 * (vec ? Vec<T>::n : 1));
+  const long long ctas = ((long long)V * slabs + 7) / 8;
+  const unsigned grid = (unsigned)(ctas < 148 * 8 ? ctas : 148 * 8);
+  if (vec) embed_few_kernel<T, true><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(dout), n, V, C, slabs, scale, dtable);
+  else embed_few_kernel<T, false><<<grid, 256, 0, s>>>(idx, static_cast<const T*>(dout), n, V, C, slabs, scale, dtable);
   return cudaGetLastError();
 }
 
@@ -592,15 +658,20 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
   const int n = (int)T;
   int* hist = reinterpret_cast<int*>(ws + p.off_hist);
   int* total = reinterpret_cast<int*>(ws + p.off_total);
+  if (n <= kFew) {
+    const cudaError_t e = dtype == FIPA_F32 ? embed_few<float>(idx, d_out, n, V, C, (float)scale, d_table, s)
+                                            : embed_few<__nv_bfloat16>(idx, d_out, n, V, C, (float)scale, d_table, s);
+    return e == cudaSuccess ? FIPA_OK : FIPA_ERR_CUDA;
+  }
   const int* key = idx;
   const int* tok = nullptr;
   int at = 0;
-  if (n > 0 && n <= kSortBlock) {
+  if (n <= kSortBlock) {
     int* okey = reinterpret_cast<int*>(ws + p.off_key[0]);
     int* otok = reinterpret_cast<int*>(ws + p.off_tok[0]);
     sort_small_kernel<<<1, kSortThreads, 0, s>>>(idx, n, V, p.passes, p.bits, okey, otok);
     key = okey;
-  } else if (n > 0) {
+  } else {
     const int mask = (1 << p.bits) - 1;
     for (int k = 0; k < p.passes; ++k) {
       at = k & 1;
@@ -613,11 +684,9 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
       tok = otok;
     }
   }
-  if (n > 0) {
-    const cudaError_t e = dtype == FIPA_F32 ? embed_sum<float>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s)
-                                            : embed_sum<__nv_bfloat16>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s);
-    if (e != cudaSuccess) return FIPA_ERR_CUDA;
-  }
+  const cudaError_t e = dtype == FIPA_F32 ? embed_sum<float>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s)
+                                          : embed_sum<__nv_bfloat16>(p, ws, at, d_out, n, V, C, (float)scale, d_table, s);
+  if (e != cudaSuccess) return FIPA_ERR_CUDA;
   const int ncross = p.nchunk > 1 ? (p.nchunk - 1 + 15) / 16 : 0;
   const long long fill = ((long long)V + 511) / 512;
   const unsigned gx = (unsigned)(ncross + (fill < 148 * 4 ? fill : 148 * 4));

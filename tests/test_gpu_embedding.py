@@ -57,7 +57,8 @@ def check(idx, V, C, dtype, scale=1.0, seed=3):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,V,C", [(1, 1, 1), (1, 5, 8), (31, 3, 7), (33, 1, 16), (513, 21, 256), (2049, 64, 20), (4096, 300, 1),
                                    (5000, 255, 128), (5000, 256, 33), (3000, 257, 8), (20000, 70000, 12), (6000, 100000, 4),
-                                   (700, 9, 1032), (300, 40, 3001), (70000, 64, 16)])
+                                   (700, 9, 1032), (300, 40, 3001), (70000, 64, 16), (128, 700, 264), (127, 3, 131),
+                                   (129, 40, 24), (90, 20000, 40)])
 @pytest.mark.parametrize("how", ["even", "one", "outside", "skew"])
 def test_against_the_definition(dtype, T, V, C, how):
     check(indices(T, V, how), V, C, dtype, scale=2.5)
