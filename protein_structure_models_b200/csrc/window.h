@@ -89,7 +89,7 @@ inline bool win_short_takes(const WinArgs& a, bool backward) {
 // that adds as much to a result's error as the rounding of the result (together
 // 2^-9.2 of it, against 2^-9.2 / 1.4); over few rows chance makes it more, and
 // there is time for a second product with what the rounding left.
-inline int win_is_fine(const WinArgs& a) { return (long long)a.B * a.Nq * a.H < 16384; }
+inline int win_is_fine(const WinArgs& a, bool backward) { return (long long)a.B * a.Nq * a.H < (backward ? 16384 : 1024); }
 
 // Whether bfloat16 q, k and v can be read 16 bytes at a time.
 inline bool win_vec(const WinArgs& a) {

@@ -106,7 +106,7 @@ struct PadPlan {
 PadPlan plan(const WinArgs& a, int es, bool backward) {
   PadPlan p{a, {}, {}, 0};
   p.in.n = p.out.n = 0;
-  p.a.fine = win_is_fine(a);
+  p.a.fine = win_is_fine(a, backward);
   if (!backward && es == 2 && win_step_takes(a)) return p;          // reads what it is given
   const int V = 16 / es, D = (a.D + V - 1) / V * V, Dv = (a.Dv + V - 1) / V * V;
   p.a.D = D;

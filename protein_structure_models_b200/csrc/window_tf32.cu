@@ -4,16 +4,20 @@
 // The mathematics, the row and column numbering and the visibility rule are
 // those of window.h; the work is divided as in window_mma.cu (a warp owns 16 rows
 // or 16 keys and walks the 16-column groups that they see).  A float32 operand x
-// travels as two tf32 numbers, hi = tf32(x) and lo = x - hi, of which the product
-// takes the upper 11 bits: x is kept to 2^-21, and a product is the sum lo hi +
-// hi lo + hi hi (lo lo is below 2^-22 of it).  The tensor cores add in float32 but
+// travels as two tf32 numbers, hi = x rounded to 11 bits and lo = x - hi, of which
+// the product takes the upper 11 bits: x is kept to 2^-21, and a product is the sum
+// lo hi + hi lo + hi hi (lo lo is below 2^-22 of it; with hi cut off instead of
+// rounded it is 2^-20, always of one sign, and gradients were off by 1.6e-6).  The tensor cores add in float32 but
 // cut off what does not fit, which over hundreds of keys would drift by 2^-24 a
 // step: the second products are summed over 16 columns at a time and added to the
 // running sums on the CUDA cores, rounded to nearest.
 //
 // Three products of 16 x 8 x 8 replace 32 multiply-adds and 10 shared-memory loads
-// of a CUDA-core tile: the training step of 8 x 256 residues, 8 heads of 16, takes
-// a third of that tile's time.
+// of a CUDA-core tile (training step of 8 x 256 residues, 8 heads of 16: 52 us
+// against 129).  Bound by the latency of the products: 8 warps an SM at 128
+// channels, where shared memory holds one CTA, wait for the one before in two of
+// three cycles; two warps a row block, one on the even and one on the odd groups of
+// columns, and products unrolled past the ends of a width keep more in flight.
 #include <math.h>
 
 #include "kernels.h"
@@ -23,6 +27,7 @@ namespace fipa {
 namespace {
 
 constexpr int T = kWinTile;                // rows and columns of a tile
+constexpr int kStep = 2;                    // products between two looks at the width: apart from them the compiler interleaves the loads
 constexpr int kThreads = 256;              // 4 x 16 rows, by two warps each: one takes the even groups of columns, one the odd
 
 template <int DP>
@@ -32,7 +37,7 @@ struct Ft {
 };
 
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;      // to nearest, in fewer cycles than the conversion takes
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 struct A4 {
@@ -42,7 +47,7 @@ struct B2 {
   uint32_t hi[2], lo[2];
 };
 __device__ __forceinline__ void mma1(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
@@ -97,7 +102,7 @@ template <int DP>
 __device__ __forceinline__ void add_product(float (&sum)[DP / 8][4], const A4 (&a)[2], const float* tile, int k0, int width, int lane) {
 #pragma unroll
   for (int n = 0; n < DP / 8; ++n) {
-    if (8 * n >= width) break;
+    if (n % kStep == 0 && 8 * n >= width) break;
     C3 c;
     c.zero();
 #pragma unroll
@@ -118,7 +123,7 @@ __device__ __forceinline__ void scores(float (&s)[2][4], uint32_t A, int r0, uin
   c[1].zero();
 #pragma unroll
   for (int k = 0; k < DP / 8; ++k) {
-    if (8 * k >= width) break;
+    if (k % kStep == 0 && 8 * k >= width) break;
     A4 a;
     B2 b[2];
     load_a<DP>(a, A, r0, 8 * k, lane);
