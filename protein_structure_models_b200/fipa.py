@@ -233,6 +233,9 @@ class Fipa:
         except Exception:
             pass
 
+    def _address(self):
+        return self.handle.value if self.handle else 0
+
     def _check(self, st):
         if st != FIPA_OK:
             raise FipaError(st, self.lib.fipa_last_error(self.handle).decode())
@@ -433,7 +436,7 @@ class Fipa:
         if workspace is None and stream is not None:
             workspace = self._window_room("fipa_window_attention_workspace_size", q, k, v, window, sinks)
             _used_on(stream, workspace)
-        r = _native.window(self.handle.value, self._code, self.device, q, k, v, -1 if left is None else left,
+        r = _native.window(self._address(), self._code, self.device, q, k, v, -1 if left is None else left,
                            -1 if right is None else right, sinks, mask, q_start, scale, want_lse, o, lse, workspace,
                            _stream_address(stream))
         if type(r) is int:
@@ -459,7 +462,7 @@ class Fipa:
         if workspace is None and stream is not None:
             workspace = self._window_room("fipa_window_attention_backward_workspace_size", q, k, v, window, sinks)
             _used_on(stream, workspace)
-        r = _native.window_backward(self.handle.value, self._code, self.device, q, k, v, -1 if left is None else left,
+        r = _native.window_backward(self._address(), self._code, self.device, q, k, v, -1 if left is None else left,
                                     -1 if right is None else right, sinks, mask, q_start, scale, out, lse, d_out, dq, dk, dv,
                                     workspace, _stream_address(stream))
         if type(r) is int:

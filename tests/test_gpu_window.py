@@ -118,10 +118,11 @@ def test_against_the_definition(handles, dtype, case):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [32, 21])
 @pytest.mark.parametrize("N,left,right,sinks", [(150, 31, 31, 2), (300, 64, 0, 4), (260, None, None, 0), (600, 3, 3, 100)])
-def test_masks_leave_rows_and_samples_empty(handles, dtype, N, left, right, sinks):
+def test_masks_leave_rows_and_samples_empty(handles, dtype, D, N, left, right, sinks):
     """Padding, holes, masked sinks, a whole sample masked; NaN and infinities in the masked places are never used."""
-    B, H, Hkv, D = 4, 4, 2, 32
+    B, H, Hkv = 4, 4, 2
     q, k, v = make(dtype, B, N, N, H, Hkv, D, D, 7)
     mask = torch.rand((B, N), generator=torch.Generator(device="cuda").manual_seed(5), device="cuda") < 0.6
     mask[0, N // 3:] = False
@@ -342,6 +343,45 @@ def test_off_16_byte_boundaries_as_on_them(handles, dtype, what):
     for w in bufs:
         assert (w[:256] == 0xff).all() and (w[-256:] == 0xff).all()
     h.sync_status()
+
+
+def test_a_closed_handle():
+    from protein_structure_models_b200 import Fipa, FipaError
+    h = Fipa("bf16", 0)
+    h.close()
+    with pytest.raises(FipaError) as e:
+        h.window_attention(*make("bf16", 1, 4, 8, 2, 2, 16, 16), (1, 1))
+    assert e.value.status == 1
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 37), ("f32", 24), ("f32", 19)])
+def test_captured_together_and_replayed(handles, dtype, D):
+    """Two calls of different sizes in one graph, with temporaries of the graph's pool; replayed on new inputs."""
+    h = handles[dtype]
+    q, k, v = make(dtype, 1, 200, 300, 4, 2, D, D, 81)
+    d = rnd(q.shape, TD[dtype], 82)
+    kw = dict(window=(50, 0), sinks=4)
+
+    def both():
+        o = h.window_attention(q, k, v, want_lse=True, **kw)
+        g = h.window_attention_backward(q, k, v, o["out"], o["lse"], d, **kw)
+        p = h.window_attention(q[:, :1], k, v, **kw)
+        return [o["out"], o["lse"], g["q"], g["k"], g["v"], p["out"]]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = both()
+    for seed in (90, 91):
+        for i, t in enumerate((q, k, v, d)):
+            t.copy_(rnd(t.shape, t.dtype, seed + 10 * i))
+        graph.replay()
+        want = both()
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
 
 
 def test_on_another_stream_with_its_own_allocations(handles):
