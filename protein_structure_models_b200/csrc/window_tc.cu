@@ -15,12 +15,14 @@
 // rounding); the streamed tile is its B operand read along the other axis.  The
 // running maximum, l, delta and all sums are float32.
 //
-// Bound by the exponentials and conversions of the 128 finishing threads (16 ex2
-// a cycle and SM); the tensor cores and the copies run beside them because two
-// or three CTAs share an SM.  Warps 0-3 finish rows, warp 4 issues the matrix
-// instructions, warps 5-6 copy tiles (16-byte asynchronous copies into the
-// 128-byte swizzle, zeros for masked and missing rows, which a tensor map could
-// not leave out).  Every wait is bounded.
+// Bound by the matrix instructions: one of 128 x 64 x 16 takes about 106 cycles of
+// its pipe whatever it holds, which the 64-column tiles pay 8 to 20 times; then by
+// the waits between products and softmax.  Two CTAs an SM (one in the backward
+// beyond 64 channels) and four stages of tiles (two in the forward beyond 64) keep
+// both sides busy; 16384 residues, 8 heads on 2 of 64, 511 keys before: training step
+// 282 us.  Warps 0-3 finish rows, warp 4 issues the matrix instructions, warps 5-6
+// copy tiles (16-byte asynchronous copies into the 128-byte swizzle, zeros for masked
+// and missing rows, which a tensor map could not leave out).  Every wait is bounded.
 #include <math.h>
 
 #include "kernels.h"
