@@ -700,7 +700,9 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
   const long long fill = ((long long)V + 511) / 512;
   const unsigned gx = (unsigned)(ncross + (fill < 148 * 4 ? fill : 148 * 4));
   const float* part = reinterpret_cast<const float*>(ws + p.off_part);
-  if (C % 4 == 0 && is_aligned(d_table, 16))
+  // long runs want more CTAs, narrow ones: 59574 tokens of 2 x 256 with the forward 41 us
+  // against 57, 327680 of 64 x 128 69 against 63
+  if (C % 4 == 0 && is_aligned(d_table, 16) && n / V < 16384)
     embed_join_kernel<4><<<dim3(gx, (unsigned)((C + 127) / 128)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, d_table);
   else
     embed_join_kernel<1><<<dim3(gx, (unsigned)((C + 31) / 32)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, d_table);

@@ -5,8 +5,9 @@
 //
 // The copies are O(N) beside kernels that read each key once a row tile, so they
 // cost little; loads of single elements in the kernels' tiles took 2.5 to 3.5
-// times as long as 16-byte ones (699 residues, 12 heads on 4 of 82: forward 73 us
-// against 24 us at 88, backward 385 against 108).  Few rows against a long cache
+// times as long as 16-byte ones (699 residues, 12 heads on 4 of 82: training step
+// 458 us, this way 152, at 88 channels 132).  The copies go by words (15 x 1321
+// residues, 4 heads of 106: training step 293 us, by elements 365).  Few rows against a long cache
 // read the cache as it is (window_step.cu), and of the keys of a forward call
 // only those that some row sees are copied.
 #include "kernels.h"
@@ -17,7 +18,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMost = 5;                    // tensors of one launch
-constexpr int kRows = 4;                    // rows that a thread has in flight
 
 struct Part {
   const void* wide;                         // [B,N,heads,wp] contiguous, the width a multiple of 16 bytes
@@ -34,59 +34,90 @@ struct Parts {
   void add(const void* wide, const void* odd, long long sb, long long sn, long long sh, int B, int N, int heads, int w, int wp, int es, int keys) {
     Part p{wide, odd, sb, sn, sh, N, heads, w, wp, 0, keys, (unsigned)((long long)B * N * heads), 0};
     while ((16 / es << p.lg) < wp) ++p.lg;
-    const unsigned per = (unsigned)(kThreads >> p.lg) * kRows;
+    const unsigned per = (unsigned)(kThreads >> p.lg);
     p.end = blocks() + (p.rows + per - 1) / per;
     t[n++] = p;
   }
 };
 
+// V elements of a row from p + c on (zeros from the width w on), by words: elements of
+// 2 bytes may begin in the middle of one.  Words that reach outside the row are
+// taken apart.
+template <typename E, int V>
+__device__ __forceinline__ uint4 gather(const E* __restrict__ p, int c, int w) {
+  uint32_t r[4];
+  if (sizeof(E) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = c + e < w ? reinterpret_cast<const uint32_t*>(p)[c + e] : 0u;
+  } else {
+    const int odd = (int)(reinterpret_cast<uintptr_t>(p + c) >> 1) & 1;
+    uint32_t x[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const int a = c + 2 * k - odd;                        // this word's first element
+      x[k] = 0u;
+      if (a >= 0 && a + 1 < w && (k < 4 || odd)) {
+        x[k] = *reinterpret_cast<const uint32_t*>(p + a);
+      } else if (k < 4 || odd) {
+        if (a >= 0 && a < w) x[k] = reinterpret_cast<const uint16_t*>(p)[a];
+        else if (a + 1 >= 0 && a + 1 < w) x[k] = (uint32_t)reinterpret_cast<const uint16_t*>(p)[a + 1] << 16;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = odd ? __funnelshift_r(x[e], x[e + 1], 16) : x[e];
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// And back.
+template <typename E, int V>
+__device__ __forceinline__ void scatter(E* p, int c, int w, const uint4& v) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+  if (sizeof(E) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < w) reinterpret_cast<uint32_t*>(p)[c + e] = r[e];
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(p);
+    const int odd = (int)(reinterpret_cast<uintptr_t>(p + c) >> 1) & 1;
+    if (odd) {
+      if (c < w) o[c] = (uint16_t)r[0];
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        const uint32_t x = __funnelshift_r(r[e], r[e + 1], 16);
+        if (c + 2 * e + 2 < w) *reinterpret_cast<uint32_t*>(o + c + 2 * e + 1) = x;
+        else if (c + 2 * e + 1 < w) o[c + 2 * e + 1] = (uint16_t)x;
+      }
+      if (c + 7 < w) o[c + 7] = (uint16_t)(r[3] >> 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (c + 2 * e + 1 < w) *reinterpret_cast<uint32_t*>(o + c + 2 * e) = r[e];
+        else if (c + 2 * e < w) o[c + 2 * e] = (uint16_t)r[e];
+      }
+    }
+  }
+}
+
 // BACK: from the wide tensor to the odd one.
 template <typename E, bool BACK>
 __global__ void __launch_bounds__(kThreads) win_pad_kernel(const __grid_constant__ Parts parts, const WinArgs a) {
   constexpr int V = 16 / (int)sizeof(E);
-  union Piece {
-    uint4 v;
-    E e[V];
-  };
   int i = 0;
   while (blockIdx.x >= parts.t[i].end) ++i;
   const Part& p = parts.t[i];
-  const unsigned block = blockIdx.x - (i > 0 ? parts.t[i - 1].end : 0), per = kThreads >> p.lg;
+  const unsigned block = blockIdx.x - (i > 0 ? parts.t[i - 1].end : 0), r = block * (kThreads >> p.lg) + (threadIdx.x >> p.lg);
   const int c = (int)(threadIdx.x & ((1u << p.lg) - 1)) * V;
-  const unsigned r0 = block * per * kRows + (threadIdx.x >> p.lg);
-  if (c >= p.wp) return;
-  Piece x[kRows];
-  long long at[kRows];
-  bool on[kRows];
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const unsigned r = r0 + k * per, bn = r / p.heads, b = bn / p.N, h = r - bn * p.heads;
-    const int n = (int)(bn - b * p.N);
-    on[k] = r < p.rows;
-    if (on[k] && p.keys) {
-      const int q0 = win_q0(a, (int)b);
-      on[k] = n < a.sinks || (n >= max(q0, 0) - a.left && n <= min(q0 + a.Nq - 1, a.Nk - 1) + a.right);
-    }
-    at[k] = b * p.sb + n * p.sn + h * p.sh + c;
-    if (BACK) {
-      if (on[k]) x[k].v = *(reinterpret_cast<const uint4*>(static_cast<const E*>(p.wide) + (size_t)r * p.wp + c));
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) x[k].e[e] = on[k] && c + e < p.w ? static_cast<const E*>(p.odd)[at[k] + e] : (E)0;
-    }
+  if (c >= p.wp || r >= p.rows) return;
+  const unsigned bn = r / p.heads, b = bn / p.N, h = r - bn * p.heads;
+  const int n = (int)(bn - b * p.N);
+  if (p.keys) {
+    const int q0 = win_q0(a, (int)b);
+    if (n >= a.sinks && (n < max(q0, 0) - a.left || n > min(q0 + a.Nq - 1, a.Nk - 1) + a.right)) return;
   }
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    if (!on[k]) continue;
-    if (BACK) {
-      E* o = const_cast<E*>(static_cast<const E*>(p.odd)) + at[k];
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (c + e < p.w) o[e] = x[k].e[e];
-    } else {
-      *reinterpret_cast<uint4*>(const_cast<E*>(static_cast<const E*>(p.wide)) + (size_t)(r0 + k * per) * p.wp + c) = x[k].v;
-    }
-  }
+  const E* odd = static_cast<const E*>(p.odd) + (b * p.sb + n * p.sn + h * p.sh);
+  uint4* wide = reinterpret_cast<uint4*>(const_cast<E*>(static_cast<const E*>(p.wide)) + (size_t)r * p.wp + c);
+  if (BACK) scatter<E, V>(const_cast<E*>(odd), c, p.w, *wide);
+  else *wide = gather<E, V>(odd, c, p.w);
 }
 
 template <bool BACK>
