@@ -43,6 +43,7 @@ struct Lay {
   static constexpr int NS = DP == 128 && MODE == kFwd ? 2 : 4;   // stages of the stream
   static constexpr int tail = NA * A + NS * 2 * B;
   static constexpr int bars = tail, info = tail + 128;   // info: per stage 64 x {lse, delta, position} or two words of column bits
+  static_assert((2 * NS + 7) * 8 + 8 <= info - bars, "barriers, tensor-memory address, abort flag");
   static constexpr int smem = info + NS * (MODE == kKeySide ? 768 : 8) + 1024;
   // Tensor memory.  Forward: S of even and odd tiles, P in place of S.  Row side: S,
   // dP, dS and what its rounding left.  Key side: S and dP, P and dS in their places.
@@ -142,9 +143,13 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
   uint64_t* empty = full + NS;
-  uint64_t* s_full = empty + NS;             // two: even and odd tiles, as the products run up to a tile ahead of the rows
+  // Two of each: even and odd tiles.  The products run up to a tile ahead of the
+  // rows, so in the forward a warp may finish tile t + 1 while another is still at
+  // t: on one barrier its arrivals would stand for the other's, and P(t) V would read
+  // scores that are not yet probabilities.
+  uint64_t* s_full = empty + NS;
   uint64_t* p_full = s_full + 2;
-  uint64_t* pv_done = p_full + 1;            // two, likewise
+  uint64_t* pv_done = p_full + 2;
   uint64_t* drained = pv_done + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(drained + 1);
   int* abort_flag = reinterpret_cast<int*>(slot + 1);
@@ -191,9 +196,9 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], kFinish);
       mbar_init(&pv_done[s], 1);
     }
-    mbar_init(p_full, kFinish);
     mbar_init(drained, 1);
     fence_mbar_init();
     *abort_flag = 0;
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
         // has been used), when this tile's were read (row side), or when this tile's
         // P and dS have been used (key side)
         if (MODE == kFwd && t + 1 < ntile) go = done(t - 1) && scores(t + 1);
-        if (!go || !mbar_wait(p_full, t & 1, wc, 84)) break;
+        if (!go || !mbar_wait(&p_full[t & 1], (t >> 1) & 1, wc, 84)) break;
         tc_fence_after();
         if (MODE == kRowSide && t + 1 < ntile) {
           go = scores(t + 1);
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(p_full);
+      mbar_arrive(&p_full[t & 1]);
     }
     bool done = ntile > 0 && mbar_wait(&pv_done[(ntile - 1) & 1], ((ntile - 1) >> 1) & 1, wc, 87);
     done = __all_sync(0xffffffffu, done);
