@@ -233,9 +233,17 @@ __device__ __forceinline__ float2 moments(float2 (&z)[H], int n, const NormArgs&
 }
 
 // 1 / (1 + 2^(-x log2 e)); the rounding of x log2 e, which 2^() would pass on
-// multiplied by ln 2, is put back.
-__device__ __forceinline__ float2 sigmoid(float2 x) {
+// multiplied by ln 2, is put back.  Beyond +-88, where that rounding would meet a
+// power that is infinite, the result is 0 or 1 in float32 all the same; a NaN stays one.
+__device__ __forceinline__ float within88(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-88.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(88.f));
+  return y;
+}
+__device__ __forceinline__ float2 sigmoid(float2 g) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+  const float2 x = make_float2(within88(g.x), within88(g.y));
   const float2 y = mul2(x, both(-kLog2e)), r = fma2(x, both(-kLog2e), make_float2(-y.x, -y.y));
   float2 p;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(y.x));

@@ -158,6 +158,41 @@ def test_padding_is_never_used():
     assert torch.equal(g["s"][~m], d_r[~m])
 
 
+GATES = [float("-inf"), -3e38, -1e30, -1e4, *(x / 2 for x in range(-260, 261)), 1e4, 1e30, 3e38, float("inf"), -0.0]
+
+
+@pytest.mark.parametrize("ts,tb", TYPES)
+@pytest.mark.parametrize("C", [256, 101])
+def test_gates_of_any_size(ts, tb, C):
+    """Closed and open gates: infinities, the largest finite values, every half from -130 to 130, the type's ends; as many rows as it takes."""
+    t = TD[tb]
+    v = torch.tensor([*GATES, torch.finfo(t).min, torch.finfo(t).max], device="cuda").to(t)
+    rows = 2 * len(v) // C + 7
+    a = make(rows, C, ts, tb, seed=30)
+    a["gate"] = v.repeat(rows * C // len(v) + 1)[:rows * C].view(rows, C)
+    for norm in ("layer", "rms"):
+        got, g = check(**a, norm=norm)
+        assert all(torch.isfinite(x).all() for x in (*got.values(), *g.values()))
+    shut = torch.full_like(a["gate"], float("-inf"))                   # a row of closed gates: nothing of the branch is left
+    a["gate"] = shut
+    got, g = check(**a)
+    assert torch.equal(got["r"], a["s"]) and (g["u"] == 0).all() and (g["gate"] == 0).all()
+
+
+def test_a_gate_that_is_nan_spoils_its_row_only():
+    a = make(9, 96, "f32", "bf16")
+    clean, gc = check(**a)
+    a["gate"][4, 7] = float("nan")
+    import protein_structure_models_b200 as fw
+    d_r, d_x = a.pop("d_r"), a.pop("d_x")
+    got = fw.norm_residual(**a, want_stats=True)
+    assert got["r"][4, 7].isnan() and got["x"][4].isnan().all()
+    g = fw.norm_residual_backward(a.pop("s"), a.pop("u"), got["stats"], d_r, d_x, **a)
+    other = torch.arange(9, device="cuda") != 4
+    assert g["s"][4].isnan().all() and g["gate"][4, 7].isnan()
+    assert all(torch.equal(x[other], y[other]) for x, y in ((got["r"], clean["r"]), (got["x"], clean["x"]), (g["s"], gc["s"]), (g["u"], gc["u"]), (g["gate"], gc["gate"])))
+
+
 def test_large_mean_and_tiny_variance():
     """A mean a thousand times the deviation (absolute sums say what float32 can keep), a constant row, a zero row."""
     a = make(30, 200, "f32", "f32", smean=1000.0)
