@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_window import TD, U, handles, rnd, within  # noqa: F401
+from test_gpu_window import U, check, handles, rnd, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,126 @@ def test_many_ctas_whose_warps_drift_apart(handles, N, H, Hkv, D, left, right, s
         ek = torch.einsum("hr,hrd->hd", x["sc"] * (eds + n * 2.0 ** -23 * dS.abs()), x["Q"].abs())
         within(g["v"][0, j], fold(dv), u * fold(dv).abs() + fold(ev) + 1e-30, f"d_v of key {j}")
         within(g["k"][0, j], fold(dk), u * fold(dk).abs() + fold(ek) + 1e-30, f"d_k of key {j}")
+
+
+class Sampled:
+    """A handle whose calls run a whole batch; check() sees some of its samples."""
+
+    def __init__(self, h, q, k, v, d, sel, shift=0):
+        self.h, self.t, self.d, self.sel, self.shift = h, (q, k, v), d, sel, shift
+
+    def buffer(self, shape, dtype):
+        """Off 16-byte boundaries by `shift` elements, NaN all around."""
+        b = torch.full((math.prod(shape) + 2 * 64,), math.nan, dtype=dtype, device="cuda")
+        self.bufs.append(b)
+        return b[64 + self.shift:][:math.prod(shape)].view(shape)
+
+    def window_attention(self, q, k, v, window, want_lse, mask, q_start, **kw):
+        self.bufs = []
+        (B, Nq, H, _), Dv = self.t[0].shape, self.t[2].shape[3]
+        self.o = {"out": self.buffer((B, Nq, H, Dv), q.dtype), "lse": self.buffer((B, H, Nq), torch.float32)}
+        self.h.window_attention(*self.t, window, mask=self.mask, q_start=self.start, out=self.o, **kw)
+        again = self.h.window_attention(*self.t, window, mask=self.mask, q_start=self.start, want_lse=True, **kw)
+        if self.shift == 0:
+            assert all(torch.equal(again[x], self.o[x]) for x in self.o)
+        return {x: t[self.sel] for x, t in self.o.items()}
+
+    def window_attention_backward(self, q, k, v, out, lse, d, window, mask, q_start, **kw):
+        g = {n: self.buffer(t.shape, q.dtype) for n, t in zip("qkv", self.t)}
+        args = (*self.t, self.o["out"], self.o["lse"], self.d, window)
+        self.h.window_attention_backward(*args, mask=self.mask, q_start=self.start, grads=g, **kw)
+        again = self.h.window_attention_backward(*args, mask=self.mask, q_start=self.start, **kw)
+        if self.shift == 0:
+            assert all(torch.equal(again[x], g[x]) for x in g)
+        for b in self.bufs:
+            assert b[:64 + self.shift].isnan().all() and b[self.shift - 64:].isnan().all()
+        return {x: t[self.sel] for x, t in g.items()}
+
+    def sync_status(self):
+        self.h.sync_status()
+
+    mask = start = None
+
+
+# Calls that window_short.cu takes in both directions: 296 sequences or more (samples
+# times key heads) of at most 512 rows and keys that fit half an SM's shared memory.
+SHORT = [  # B, Nq, Nk, H, Hkv, D, Dv, left, right, sinks
+    (300, 1, 1, 1, 1, 16, 16, 0, 0, 0),
+    (40, 31, 31, 8, 8, 16, 16, 5, 0, 2),
+    (40, 33, 33, 24, 8, 32, 32, None, None, 0),
+    (37, 150, 150, 8, 8, 16, 16, 31, 31, 2),
+    (38, 150, 150, 24, 8, 16, 16, 20, 3, 40),
+    (40, 33, 33, 24, 8, 64, 64, 8, 8, 1),
+    (40, 90, 90, 16, 8, 21, 21, 64, 0, 33),
+    (75, 40, 200, 4, 4, 32, 24, 70, 9, 70),
+    (300, 2, 100, 2, 1, 64, 40, 50, 0, 5),
+    (296, 512, 512, 1, 1, 16, 8, 100, 0, 100),
+    (60, 300, 300, 5, 5, 8, 13, 3, 3, 128),
+]
+
+
+def batch(case, seed=0):
+    B, Nq, Nk, H, Hkv, D, Dv = case[:7]
+    t = torch.bfloat16
+    return rnd((B, Nq, H, D), t, seed), rnd((B, Nk, Hkv, D), t, seed + 1), rnd((B, Nk, Hkv, Dv), t, seed + 2), rnd((B, Nq, H, Dv), t, seed + 3)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("case", SHORT, ids=lambda c: "-".join(map(str, c)))
+def test_many_short_sequences(handles, case, masked):  # noqa: F811
+    """Whole and masked; a whole sample, the sinks, a tail and every other key masked, with NaN and infinities there."""
+    B, Nq, Nk, left, right, sinks = case[0], case[1], case[2], *case[7:]
+    q, k, v, d = batch(case)
+    sel = torch.tensor([0, 1, 2, 3, B // 2, B - 1][:6 if Nk < 400 else 3], device="cuda")
+    h = Sampled(handles["bf16"], q, k, v, d, sel)
+    if masked:
+        h.mask = torch.rand((B, Nk), generator=torch.Generator(device="cuda").manual_seed(8), device="cuda") < 0.6
+        h.mask[0, Nk // 3:] = False
+        h.mask[1] = False
+        h.mask[2, :sinks] = False
+        h.mask[3] = torch.arange(Nk, device="cuda") % 2 == 1
+        gone = ~h.mask
+        for t, rows, bad in ((q, gone[:, -Nq:], math.nan), (k, gone, math.inf), (v, gone, math.nan), (d, gone[:, -Nq:], -math.inf)):
+            t[rows] = bad
+    check(h, q[sel], k[sel], v[sel], left, right, sinks, mask=h.mask[sel] if masked else None, d_out=d[sel])
+
+
+@pytest.mark.parametrize("case", [(75, 40, 200, 4, 4, 32, 24, 70, 9, 70), (100, 60, 128, 6, 3, 16, 16, 20, 0, 3), (43, 9, 33, 7, 7, 64, 64, 4, 2, 0)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_short_sequences_at_positions_of_their_own(handles, case):  # noqa: F811
+    """Chunks of queries anywhere, partly and wholly outside the keys, the ends of int32 among them."""
+    B, Nq, Nk, left, right, sinks = case[0], case[1], case[2], *case[7:]
+    q, k, v, d = batch(case, 50)
+    start = torch.randint(-Nq, Nk, (B,), generator=torch.Generator().manual_seed(9)).int()
+    start[:9] = torch.tensor([0, Nk - Nq, Nk // 2, -1, Nk, -Nq, 1 - Nq, 2 ** 31 - 1, -2 ** 31])
+    sel = torch.arange(12, device="cuda")
+    h = Sampled(handles["bf16"], q, k, v, d, sel)
+    h.start = start.cuda()
+    check(h, q[sel], k[sel], v[sel], left, right, sinks, q_start=h.start[sel], d_out=d[sel])
+
+
+@pytest.mark.parametrize("case", [SHORT[3], SHORT[6], SHORT[7]], ids=lambda c: "-".join(map(str, c)))
+def test_short_sequences_into_buffers_off_16_bytes(handles, case):  # noqa: F811
+    q, k, v, d = batch(case, 60)
+    sel = torch.tensor([0, case[0] - 1], device="cuda")
+    check(Sampled(handles["bf16"], q, k, v, d, sel, shift=1), q[sel], k[sel], v[sel], *case[7:], d_out=d[sel])
+
+
+def test_short_sequences_in_a_graph(handles):  # noqa: F811
+    h, (q, k, v, d) = handles["bf16"], batch(SHORT[4], 70)
+    kw = dict(window=SHORT[4][7:9], sinks=SHORT[4][9])
+
+    def step():
+        o = h.window_attention(q, k, v, want_lse=True, **kw)
+        return [o["out"], o["lse"], *h.window_attention_backward(q, k, v, o["out"], o["lse"], d, **kw).values()]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step()
+    for seed in (80, 81):
+        for t in (q, k, v, d):
+            t.copy_(rnd(t.shape, t.dtype, seed))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(kept, step()))
