@@ -168,14 +168,22 @@ def load_library():
     lib.fipa_embedding_backward.restype = c_int
     lib.fipa_destroy.argtypes = [vp]
     lib.fipa_destroy.restype = c_int
-    global _native
-    try:
-        from . import _native
-    except ImportError as e:
-        raise RuntimeError(f"{e}; build it with `python -m protein_structure_models_b200.build`") from e
-    _native.bind({name: ctypes.cast(getattr(lib, name), vp).value for name in NATIVE_CALLS})
     _lib = lib
     return lib
+
+
+def load_native():
+    """Load the compiled calls of the sequence operators (raises if they have not been built)."""
+    global _native
+    if _native is None:
+        lib = load_library()
+        try:
+            from . import _native as calls
+        except ImportError as e:
+            raise RuntimeError(f"{e}; build it with `python -m protein_structure_models_b200.build`") from e
+        calls.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in NATIVE_CALLS})
+        _native = calls
+    return _native
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
@@ -436,9 +444,9 @@ class Fipa:
         if workspace is None and stream is not None:
             workspace = self._window_room("fipa_window_attention_workspace_size", q, k, v, window, sinks)
             _used_on(stream, workspace)
-        r = _native.window(self._address(), self._code, self.device, q, k, v, -1 if left is None else left,
-                           -1 if right is None else right, sinks, mask, q_start, scale, want_lse, o, lse, workspace,
-                           _stream_address(stream))
+        r = (_native or load_native()).window(
+            self._address(), self._code, self.device, q, k, v, -1 if left is None else left, -1 if right is None else right, sinks,
+            mask, q_start, scale, want_lse, o, lse, workspace, _stream_address(stream))
         if type(r) is int:
             self._check(r)
         if out is None:
@@ -462,9 +470,9 @@ class Fipa:
         if workspace is None and stream is not None:
             workspace = self._window_room("fipa_window_attention_backward_workspace_size", q, k, v, window, sinks)
             _used_on(stream, workspace)
-        r = _native.window_backward(self._address(), self._code, self.device, q, k, v, -1 if left is None else left,
-                                    -1 if right is None else right, sinks, mask, q_start, scale, out, lse, d_out, dq, dk, dv,
-                                    workspace, _stream_address(stream))
+        r = (_native or load_native()).window_backward(
+            self._address(), self._code, self.device, q, k, v, -1 if left is None else left, -1 if right is None else right, sinks,
+            mask, q_start, scale, out, lse, d_out, dq, dk, dv, workspace, _stream_address(stream))
         if type(r) is int:
             self._check(r)
         if grads is None:
@@ -627,15 +635,13 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
     parameters [C] float32, mask [...] bool/uint8 (0: padding, r = s and x = 0).
     Returns {"r" (with u), "x" (with pre)} and, with want_stats, "stats" [rows, 4] for the
     backward.  Without u, x = Norm(s, pre) in branch_dtype (default: that of s)."""
-    if _native is None:
-        load_library()
     a = _norm_arguments(s, u, gate, res_scale, post, pre, mask, norm, eps, branch_dtype)
     r = x = stats = None
     if out is not None:
         r, x, stats = out.get("r"), out.get("x"), out.get("stats")
         if (u is not None and r is None) or (pre is not None and x is None):
             raise ValueError("out: buffer r or x missing")
-    res = _native.norm(*a, want_stats, out is not None, r, x, stats, _stream_address(stream))
+    res = (_native or load_native()).norm(*a, want_stats, out is not None, r, x, stats, _stream_address(stream))
     if type(res) is int:
         _ok(res, "fipa_norm_residual")
     if out is None:
@@ -669,7 +675,7 @@ def norm_residual_backward(s: torch.Tensor, u: Optional[torch.Tensor], stats: to
         workspace = s.new_empty(n.value, dtype=torch.uint8)
         _used_on(stream, workspace)
     given = _NO_GRADS if grads is None else [grads.get(f) for f in NORM_GRADS]
-    res = _native.norm_backward(*a, stats, d_r, d_x, grads is not None, *given, workspace, _stream_address(stream))
+    res = (_native or load_native()).norm_backward(*a, stats, d_r, d_x, grads is not None, *given, workspace, _stream_address(stream))
     if type(res) is int:
         _ok(res, "fipa_norm_residual_backward")
     if grads is None:
@@ -685,9 +691,7 @@ def embedding(idx: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: O
               stream: Optional[torch.cuda.Stream] = None) -> dict:
     """fipa_embedding: {"out": scale * table[idx]} for idx [...] int32 and table [V, C]
     float32/bfloat16; an index outside [0, V) gives a zero row."""
-    if _native is None:
-        load_library()
-    r = _native.embedding(idx, table, scale, None if out is None else out["out"], _stream_address(stream))
+    r = (_native or load_native()).embedding(idx, table, scale, None if out is None else out["out"], _stream_address(stream))
     if type(r) is int:
         _ok(r, "fipa_embedding")
     if out is None:
@@ -708,13 +712,11 @@ def embedding_backward(idx: torch.Tensor, d_out: torch.Tensor, V: int, scale: fl
                        workspace: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
                        stream: Optional[torch.cuda.Stream] = None) -> dict:
     """fipa_embedding_backward: {"table": [V, C] float32}, the gradient of <d_out, out>."""
-    if _native is None:
-        load_library()
     if workspace is None and stream is not None:
         workspace = d_out.new_empty(embedding_backward_workspace_size(idx.numel(), V, d_out.shape[-1]), dtype=torch.uint8)
         _used_on(stream, workspace)
-    r = _native.embedding_backward(idx, d_out, V, scale, None if grads is None else grads["table"], workspace,
-                                   _stream_address(stream))
+    r = (_native or load_native()).embedding_backward(idx, d_out, V, scale, None if grads is None else grads["table"], workspace,
+                                                      _stream_address(stream))
     if type(r) is int:
         _ok(r, "fipa_embedding_backward")
     if grads is None:
