@@ -51,19 +51,36 @@ def _run(cmd) -> str:
     return res.stdout + res.stderr
 
 
+def built_for() -> str:
+    """What the Python calls are compiled against; the module carries it as its documentation."""
+    import sysconfig
+
+    import torch
+    return f"Calls of the sequence operators for {sysconfig.get_config_var('SOABI')}, PyTorch {torch.__version__}, " \
+        f"C++ ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}."
+
+
+def native_needs_build() -> bool:
+    """Older than its sources, or made for another Python or PyTorch, whose interfaces it would not fit (found without loading it)."""
+    if _stale(NATIVE, [NATIVE_SOURCE, os.path.join(INCLUDE, "fipa.h")]):
+        return True
+    with open(NATIVE, "rb") as f:
+        return built_for().encode() + b"\0" not in f.read()
+
+
 def build_native(force: bool = False) -> str:
     """Compile the Python calls against the headers of Python and PyTorch; returns the module's path."""
     import sysconfig
 
     import torch
-    if not force and not _stale(NATIVE, [NATIVE_SOURCE, os.path.join(INCLUDE, "fipa.h")]):
+    if not force and not native_needs_build():
         return NATIVE
     home = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     inc = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc], NATIVE_SOURCE,
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DFIPA_BUILT_FOR="{built_for()}"', *[f"-I{d}" for d in inc], NATIVE_SOURCE,
           "-o", NATIVE + ".tmp", "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(NATIVE + ".tmp", NATIVE)
     return NATIVE

@@ -407,7 +407,8 @@ PyObject* bind(PyObject*, PyObject* dict) {
 #define FIPA_FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FIPA_FAST(window), FIPA_FAST(window_backward), FIPA_FAST(norm), FIPA_FAST(norm_backward), FIPA_FAST(embedding),
                          FIPA_FAST(embedding_backward), {"bind", &bind, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// FIPA_BUILT_FOR: the Python and PyTorch that this was compiled against, for the build to find in the file.
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", FIPA_BUILT_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

@@ -56,3 +56,22 @@ def test_they_refuse_tensors_of_the_host():
         fw.embedding(torch.zeros(2, dtype=torch.int32), torch.zeros(2, 8))
     with pytest.raises(ValueError):
         fw.norm_residual(torch.zeros(2, 8), torch.zeros(2, 8))
+
+
+def test_they_are_built_again_for_another_python_or_pytorch(monkeypatch):
+    import sysconfig
+
+    import torch
+
+    from protein_structure_models_b200 import build, fipa
+    assert not build.native_needs_build() and fipa.load_native().__doc__ == build.built_for()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", torch.__version__ + "1")
+        assert build.native_needs_build()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-313-x86_64-linux-gnu")
+        assert build.native_needs_build()
+    with monkeypatch.context() as m:
+        m.setattr(build, "NATIVE", build.NATIVE + ".none")
+        assert build.native_needs_build()
+    assert not build.native_needs_build()
