@@ -439,8 +439,8 @@ class Fipa:
         o = lse = None
         if out is not None:
             o, lse = out.get("out"), out.get("lse")
-            if o is None:
-                raise ValueError("out: buffer missing")
+            if o is None or (want_lse and lse is None):
+                raise ValueError("out: buffer out or lse missing")
         if workspace is None and stream is not None:
             workspace = self._window_room("fipa_window_attention_workspace_size", q, k, v, window, sinks)
             _used_on(stream, workspace)
@@ -639,8 +639,8 @@ def norm_residual(s: torch.Tensor, u: Optional[torch.Tensor] = None, gate: Optio
     r = x = stats = None
     if out is not None:
         r, x, stats = out.get("r"), out.get("x"), out.get("stats")
-        if (u is not None and r is None) or (pre is not None and x is None):
-            raise ValueError("out: buffer r or x missing")
+        if (u is not None and r is None) or (pre is not None and x is None) or (want_stats and stats is None):
+            raise ValueError("out: buffer r, x or stats missing")
     res = (_native or load_native()).norm(*a, want_stats, out is not None, r, x, stats, _stream_address(stream))
     if type(res) is int:
         _ok(res, "fipa_norm_residual")

@@ -75,3 +75,17 @@ def test_they_are_built_again_for_another_python_or_pytorch(monkeypatch):
         m.setattr(build, "NATIVE", build.NATIVE + ".none")
         assert build.native_needs_build()
     assert not build.native_needs_build()
+
+
+def test_what_is_asked_for_needs_a_buffer():
+    """want_lse and want_stats beside `out` without such a buffer are refused, not dropped."""
+    import torch
+
+    import protein_structure_models_b200 as fw
+    t, x = torch.zeros(1, 4, 2, 8), torch.zeros(2, 8)
+    h = object.__new__(fw.Fipa)
+    for out in ({"out": t}, {"lse": t}):
+        with pytest.raises(ValueError, match="buffer out or lse missing"):
+            h.window_attention(t, t, t, (1, 1), want_lse=True, out=out)
+    with pytest.raises(ValueError, match="buffer r, x or stats missing"):
+        fw.norm_residual(x, x, out={"r": x}, want_stats=True)
