@@ -434,7 +434,7 @@ typedef struct {
   int C;                        /* channels, 1..8192                           */
   fipa_dtype stream_dtype, branch_dtype;
   fipa_norm_kind norm;
-  double eps;                   /* > 0                                         */
+  double eps;                   /* > 0, as float32 too                         */
 } fipa_norm_dims;
 typedef struct {
   const void *s, *u, *gate;     /* [rows, C]; u, gate optional                 */

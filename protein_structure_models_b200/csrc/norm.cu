@@ -577,7 +577,7 @@ fipa_status norm_args(const fipa_norm_dims* d, const fipa_norm_inputs* in, NormA
   if (d->rows < 0 || d->C <= 0) return FIPA_ERR_INVALID_ARG;
   if ((d->stream_dtype != FIPA_F32 && d->stream_dtype != FIPA_BF16) ||
       (d->branch_dtype != FIPA_F32 && d->branch_dtype != FIPA_BF16) ||
-      (d->norm != FIPA_NORM_LAYER && d->norm != FIPA_NORM_RMS) || !(d->eps > 0.0) || !isfinite((float)d->eps))
+      (d->norm != FIPA_NORM_LAYER && d->norm != FIPA_NORM_RMS) || !((float)d->eps > 0.f) || !isfinite((float)d->eps))
     return FIPA_ERR_INVALID_ARG;
   if (d->C > kNormMaxC) return FIPA_ERR_UNSUPPORTED;
   const bool u = in->u != nullptr || d->rows == 0;           // an empty tensor may have no address

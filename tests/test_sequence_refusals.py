@@ -80,3 +80,9 @@ def test_window_attention_without_a_handle(lib):
     assert lib.fipa_window_attention_backward(None, t, t, t, None, None, w, P, P, P, P, P, P, P, 1 << 20, None) == 1
     assert lib.fipa_window_attention_workspace_size(None, t, t, t, w, ctypes.byref(n)) == 1
     assert lib.fipa_window_attention_backward_workspace_size(None, t, t, t, w, ctypes.byref(n)) == 1
+
+
+@pytest.mark.parametrize("eps", [1e-46, 1e-300, -1e-5, float("nan"), 1e39])
+def test_norm_residual_eps_that_float32_does_not_hold(lib, eps):
+    """An eps that float32 rounds to 0 would make a constant row 0 / 0."""
+    assert lib.fipa_norm_residual(dims(eps=eps), inputs(), P, None, None, None) == 1
