@@ -367,7 +367,7 @@ typedef struct {
   int D, Dv;          /* query / key and value channels, 1..128 each                    */
   int left, right;    /* window before and after the query's own position; < 0: no bound */
   int sinks;          /* first tokens that stay visible, 0..128                         */
-  double scale;       /* finite, > 0                                                    */
+  double scale;       /* > 0, as float32 too; scale log2 e finite                       */
 } fipa_window;
 
 /* [B, N, heads, width] with strides in elements (>= 0), the width contiguous:

@@ -797,8 +797,9 @@ fipa_status window_args(fipa_handle* h, const fipa_window* w, fipa::WinArgs* a) 
     return fail(h, FIPA_ERR_INVALID_ARG, "every size must be > 0");
   if (w->H % w->Hkv != 0) return fail(h, FIPA_ERR_INVALID_ARG, "H must be a multiple of Hkv");
   if (w->sinks < 0) return fail(h, FIPA_ERR_INVALID_ARG, "sinks must be >= 0");
-  if (!(w->scale > 0.0) || !std::isfinite((float)w->scale) || !((float)w->scale > 0.f))
-    return fail(h, FIPA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  // exponents are powers of two: scale log2 e has to be a float32 too
+  if (!((float)w->scale > 0.f) || !std::isfinite((float)w->scale * 1.4426950408889634f))
+    return fail(h, FIPA_ERR_INVALID_ARG, "scale must be > 0 and finite, times log2 e too");
   if (w->D > fipa::kWinMaxD || w->Dv > fipa::kWinMaxD) return fail(h, FIPA_ERR_UNSUPPORTED, "D and Dv must be <= 128");
   if (w->sinks > fipa::kWinMaxSinks) return fail(h, FIPA_ERR_UNSUPPORTED, "sinks must be <= 128");
   const int64_t lim = 0x3fffffff;

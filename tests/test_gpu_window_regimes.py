@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_window import U, check, handles, rnd, within  # noqa: F401
+from test_gpu_window import TD, U, check, handles, rnd, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -203,3 +203,18 @@ def test_short_sequences_in_a_graph(handles):  # noqa: F811
             t.copy_(rnd(t.shape, t.dtype, seed))
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(kept, step()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales_at_the_ends_of_float32(handles, dtype):  # noqa: F811
+    """A scale whose product with log2 e is not finite is refused (0 queries would give NaN); the largest that is not, with 0 queries, gives means."""
+    from protein_structure_models_b200 import FipaError
+    h = handles[dtype]
+    q, k, v = (rnd((1, 40, 2, 16), TD[dtype], i) for i in range(3))
+    q.zero_()
+    for scale in (3e38, 2.4e38, math.nan, 1e-46, 0.0):
+        with pytest.raises(FipaError) as e:
+            h.window_attention(q, k, v, (5, 5), scale=scale)
+        assert e.value.status == 1
+    for scale in (2.3e38, 1e-30):
+        check(h, q, k, v, 5, 5, 1, scale=scale, backward=False)
