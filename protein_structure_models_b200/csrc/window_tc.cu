@@ -338,10 +338,6 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
         tc_commit(&pv_done[t & 1]);
         if (MODE == kKeySide && t + 1 < ntile) go = done(t) && scores(t + 1);
       }
-      if (*abort_flag) {                                    // what is in flight ends before the memory is given back
-        tc_commit(drained);
-        drain(drained, 0, a.timeout_ns);
-      }
     }
   } else {
     // ------------------------------------------------------------- rows
@@ -565,6 +561,11 @@ __global__ void __launch_bounds__(kThreads, (Lay<MODE, DP>::per_sm)) win_tc_kern
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {
+    // whichever warp's wait ran out: what is in flight ends before the memory is given back
+    if (lane == 0 && *abort_flag) {
+      tc_commit(drained);
+      drain(drained, 0, a.timeout_ns);
+    }
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, L::cols);
