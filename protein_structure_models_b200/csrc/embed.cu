@@ -20,7 +20,7 @@ namespace fipa {
 namespace {
 
 constexpr int kSortThreads = 256;
-constexpr int kSortItems = 2;                              // per thread (8: 83 us for 65536 tokens of 32000 x 512 instead of 78)
+constexpr int kSortItems = 2;                              // per thread (8: 83 us for 65536 tokens of 32000 x 512 with the forward, instead of 77)
 constexpr int kSortBlock = kSortThreads * kSortItems;
 constexpr int kSmallItems = 8;                             // likewise where one CTA sorts the whole list
 constexpr int kSmallBlock = kSortThreads * kSmallItems;
@@ -700,8 +700,12 @@ FIPA_API fipa_status fipa_embedding_backward(fipa_dtype dtype, const int32_t* id
   const long long fill = ((long long)V + 511) / 512;
   const unsigned gx = (unsigned)(ncross + (fill < 148 * 4 ? fill : 148 * 4));
   const float* part = reinterpret_cast<const float*>(ws + p.off_part);
-  // long runs want more CTAs, narrow ones: 59574 tokens of 2 x 256 with the forward 41 us
-  // against 57, 327680 of 64 x 128 69 against 63
+  // Long runs want more CTAs, narrow ones; us of the gradient of T tokens of V x C in
+  // bfloat16, cold, wide against narrow slabs:
+  //   59574 of 2 x 256  59 / 45    160000 of 8 x 128   55 / 49    327680 of 64 x 128  53 / 61
+  //   40000 of 1 x 512  74 / 55    100000 of 8 x 256   49 / 51    262144 of 32 x 64   45 / 43
+  //   65536 of 4 x 256  45 / 41    200000 of 16 x 128  51 / 53    10000 of 1 x 512    35 / 29
+  // From 5000 to 16384 tokens a row it is also a matter of how many rows and columns there are.
   if (C % 4 == 0 && is_aligned(d_table, 16) && n / V < 16384)
     embed_join_kernel<4><<<dim3(gx, (unsigned)((C + 127) / 128)), 512, 0, s>>>(key, n, V, C, p.L, p.nchunk, ncross, (float)scale, part, d_table);
   else

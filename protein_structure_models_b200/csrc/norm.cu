@@ -555,8 +555,13 @@ cudaError_t norm_launch(const NormArgs& a, bool bwd, int grid, cudaStream_t st) 
   else norm_fwd_kernel<TS, TB, VEC, BLOCK, TPR><<<grid, BLOCK, smem, st>>>(a);
   return cudaGetLastError();
 }
-// Threads a row known at compile time where a row is a warp's (C up to 256) or the
-// CTA's (C beyond 1024): columns become constant offsets, sums unroll.
+// Threads a row known at compile time where a row is a warp's (C of 129 to 256) or the
+// CTA's (C beyond 1024): columns become constant offsets, sums unroll.  Forward / backward
+// in us of a float32 stream with a bfloat16 branch, compiled in against passed, cold:
+//   100000 x 200: 70 / 129 against 78 / 141
+// The other widths are passed.  Up to 128 channels little is lost (156250 x 128: 66 / 109
+// against 64 / 117), beyond 256 more (52083 x 384: 86 / 150 against 117 / 170,
+// 19531 x 1024: 72 / 135 against 94 / 150); not built.
 template <typename TS, typename TB, bool VEC>
 cudaError_t norm_launch(const NormArgs& a, bool bwd, int grid, cudaStream_t st) {
   switch (a.tpr) {

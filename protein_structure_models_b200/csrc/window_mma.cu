@@ -689,7 +689,7 @@ bool vectors(const WinArgs& a, bool backward) {
 //   512 x 40 x 8 of 128: 113 / 341 against 120 / 503
 bool use_tc(const WinArgs& a, bool backward) {
   const long long w = a.D > a.Dv ? a.D : a.Dv, all = (long long)a.left + a.right + 1, win = all < a.Nk ? all : a.Nk;
-  if ((long long)a.B * a.Nq * a.H < 512) return false;     // see win_is_fine
+  if ((long long)a.B * a.Nq * a.H < 512) return false;     // four row tiles at most: the warp-level kernels, with win_is_fine's second products
   return win * w * w >= 200000 && (long long)a.Nq * a.G >= 64 && a.Nk >= 64 && vectors(a, backward);
 }
 }  // namespace

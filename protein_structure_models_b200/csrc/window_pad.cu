@@ -6,8 +6,8 @@
 // The copies are O(N) beside kernels that read each key once a row tile, so they
 // cost little; loads of single elements in the kernels' tiles took 2.5 to 3.5
 // times as long as 16-byte ones (699 residues, 12 heads on 4 of 82: training step
-// 458 us, this way 152, at 88 channels 132).  The copies go by words (15 x 1321
-// residues, 4 heads of 106: training step 293 us, by elements 365).  Few rows against a long cache
+// 458 us, this way 141, at 88 channels 128).  The copies go by words (15 x 1321
+// residues, 4 heads of 106: training step 288 us, by elements 365).  Few rows against a long cache
 // read the cache as it is (window_step.cu), and of the keys of a forward call
 // only those that some row sees are copied.
 #include "kernels.h"

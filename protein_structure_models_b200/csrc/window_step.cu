@@ -14,7 +14,7 @@
 // channels of keys 2c, 2c + 1, 2c + 8, 2c + 9, a byte permutation pairs them,
 // and column g of the product's j-th tile is channel DP / 8 g + j.  (A ring of
 // tiles in shared memory took three times the instructions a tile and 25 us at
-// 64 x 1028 keys of 4 x 64 channels, this way 21.7, 2.7 TB/s of what is seen.)
+// 64 x 1028 keys of 4 x 64 channels, this way 21.6, 2.7 TB/s of what is seen.)
 //
 // The partial results meet in shared memory, across the cluster by distributed
 // shared memory, and are joined in a fixed order as sum_w exp(m_w - m) O_w: one

@@ -20,7 +20,7 @@
 // the waits between products and softmax.  Two CTAs an SM (one in the backward
 // beyond 64 channels) and four stages of tiles (two in the forward beyond 64) keep
 // both sides busy; 16384 residues, 8 heads on 2 of 64, 511 keys before: training step
-// 282 us.  Warps 0-3 finish rows, warp 4 issues the matrix instructions, warps 5-6
+// 283 us.  Warps 0-3 finish rows, warp 4 issues the matrix instructions, warps 5-6
 // copy tiles (16-byte asynchronous copies into the 128-byte swizzle, zeros for masked
 // and missing rows, which a tensor map could not leave out).  Every wait is bounded.
 #include <math.h>
